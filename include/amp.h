@@ -1,13 +1,16 @@
 /*
  * amp.h -- C ABI of the MI355X (gfx950) mixed-precision training hot path.
  *
- * Three parts, as the pages describe mixed-precision training:
+ * As the pages describe mixed-precision training:
  *   1. scaled down-casts to FP16 / BF16 / FP8 (E4M3 forward, E5M2 backward)
  *      with amax capture, delayed and current scaling, plus the NVFP4,
  *      MX and fine-grained (tile / block) FP8 quantizers;
  *   2. low-precision GEMM with FP32 accumulation (forward, dgrad, wgrad);
  *   3. the fused FP32-master AdamW step with dynamic loss scaling, with
- *      gradient accumulation and global-norm clipping.
+ *      gradient accumulation and global-norm clipping;
+ *   4. what lies between the GEMMs of a transformer block in fine-grained FP8:
+ *      RMS norm and gated activation with FP8 outputs and FP8 activation
+ *      checkpoints, and their backward passes.
  *
  * Conventions for every call
  * --------------------------
@@ -395,6 +398,118 @@ int amp_gemm_blockwise(int64_t M, int64_t N, int64_t K,
                        const void* A, int at, int64_t lda, const float* sA, int64_t ldsA,
                        int a_block, const void* B, int bt, int64_t ldb, const float* sB,
                        int64_t ldsB, int b_block, void* C, int ct, int64_t ldc, void* stream);
+
+/* ---- Norm and gated activation between fine-grained FP8 GEMMs -------------
+ * The element-wise part of a transformer block whose GEMMs are
+ * amp_gemm_blockwise: each call reads its input once and writes every form of
+ * its result that a GEMM, the residual stream or the backward pass reads.
+ * FP8 checkpoints are what the backward pass reads in place of 16-bit
+ * activations.  Sums and statistics are FP32; each output is rounded once.
+ * One token is rows == 1. */
+
+/* A matrix in FP8 with one FP32 scale_inv per 1x128 tile along its contiguous
+ * dimension, as amp_quantize_blockwise writes it with block == 0 and
+ * amp_gemm_blockwise reads it: codes q [R, K], row stride ldq >= K; scale_inv
+ * at s[(k/128)*lds + r], lds >= R.  Tiles are scaled as there, scale =
+ * fp8_max / amax(tile), with one difference: where the quotient overflows (an
+ * amax below fp8_max / FLT_MAX) the scale is 1, as for an amax of 0.
+ * Passed by pointer (read during the call only); NULL where optional. */
+typedef struct {
+  uint8_t* q;
+  float* s;
+  int64_t ldq, lds;
+  int32_t type; /* AMP_E4M3 or AMP_E5M2 */
+  int32_t pad_;
+} amp_fp8_tiles;
+
+/* amp_rmsnorm -- residual addition, RMS norm and FP8 / 16-bit outputs.
+ *   h = round_xt(x + res) (res NULL: x);  r = 1 / sqrt(mean_c(h^2) + eps);
+ *   y = (h * r) * gamma
+ * x, res: [rows, cols] of xt in {F32, F16, BF16}, strides ldx, ldr >= cols.
+ * gamma: [cols] of gt in {F32, F16, BF16}; NULL means 1.  eps >= 0 and finite
+ *    (with eps == 0 an all-zero row has r = inf and y = NaN).
+ * Outputs, at least one (each may be NULL):
+ *   h: [rows, cols] of xt, stride ldh; may be x or res themselves, with the
+ *      same stride.  y is formed from the rounded h.
+ *   y: [rows, cols] of yt in {F16, BF16, E4M3, E5M2}, stride ldy, rounded as by
+ *      amp_cast from fl32(y * *d_scale) (d_scale NULL: 1).
+ *   yq: y in 1x128 tiles.       ckpt: h in 1x128 tiles.
+ *   d_amax: device FP32, accumulated with max |y| (unscaled; as amp_cast).
+ *   rstd: [rows] FP32, r.
+ * Squares are summed in FP32: a row whose sum overflows has r = 0.  Apart
+ * from h no output may overlap an input.  rows or cols == 0 is a no-op. */
+int amp_rmsnorm(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx,
+                const void* res, int64_t ldr, const void* gamma, int gt, float eps,
+                void* h, int64_t ldh, void* y, int yt, int64_t ldy, const float* d_scale,
+                float* d_amax, const amp_fp8_tiles* yq, const amp_fp8_tiles* ckpt, float* rstd,
+                void* stream);
+
+/* amp_rmsnorm_backward -- gradients of amp_rmsnorm.
+ *   n = h * r;  g = dy * gamma;  dx = r * (g - n * mean_c(g * n)) + dres;
+ *   dgamma = sum_rows(dy * n)
+ * dy: [rows, cols] of dt in {F32, F16, BF16}, stride lddy.
+ * h: the normalised input [rows, cols] of dt, stride ldh; or ckpt: its FP8
+ *    checkpoint (exactly one of the two).
+ * gamma as in the forward call; rstd: [rows], its output.
+ * dres: [rows, cols] of dt, stride lddr: the gradient that reaches h past the
+ *    norm (the residual branch); NULL for none.
+ * dx: [rows, cols] of dt, stride lddx, the gradient of h and so of x and of
+ *    res; may be dy or dres themselves, with the same stride; NULL for none.
+ * dgamma: [cols] FP32, overwritten (zeros for rows == 0); NULL for none.
+ * d_work: FP32 [min(rows, AMP_RMSNORM_PARTIALS), cols], the partial sums of
+ *    dgamma (needed with dgamma); calls that may overlap need one each.  The
+ *    sums are added in a fixed order: the result is reproducible.
+ * cols == 0 is a no-op. */
+#define AMP_RMSNORM_PARTIALS 512
+int amp_rmsnorm_backward(const void* dy, int dt, int64_t rows, int64_t cols, int64_t lddy,
+                         const void* h, int64_t ldh, const amp_fp8_tiles* ckpt,
+                         const void* gamma, int gt, const float* rstd, const void* dres,
+                         int64_t lddr, void* dx, int64_t lddx, float* dgamma, float* d_work,
+                         void* stream);
+
+/* amp_swiglu -- gated activation y = g * sigmoid(g) * u of x = [g | u].
+ * x: [rows, 2*cols] of xt in {F32, F16, BF16} (g the first cols columns, u the
+ *    others), stride ldx >= 2*cols.
+ * Outputs, at least one of y, yq, ckpt:
+ *   y, d_scale, d_amax, yq: as amp_rmsnorm, [rows, cols];
+ *   ckpt: x in FP8, q [rows, 2*cols], the tiles starting again at u: tile kb of
+ *      half i is at s[(i*ceil(cols/128) + kb)*lds + r] (for cols % 128 == 0
+ *      the layout of any [rows, 2*cols] matrix in tiles).
+ * No output may overlap x.  rows or cols == 0 is a no-op. */
+int amp_swiglu(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx, void* y, int yt,
+               int64_t ldy, const float* d_scale, float* d_amax, const amp_fp8_tiles* yq,
+               const amp_fp8_tiles* ckpt, void* stream);
+
+/* amp_swiglu_backward -- gradient of amp_swiglu and the recomputed activation.
+ *   s = sigmoid(g);  dg = dy * u * s * (1 + g * (1 - s));  du = dy * g * s
+ * dy: [rows, cols] of dt in {F32, F16, BF16}, stride lddy.
+ * x: [rows, 2*cols] of dt, stride ldx; or ckpt: its checkpoint as amp_swiglu
+ *    writes it (exactly one of the two).
+ * Outputs, at least one:
+ *   dx: [dg | du], [rows, 2*cols] of dt, stride lddx; may be x itself, with
+ *      the same stride;
+ *   dxq: the same in 1x128 tiles, the dgrad operand (cols % 128 == 0, else
+ *      AMP_EUNSUPPORTED: a tile would straddle the halves);
+ *   dxqt: dx^T [2*cols, rows] in 1x128 tiles (along the rows of x), the wgrad
+ *      operand of the product before the activation;
+ *   yqt: y^T [cols, rows] in 1x128 tiles, y recomputed: the wgrad operand of
+ *      the product after it.
+ * rows or cols == 0 is a no-op. */
+int amp_swiglu_backward(const void* dy, int dt, int64_t rows, int64_t cols, int64_t lddy,
+                        const void* x, int64_t ldx, const amp_fp8_tiles* ckpt, void* dx,
+                        int64_t lddx, const amp_fp8_tiles* dxq, const amp_fp8_tiles* dxqt,
+                        const amp_fp8_tiles* yqt, void* stream);
+
+/* amp_requantize_blockwise -- the transposed operand of a matrix kept in FP8:
+ *   v[r][c] = (code * scale_inv) * d_row[r] * col[c];  qt = v^T in 1x128 tiles
+ * x: [rows, cols] in tiles; qt: [cols, rows] (tiles along the rows of x).
+ * d_row: [rows] FP32, col: [cols] of ct in {F32, F16, BF16}; NULL means 1.
+ * With d_row = rstd and col = gamma, v is the output of amp_rmsnorm
+ * recomputed from the checkpoint of its input.  rows or cols == 0 is a
+ * no-op. */
+int amp_requantize_blockwise(const amp_fp8_tiles* x, int64_t rows, int64_t cols,
+                             const float* d_row, const void* col, int ct,
+                             const amp_fp8_tiles* qt, void* stream);
 
 /* ---- FP16 AMP training step of a two-layer MLP: the element-wise glue ----
  * Page "혼합 정밀도 학습" (itwiki), section "FP16 학습 루프": Linear(512, 2048)

@@ -28,7 +28,8 @@ __all__ = [
     "amp_cast_current_scaling", "amp_mx_quantize", "GEMM_MX",
     "amp_quantize_blockwise", "amp_gemm_blockwise", "amp_cast_ex",
     "amp_found_inf_from_amax", "amp_stream_copy", "amp_grad_norm_accumulate_noalloc",
-    "amp_fp8_mfma_probe",
+    "amp_fp8_mfma_probe", "Fp8Tiles", "RMSNORM_PARTIALS", "amp_rmsnorm", "amp_rmsnorm_backward",
+    "amp_swiglu", "amp_swiglu_backward", "amp_requantize_blockwise",
 ]
 
 F32, F16, BF16, E4M3, E5M2, E2M1X2 = 0, 1, 2, 3, 4, 5
@@ -40,6 +41,7 @@ AMAX_MAX, AMAX_MOST_RECENT = 0, 1
 OPT_SKIP_CHECK = 1
 GEMM_FP8_NATIVE = 1
 GEMM_MX = 2
+RMSNORM_PARTIALS = 512                     # rows of amp_rmsnorm_backward's work area
 
 # Device-resident state layouts (mirror the C structs; for reading back).
 SCALER_STATE_DTYPE = np.dtype([("scale", "<f4"), ("growth_tracker", "<i4"),
@@ -80,6 +82,20 @@ class BlockScales(ctypes.Structure):
                 ("block2d", ctypes.c_int32), ("pad_", ctypes.c_int32)]
 
 
+class Fp8Tiles(ctypes.Structure):
+    """A matrix in FP8 with one FP32 scale_inv per 1x128 tile (``amp_fp8_tiles``).
+
+    ``q``: codes [R, K], row stride ``ldq``; ``s``: scale_inv of tile kb of row
+    r at ``s[kb * lds + r]``.  Tensors given for them are kept alive and, in
+    every call, checked against what the call spans."""
+    _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("ldq", ctypes.c_int64),
+                ("lds", ctypes.c_int64), ("type", ctypes.c_int32), ("pad_", ctypes.c_int32)]
+
+    def __init__(self, q, s, ldq, lds, dtype=3):
+        super().__init__(_ptr(q), _ptr(s), ldq, lds, dtype, 0)
+        self.tensors = (q, s)
+
+
 _P, _I, _I64, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64
 _SIGS = {
     "amp_abi_version": ([], _I),
@@ -115,6 +131,14 @@ _SIGS = {
     "amp_delayed_scaling_update": ([_P, _P, ctypes.c_int32, _P, _P], _I),
     "amp_nvfp4_quantize": ([_P, _I, _I64, _I64, _I64, _I, _I, _I, _U64, _I, _U64, _P, _P, _P,
                             _P], _I),
+    "amp_rmsnorm": ([_P, _I, _I64, _I64, _I64, _P, _I64, _P, _I, ctypes.c_float, _P, _I64, _P, _I,
+                     _I64, _P, _P, _P, _P, _P, _P], _I),
+    "amp_rmsnorm_backward": ([_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P, _I, _P, _P, _I64, _P,
+                              _I64, _P, _P, _P], _I),
+    "amp_swiglu": ([_P, _I, _I64, _I64, _I64, _P, _I, _I64, _P, _P, _P, _P, _P], _I),
+    "amp_swiglu_backward": ([_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _P, _P, _P],
+                            _I),
+    "amp_requantize_blockwise": ([_P, _I64, _I64, _P, _P, _I, _P, _P], _I),
     "amp_bias_gelu_f16": ([_P, _I64, _I64, _P, _P, _P, _P], _I),
     "amp_softmax_xent_f16": ([_P, _P, _I64, _I64, _P, _P, _P, _P], _I),
     "amp_gelu_backward_f16": ([_P, _P, _I64, _P, _P], _I),
@@ -319,6 +343,86 @@ def amp_gemm_blockwise(M, N, K, A, at, lda, sA, ldsA, a_block, B, bt, ldb, sB, l
     _check("amp_gemm_blockwise", load().amp_gemm_blockwise(
         M, N, K, _ptr(A), at, lda, _ptr(sA), ldsA, int(a_block), _ptr(B), bt, ldb, _ptr(sB),
         ldsB, int(b_block), _ptr(C), ct, ldc, _stream(stream)))
+
+
+def _room_tiles(fn: str, what: str, t, rows, cols, nb=None) -> None:
+    """The same for an FP8 matrix [rows, cols] (``nb``: its tiles along K)."""
+    if t is None or rows <= 0 or cols <= 0:
+        return
+    q, s = t.tensors
+    _room(fn, what + ".q", q, (rows - 1) * t.ldq + cols)
+    _room(fn, what + ".s", s, 4 * ((nb if nb else -(-cols // 128)) - 1) * t.lds + 4 * rows)
+
+
+def amp_rmsnorm(x, xt, rows, cols, ldx, res, ldr, gamma, gt, eps, h=None, ldh=0, y=None, yt=BF16,
+                ldy=0, d_scale=None, d_amax=None, yq=None, ckpt=None, rstd=None, stream=None):
+    f = "amp_rmsnorm"
+    _room(f, "x", x, _mat(rows, cols, ldx, xt))
+    _room(f, "res", res, _mat(rows, cols, ldr, xt))
+    _room(f, "gamma", gamma, _vec(cols, gt))
+    _room(f, "h", h, _mat(rows, cols, ldh, xt))
+    _room(f, "y", y, _mat(rows, cols, ldy, yt))
+    _room(f, "rstd", rstd, _vec(rows, F32))
+    _room_tiles(f, "yq", yq, rows, cols)
+    _room_tiles(f, "ckpt", ckpt, rows, cols)
+    _check(f, load().amp_rmsnorm(
+        _ptr(x), xt, rows, cols, ldx, _ptr(res), ldr, _ptr(gamma), gt, eps, _ptr(h), ldh, _ptr(y),
+        yt, ldy, _ptr(d_scale), _ptr(d_amax), _ptr(yq), _ptr(ckpt), _ptr(rstd), _stream(stream)))
+
+
+def amp_rmsnorm_backward(dy, dt, rows, cols, lddy, h, ldh, ckpt, gamma, gt, rstd, dres=None, lddr=0,
+                         dx=None, lddx=0, dgamma=None, d_work=None, stream=None):
+    f = "amp_rmsnorm_backward"
+    _room(f, "dy", dy, _mat(rows, cols, lddy, dt))
+    _room(f, "h", h, _mat(rows, cols, ldh, dt))
+    _room_tiles(f, "ckpt", ckpt, rows, cols)
+    _room(f, "gamma", gamma, _vec(cols, gt))
+    _room(f, "rstd", rstd, _vec(rows, F32))
+    _room(f, "dres", dres, _mat(rows, cols, lddr, dt))
+    _room(f, "dx", dx, _mat(rows, cols, lddx, dt))
+    if dgamma is not None:
+        _room(f, "dgamma", dgamma, _vec(cols, F32))
+        _room(f, "d_work", d_work, _vec(min(rows, RMSNORM_PARTIALS) * cols, F32))
+    _check(f, load().amp_rmsnorm_backward(
+        _ptr(dy), dt, rows, cols, lddy, _ptr(h), ldh, _ptr(ckpt), _ptr(gamma), gt, _ptr(rstd),
+        _ptr(dres), lddr, _ptr(dx), lddx, _ptr(dgamma), _ptr(d_work), _stream(stream)))
+
+
+def amp_swiglu(x, xt, rows, cols, ldx, y=None, yt=BF16, ldy=0, d_scale=None, d_amax=None, yq=None,
+               ckpt=None, stream=None):
+    f = "amp_swiglu"
+    _room(f, "x", x, _mat(rows, 2 * cols, ldx, xt))
+    _room(f, "y", y, _mat(rows, cols, ldy, yt))
+    _room_tiles(f, "yq", yq, rows, cols)
+    _room_tiles(f, "ckpt", ckpt, rows, 2 * cols, 2 * -(-cols // 128))
+    _check(f, load().amp_swiglu(
+        _ptr(x), xt, rows, cols, ldx, _ptr(y), yt, ldy, _ptr(d_scale), _ptr(d_amax), _ptr(yq),
+        _ptr(ckpt), _stream(stream)))
+
+
+def amp_swiglu_backward(dy, dt, rows, cols, lddy, x, ldx, ckpt, dx=None, lddx=0, dxq=None,
+                        dxqt=None, yqt=None, stream=None):
+    f = "amp_swiglu_backward"
+    _room(f, "dy", dy, _mat(rows, cols, lddy, dt))
+    _room(f, "x", x, _mat(rows, 2 * cols, ldx, dt))
+    _room_tiles(f, "ckpt", ckpt, rows, 2 * cols, 2 * -(-cols // 128))
+    _room(f, "dx", dx, _mat(rows, 2 * cols, lddx, dt))
+    _room_tiles(f, "dxq", dxq, rows, 2 * cols)
+    _room_tiles(f, "dxqt", dxqt, 2 * cols, rows)
+    _room_tiles(f, "yqt", yqt, cols, rows)
+    _check(f, load().amp_swiglu_backward(
+        _ptr(dy), dt, rows, cols, lddy, _ptr(x), ldx, _ptr(ckpt), _ptr(dx), lddx, _ptr(dxq),
+        _ptr(dxqt), _ptr(yqt), _stream(stream)))
+
+
+def amp_requantize_blockwise(x, rows, cols, d_row, col, ct, qt, stream=None):
+    f = "amp_requantize_blockwise"
+    _room_tiles(f, "x", x, rows, cols)
+    _room(f, "d_row", d_row, _vec(rows, F32))
+    _room(f, "col", col, _vec(cols, ct))
+    _room_tiles(f, "qt", qt, cols, rows)
+    _check(f, load().amp_requantize_blockwise(_ptr(x), rows, cols, _ptr(d_row), _ptr(col), ct,
+                                              _ptr(qt), _stream(stream)))
 
 
 def amp_mx_quantize(x, xt, rows, cols, ldx, transpose, yt, q, scales, stream=None):

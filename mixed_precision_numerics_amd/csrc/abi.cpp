@@ -59,6 +59,16 @@ bool is_fp8(int t) { return t == AMP_E4M3 || t == AMP_E5M2; }
 // error, not a memory fault.  NULL passes (optional arguments).
 bool al(const void* p, uintptr_t a) { return p == nullptr || amp::aligned(p, a); }
 
+// An FP8 matrix [rows, cols] in 1x128 tiles (NULL: absent, valid).
+int tiles_status(const amp_fp8_tiles* t, int64_t rows, int64_t cols) {
+  if (!t) return AMP_OK;
+  if (!is_fp8(t->type)) return AMP_EUNSUPPORTED;
+  if (!t->q || !t->s || !al(t->s, 4) || t->ldq < cols || t->lds < rows) return AMP_EINVAL;
+  return AMP_OK;
+}
+
+amp_fp8_tiles or_none(const amp_fp8_tiles* t) { return t ? *t : amp_fp8_tiles{}; }
+
 }  // namespace
 
 extern "C" {
@@ -392,6 +402,95 @@ int amp_nvfp4_quantize(const void* x, int xt, int64_t rows, int64_t cols, int64_
   return hip_status(amp::launch_nvfp4_quantize(x, xt, rows, cols, ldx, transpose, block2d, rht,
                                                rht_seed, rnd, sr_seed, q, scales, d_tensor,
                                                static_cast<hipStream_t>(stream)));
+}
+
+int amp_rmsnorm(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx, const void* res,
+                int64_t ldr, const void* gamma, int gt, float eps, void* h, int64_t ldh, void* y,
+                int yt, int64_t ldy, const float* d_scale, float* d_amax, const amp_fp8_tiles* yq,
+                const amp_fp8_tiles* ckpt, float* rstd, void* stream) {
+  if (!al(d_scale, 4) || !al(d_amax, 4) || !al(rstd, 4)) return AMP_EINVAL;
+  if (rows < 0 || cols < 0 || !(eps >= 0.0f && eps < 3.0e38f)) return AMP_EINVAL;
+  if (!is_cast_in(xt) || (gamma && !is_cast_in(gt)) || (y && !is_cast_out(yt))) return AMP_EUNSUPPORTED;
+  if (rows == 0 || cols == 0) return AMP_OK;
+  if (!x || (!h && !y && !yq && !ckpt && !d_amax && !rstd)) return AMP_EINVAL;
+  if (ldx < cols || (res && ldr < cols) || (h && ldh < cols) || (y && ldy < cols)) return AMP_EINVAL;
+  if (int e = tiles_status(yq, rows, cols)) return e;
+  if (int e = tiles_status(ckpt, rows, cols)) return e;
+  if ((h == x && ldh != ldx) || (h && h == res && ldh != ldr)) return AMP_EINVAL;
+  if (int e = check_device()) return e;
+  return hip_status(amp::launch_rmsnorm(x, xt, rows, cols, ldx, res, ldr, gamma, gt, eps, h, ldh, y, yt, ldy,
+                                        d_scale, d_amax, or_none(yq), or_none(ckpt), rstd,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+int amp_rmsnorm_backward(const void* dy, int dt, int64_t rows, int64_t cols, int64_t lddy, const void* h,
+                         int64_t ldh, const amp_fp8_tiles* ckpt, const void* gamma, int gt,
+                         const float* rstd, const void* dres, int64_t lddr, void* dx, int64_t lddx,
+                         float* dgamma, float* d_work, void* stream) {
+  if (!al(rstd, 4) || !al(dgamma, 4) || !al(d_work, 4)) return AMP_EINVAL;
+  if (rows < 0 || cols < 0) return AMP_EINVAL;
+  if (!is_cast_in(dt) || (gamma && !is_cast_in(gt))) return AMP_EUNSUPPORTED;
+  if (cols == 0 || (rows == 0 && !dgamma)) return AMP_OK;
+  if (rows > 0) {
+    if (!dy || !rstd || (!dx && !dgamma) || (dgamma && !d_work)) return AMP_EINVAL;
+    if ((h != nullptr) == (ckpt != nullptr)) return AMP_EINVAL;
+    if (lddy < cols || (h && ldh < cols) || (dres && lddr < cols) || (dx && lddx < cols)) return AMP_EINVAL;
+    if (int e = tiles_status(ckpt, rows, cols)) return e;
+    if ((dx == dy && lddx != lddy) || (dx && dx == dres && lddx != lddr)) return AMP_EINVAL;
+  }
+  if (int e = check_device()) return e;
+  return hip_status(amp::launch_rmsnorm_backward(dy, dt, rows, cols, lddy, h, ldh, or_none(ckpt), gamma, gt, rstd,
+                                                 dres, lddr, dx, lddx, dgamma, d_work,
+                                                 static_cast<hipStream_t>(stream)));
+}
+
+int amp_swiglu(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx, void* y, int yt, int64_t ldy,
+               const float* d_scale, float* d_amax, const amp_fp8_tiles* yq, const amp_fp8_tiles* ckpt,
+               void* stream) {
+  if (!al(d_scale, 4) || !al(d_amax, 4)) return AMP_EINVAL;
+  if (rows < 0 || cols < 0) return AMP_EINVAL;
+  if (!is_cast_in(xt) || (y && !is_cast_out(yt))) return AMP_EUNSUPPORTED;
+  if (rows == 0 || cols == 0) return AMP_OK;
+  if (!x || (!y && !yq && !ckpt && !d_amax)) return AMP_EINVAL;
+  if (ldx < 2 * cols || (y && ldy < cols)) return AMP_EINVAL;
+  if (int e = tiles_status(yq, rows, cols)) return e;
+  if (int e = tiles_status(ckpt, rows, 2 * cols)) return e;
+  if (int e = check_device()) return e;
+  return hip_status(amp::launch_swiglu(x, xt, rows, cols, ldx, y, yt, ldy, d_scale, d_amax, or_none(yq),
+                                       or_none(ckpt), static_cast<hipStream_t>(stream)));
+}
+
+int amp_swiglu_backward(const void* dy, int dt, int64_t rows, int64_t cols, int64_t lddy, const void* x,
+                        int64_t ldx, const amp_fp8_tiles* ckpt, void* dx, int64_t lddx,
+                        const amp_fp8_tiles* dxq, const amp_fp8_tiles* dxqt, const amp_fp8_tiles* yqt,
+                        void* stream) {
+  if (rows < 0 || cols < 0) return AMP_EINVAL;
+  if (!is_cast_in(dt) || (dxq && cols % 128 != 0)) return AMP_EUNSUPPORTED;
+  if (rows == 0 || cols == 0) return AMP_OK;
+  if (!dy || (x != nullptr) == (ckpt != nullptr) || (!dx && !dxq && !dxqt && !yqt)) return AMP_EINVAL;
+  if (lddy < cols || (x && ldx < 2 * cols) || (dx && lddx < 2 * cols)) return AMP_EINVAL;
+  if (int e = tiles_status(ckpt, rows, 2 * cols)) return e;
+  if (int e = tiles_status(dxq, rows, 2 * cols)) return e;
+  if (int e = tiles_status(dxqt, 2 * cols, rows)) return e;
+  if (int e = tiles_status(yqt, cols, rows)) return e;
+  if (dx && dx == x && lddx != ldx) return AMP_EINVAL;
+  if (int e = check_device()) return e;
+  return hip_status(amp::launch_swiglu_backward(dy, dt, rows, cols, lddy, x, ldx, or_none(ckpt), dx, lddx,
+                                                or_none(dxq), or_none(dxqt), or_none(yqt),
+                                                static_cast<hipStream_t>(stream)));
+}
+
+int amp_requantize_blockwise(const amp_fp8_tiles* x, int64_t rows, int64_t cols, const float* d_row,
+                             const void* col, int ct, const amp_fp8_tiles* qt, void* stream) {
+  if (!al(d_row, 4)) return AMP_EINVAL;
+  if (rows < 0 || cols < 0) return AMP_EINVAL;
+  if (col && !is_cast_in(ct)) return AMP_EUNSUPPORTED;
+  if (rows == 0 || cols == 0) return AMP_OK;
+  if (!x || !qt) return AMP_EINVAL;
+  if (int e = tiles_status(x, rows, cols)) return e;
+  if (int e = tiles_status(qt, cols, rows)) return e;
+  if (int e = check_device()) return e;
+  return hip_status(amp::launch_requantize(*x, rows, cols, d_row, col, ct, *qt, static_cast<hipStream_t>(stream)));
 }
 
 int amp_bias_gelu_f16(const float* acc, int64_t rows, int64_t cols, const void* b16, void* z16,

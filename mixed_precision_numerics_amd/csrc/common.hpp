@@ -124,6 +124,26 @@ hipError_t launch_nvfp4_quantize(const void* x, int xt, int64_t rows, int64_t co
 
 hipError_t launch_mx_quantize(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx,
                               int transpose, int yt, uint8_t* q, uint8_t* scales, hipStream_t s);
+hipError_t launch_rmsnorm(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx,
+                          const void* res, int64_t ldr, const void* gamma, int gt, float eps,
+                          void* h, int64_t ldh, void* y, int yt, int64_t ldy, const float* scale,
+                          float* amax, const amp_fp8_tiles& yq, const amp_fp8_tiles& ckpt,
+                          float* rstd, hipStream_t s);
+hipError_t launch_rmsnorm_backward(const void* dy, int dt, int64_t rows, int64_t cols,
+                                   int64_t lddy, const void* h, int64_t ldh,
+                                   const amp_fp8_tiles& ckpt, const void* gamma, int gt,
+                                   const float* rstd, const void* dres, int64_t lddr, void* dx,
+                                   int64_t lddx, float* dgamma, float* work, hipStream_t s);
+hipError_t launch_swiglu(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx, void* y,
+                         int yt, int64_t ldy, const float* scale, float* amax,
+                         const amp_fp8_tiles& yq, const amp_fp8_tiles& ckpt, hipStream_t s);
+hipError_t launch_swiglu_backward(const void* dy, int dt, int64_t rows, int64_t cols,
+                                  int64_t lddy, const void* x, int64_t ldx,
+                                  const amp_fp8_tiles& ckpt, void* dx, int64_t lddx,
+                                  const amp_fp8_tiles& dxq, const amp_fp8_tiles& dxqt,
+                                  const amp_fp8_tiles& yqt, hipStream_t s);
+hipError_t launch_requantize(const amp_fp8_tiles& x, int64_t rows, int64_t cols, const float* row,
+                             const void* col, int ct, const amp_fp8_tiles& qt, hipStream_t s);
 hipError_t launch_bias_gelu(const float* acc, int64_t rows, int64_t cols, const void* b16,
                             void* z16, void* a16, hipStream_t s);
 hipError_t launch_softmax_xent(const void* logits16, const int32_t* labels, int64_t rows,

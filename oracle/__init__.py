@@ -35,6 +35,7 @@ mlp       the tiny FP16 AMP training step (512->2048->GELU->10)
 clip      FP32 gradient accumulation, global norm, clip coefficient
 mx        MX block formats (UE8M0 scale per 32 elements)
 blockwise fine-grained FP8 scaling (1x128 tiles, 128x128 blocks) and GEMM
+block     RMS norm, gated activation, their gradients, and 1x128 requantization
 
 Functions whose correctness cannot be pinned against anything outside the
 oracle say "parity unpinned" in their docstring.

@@ -1,0 +1,125 @@
+"""Refusals of the norm, gated-activation and requantization entry points: all
+come before any device work, so they need no GPU."""
+import os
+
+import pytest
+import torch
+
+import mixed_precision_numerics_amd as amp
+
+pytestmark = pytest.mark.skipif(not os.path.exists(amp.lib_path()), reason="libamp.so not built")
+EINVAL, EUNSUP = -1, -2
+P = 4096            # a pointer that no refused call follows
+
+
+def tiles(ldq, lds, t=amp.E4M3, q=P, s=P):
+    return amp.Fp8Tiles(q, s, ldq, lds, t)
+
+
+def status(fn, *a):
+    args = [amp.ctypes.addressof(x) if isinstance(x, amp.Fp8Tiles) else x for x in a]
+    return getattr(amp.load(), fn)(*args)
+
+
+def norm(**k):
+    a = dict(x=P, xt=amp.BF16, rows=4, cols=300, ldx=300, res=None, ldr=0, gamma=P, gt=amp.F32, eps=1e-5, h=None, ldh=0, y=P,
+             yt=amp.BF16, ldy=300, d_scale=None, d_amax=None, yq=None, ckpt=None, rstd=None)
+    a.update(k)
+    return status("amp_rmsnorm", *a.values(), None)
+
+
+def norm_back(**k):
+    a = dict(dy=P, dt=amp.BF16, rows=4, cols=300, lddy=300, h=P, ldh=300, ckpt=None, gamma=P, gt=amp.F32, rstd=P, dres=None, lddr=0,
+             dx=2 * P, lddx=300, dgamma=P, d_work=P)
+    a.update(k)
+    return status("amp_rmsnorm_backward", *a.values(), None)
+
+
+def gate(**k):
+    a = dict(x=P, xt=amp.BF16, rows=4, cols=300, ldx=600, y=P, yt=amp.BF16, ldy=300, d_scale=None, d_amax=None, yq=None, ckpt=None)
+    a.update(k)
+    return status("amp_swiglu", *a.values(), None)
+
+
+def gate_back(**k):
+    a = dict(dy=P, dt=amp.BF16, rows=4, cols=300, lddy=300, x=P, ldx=600, ckpt=None, dx=2 * P, lddx=600, dxq=None, dxqt=None, yqt=None)
+    a.update(k)
+    return status("amp_swiglu_backward", *a.values(), None)
+
+
+def requant(**k):
+    a = dict(x=tiles(300, 4), rows=4, cols=300, d_row=None, col=None, ct=0, qt=tiles(4, 300))
+    a.update(k)
+    return status("amp_requantize_blockwise", *a.values(), None)
+
+
+
+@pytest.mark.parametrize("call,bad", [
+    (norm, dict(rows=-1)), (norm, dict(cols=-1)), (norm, dict(eps=-1e-5)), (norm, dict(eps=float("nan"))),
+    (norm, dict(eps=float("inf"))), (norm, dict(x=None)), (norm, dict(y=None)), (norm, dict(ldx=299)),
+    (norm, dict(res=P, ldr=299)), (norm, dict(h=2 * P, ldh=299)), (norm, dict(ldy=299)), (norm, dict(rstd=P + 2)),
+    (norm, dict(d_amax=P + 1)), (norm, dict(d_scale=P + 2)), (norm, dict(yq=tiles(299, 4))), (norm, dict(yq=tiles(300, 3))),
+    (norm, dict(ckpt=tiles(300, 4, q=None))), (norm, dict(ckpt=tiles(300, 4, s=None))), (norm, dict(ckpt=tiles(300, 4, s=P + 2))),
+    (norm, dict(h=P, ldh=304)), (norm, dict(res=2 * P, ldr=300, h=2 * P, ldh=301)),
+    (norm_back, dict(rows=-1)), (norm_back, dict(dy=None)), (norm_back, dict(rstd=None)), (norm_back, dict(h=None)),
+    (norm_back, dict(ckpt=tiles(300, 4))), (norm_back, dict(h=None, ckpt=tiles(300, 3))), (norm_back, dict(d_work=None)),
+    (norm_back, dict(dx=None, dgamma=None)), (norm_back, dict(lddy=299)), (norm_back, dict(ldh=299)), (norm_back, dict(lddx=299)),
+    (norm_back, dict(dres=P, lddr=299)), (norm_back, dict(dgamma=P + 2)), (norm_back, dict(dx=P, lddx=301)),
+    (norm_back, dict(dres=2 * P, lddr=301)),
+    (gate, dict(rows=-1)), (gate, dict(cols=-2)), (gate, dict(x=None)), (gate, dict(y=None)), (gate, dict(ldx=599)),
+    (gate, dict(ldy=299)), (gate, dict(yq=tiles(300, 3))), (gate, dict(ckpt=tiles(599, 4))), (gate, dict(d_scale=P + 1)),
+    (gate_back, dict(rows=-1)), (gate_back, dict(dy=None)), (gate_back, dict(x=None)), (gate_back, dict(ckpt=tiles(600, 4))),
+    (gate_back, dict(dx=None)), (gate_back, dict(lddy=299)), (gate_back, dict(ldx=599)), (gate_back, dict(lddx=599)),
+    (gate_back, dict(dxqt=tiles(4, 599))), (gate_back, dict(dxqt=tiles(3, 600))), (gate_back, dict(yqt=tiles(4, 299))),
+    (gate_back, dict(dx=P, lddx=601)),
+    (requant, dict(rows=-1)), (requant, dict(x=None)), (requant, dict(qt=None)), (requant, dict(x=tiles(299, 4))),
+    (requant, dict(x=tiles(300, 3))), (requant, dict(qt=tiles(3, 300))), (requant, dict(qt=tiles(4, 299))),
+    (requant, dict(d_row=P + 2)),
+])
+def test_invalid_arguments(call, bad):
+    assert call(**bad) == EINVAL
+
+
+@pytest.mark.parametrize("call,bad", [
+    (norm, dict(xt=amp.E4M3)), (norm, dict(gt=amp.E5M2)), (norm, dict(yt=amp.F32)), (norm, dict(yq=tiles(300, 4, amp.BF16))),
+    (norm_back, dict(dt=amp.E4M3)), (norm_back, dict(gt=9)), (norm_back, dict(h=None, ckpt=tiles(300, 4, amp.E2M1X2))),
+    (gate, dict(xt=7)), (gate, dict(yt=amp.E2M1X2)), (gate, dict(ckpt=tiles(600, 4, amp.F16))),
+    (gate_back, dict(dt=amp.E5M2)), (gate_back, dict(dxq=tiles(600, 4))),    # 300 columns: a tile across the halves
+    (requant, dict(col=P, ct=amp.E4M3)), (requant, dict(qt=tiles(4, 300, amp.F32))),
+])
+def test_unsupported_types_and_layouts(call, bad):
+    assert call(**bad) == EUNSUP
+
+
+def test_empty_work_is_accepted_without_pointers():
+    assert norm(rows=0, x=None, y=None) == 0 and norm(cols=0, ldx=0) == 0
+    assert gate(rows=0, x=None) == 0 and gate_back(cols=0, dy=None) == 0 and requant(rows=0, x=None) == 0
+    assert norm_back(rows=0, dgamma=None) == 0 and norm_back(cols=0) == 0
+
+
+def test_binding_refuses_tensors_smaller_than_the_call_spans():
+    bf, u8 = torch.bfloat16, torch.uint8
+    x, g = torch.zeros(4, 300, dtype=bf), torch.zeros(300)
+    ok = amp.Fp8Tiles(torch.zeros(4, 300, dtype=u8), torch.zeros(3, 4), 300, 4)
+    short_q = amp.Fp8Tiles(torch.zeros(1199, dtype=u8), torch.zeros(3, 4), 300, 4)
+    short_s = amp.Fp8Tiles(torch.zeros(1200, dtype=u8), torch.zeros(11), 300, 4)
+
+    def refused(what, fn, *a, **k):
+        with pytest.raises(ValueError, match=what + " holds"):
+            fn(*a, **k)
+    refused("x", amp.amp_rmsnorm, x, amp.BF16, 4, 301, 301, None, 0, None, 0, 1e-5, yq=ok)
+    refused("res", amp.amp_rmsnorm, x, amp.BF16, 4, 300, 300, x[1:], 300, None, 0, 1e-5, yq=ok)
+    refused("gamma", amp.amp_rmsnorm, x, amp.BF16, 4, 300, 300, None, 0, g[1:], amp.F32, 1e-5, yq=ok)
+    refused("yq.q", amp.amp_rmsnorm, x, amp.BF16, 4, 300, 300, None, 0, g, amp.F32, 1e-5, yq=short_q)
+    refused("ckpt.s", amp.amp_rmsnorm, x, amp.BF16, 4, 300, 300, None, 0, g, amp.F32, 1e-5, ckpt=short_s)
+    refused("rstd", amp.amp_rmsnorm, x, amp.BF16, 4, 300, 300, None, 0, g, amp.F32, 1e-5, rstd=torch.zeros(3))
+    refused("d_work", amp.amp_rmsnorm_backward, x, amp.BF16, 4, 300, 300, x, 300, None, g, amp.F32, torch.zeros(4), None, 0, None, 0,
+            g, torch.zeros(1199))
+    refused("x", amp.amp_swiglu, x, amp.BF16, 4, 151, 302, yq=ok)
+    refused("ckpt.s", amp.amp_swiglu, x, amp.BF16, 4, 150, 300, ckpt=ok)      # 2 halves of 2 tiles
+    refused("dxqt.q", amp.amp_swiglu_backward, x, amp.BF16, 4, 150, 300, x, 300, None, dxqt=amp.Fp8Tiles(
+        torch.zeros(1199, dtype=u8), torch.zeros(300), 4, 300))
+    refused("d_row", amp.amp_requantize_blockwise, ok, 4, 300, torch.zeros(3), None, 0, amp.Fp8Tiles(
+        torch.zeros(300, 4, dtype=u8), torch.zeros(300), 4, 300))
+    refused("qt.s", amp.amp_requantize_blockwise, ok, 4, 300, None, None, 0, amp.Fp8Tiles(
+        torch.zeros(300, 4, dtype=u8), torch.zeros(299), 4, 300))

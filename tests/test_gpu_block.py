@@ -1,0 +1,603 @@
+"""RMS norm, gated activation, their backward passes and the transposed
+requantization on the GPU, against oracle/block.py in float64: every output
+lies in the interval that the FP32 operations' roundings allow (block_util)."""
+import numpy as np
+import pytest
+import torch
+
+import mixed_precision_numerics_amd as amp
+from oracle import block as B
+from oracle import formats as F
+import synth
+from block_util import (U, check_scaled, check_tiles, check_values, dx_err, norm_err, swiglu_back_err,
+                        swiglu_err)
+from gpu_util import dev, empty, host
+
+pytestmark = pytest.mark.gpu
+
+FMT = {amp.F32: F.F32, amp.F16: F.F16, amp.BF16: F.BF16, amp.E4M3: F.E4M3, amp.E5M2: F.E5M2}
+NPT = {amp.F32: np.uint32, amp.F16: np.uint16, amp.BF16: np.uint16, amp.E4M3: np.uint8, amp.E5M2: np.uint8}
+EPS = 1e-5
+TYPES = [amp.BF16, amp.F16, amp.F32]
+
+
+def rand(seed, *shape, scale=1.0):
+    return synth.rng(seed).standard_normal(shape) * scale
+
+
+def stored(v, t):
+    """(codes, values) of v rounded to type t."""
+    c = F.encode(np.clip(v, -6e4, 6e4) if t == amp.F16 else F.f32(v), FMT[t])
+    return c, F.decode(c, FMT[t])
+
+
+class Mat:
+    """A device matrix of type t, rows padded by `pad` elements and guard bytes behind the last."""
+
+    def __init__(self, rows, cols, t, pad=0, v=None):
+        self.rows, self.cols, self.t, self.ld = rows, cols, t, cols + pad
+        self.fill = 0xA5
+        n = rows * self.ld + 16
+        a = np.full(n * NPT[t]().itemsize, self.fill, np.uint8).view(NPT[t])
+        if v is not None:
+            codes, self.v = stored(v, t)
+            a[:rows * self.ld].reshape(rows, self.ld)[:, :cols] = codes
+        self.d = dev(a)
+
+    def codes(self):
+        a = host(self.d, NPT[self.t])
+        m = a[:self.rows * self.ld].reshape(self.rows, self.ld)
+        guard = np.concatenate([m[:, self.cols:].ravel(), a[self.rows * self.ld:]])
+        assert np.all(guard.view(np.uint8) == self.fill), "written outside the matrix"
+        return m[:, :self.cols]
+
+    def values(self):
+        return F.decode(self.codes(), FMT[self.t])
+
+
+class Tiles:
+    """A device FP8 matrix in 1x128 tiles, padded and guarded; `parts` halves restart their tiles."""
+
+    def __init__(self, rows, cols, t=amp.E4M3, pad=0, parts=1, v=None):
+        self.parts, self.t = parts, t
+        nb = parts * -(-(cols // parts) // 128)
+        self.q = Mat(rows, cols, t, pad)
+        self.s = Mat(nb, rows, amp.F32, pad)
+        if v is not None:
+            p = [B.quantize(x, FMT[t]) for x in np.split(v, parts, axis=1)]
+            q, s = np.concatenate([a for a, _ in p], 1), np.concatenate([b for _, b in p], 0)
+            self.q = Mat(rows, cols, t, pad, F.decode(q, FMT[t]))
+            self.s = Mat(nb, rows, amp.F32, pad, s)
+            self.v = B.dequantize(q, s, FMT[t], parts)
+        self.arg = amp.Fp8Tiles(self.q.d, self.s.d, self.q.ld, self.s.ld, t)
+
+    def check(self, v, err, what):
+        err = np.broadcast_to(err, v.shape)
+        q, s = self.q.codes(), self.s.values()
+        w = q.shape[1] // self.parts
+        nb = s.shape[0] // self.parts
+        for i in range(self.parts):
+            k = slice(i * w, (i + 1) * w)
+            check_tiles(q[:, k], s[i * nb:(i + 1) * nb], FMT[self.t], v[:, k], err[:, k], what)
+
+
+def loud(seed, rows, cols):
+    """Rows of normal values with a loud row, a quiet column and a zero tile."""
+    v = rand(seed, rows, cols)
+    v[rows // 2] *= 1e3
+    v[:, cols // 3] *= 1e-4
+    v[0, :128] = 0.0
+    return v
+
+
+# ---------------------------------------------------------------- forward ---
+
+# one element; part of a vector; one past a tile; several vectors a lane; a row
+# in 256 and in 1024 threads' registers; odd; more rows than a block holds
+NORM_SHAPES = [(1, 1), (3, 5), (2, 129), (9, 512), (5, 1000), (33, 2047), (3, 4096), (2, 7001), (2, 20483)]
+
+
+@pytest.mark.parametrize("xt", TYPES)
+@pytest.mark.parametrize("rows,cols", NORM_SHAPES)
+def test_norm_every_output(xt, rows, cols):
+    pad = 3 if rows % 2 else 8
+    x, res = Mat(rows, cols, xt, pad, loud(rows + cols, rows, cols)), Mat(rows, cols, xt, pad + 5, loud(cols, rows, cols))
+    gamma = Mat(1, cols, xt, 0, 1 + rand(7, 1, cols, scale=0.1))
+    half = amp.F16 if xt == amp.F16 else amp.BF16
+    h, y, rstd = Mat(rows, cols, xt, pad), Mat(rows, cols, half, pad + 1), Mat(1, rows, amp.F32)
+    yq, ck = Tiles(rows, cols, amp.E4M3, pad), Tiles(rows, cols, amp.E5M2, pad + 2)
+    am = torch.zeros(1, device="cuda")
+    amp.amp_rmsnorm(x.d, xt, rows, cols, x.ld, res.d, res.ld, gamma.d, xt, EPS, h.d, h.ld, y.d, half, y.ld, None, am,
+                    yq.arg, ck.arg, rstd.d)
+    wh = B.residual_add(x.v, res.v, FMT[xt])
+    wy, wr = B.rmsnorm(wh, gamma.v[0], EPS)
+    e = norm_err(cols)
+    assert np.array_equal(h.values(), wh)
+    check_values(rstd.values()[0], F.F32, wr, e * wr, "rstd")
+    ey = np.abs(wy) * (e + 3 * U)
+    check_values(y.values(), FMT[half], wy, ey, "y")
+    check_values(am.cpu().numpy(), F.F32, np.abs(wy).max(keepdims=True)[0], ey.max(), "amax")
+    yq.check(wy, ey, "yq")
+    ck.check(wh, 0.0, "checkpoint")
+
+
+@pytest.mark.parametrize("xt,cols", [(amp.BF16, 70003), (amp.F32, 33001), (amp.F16, 66000)])
+def test_norm_of_rows_longer_than_the_registers_hold(xt, cols):
+    test_norm_every_output(xt, 3, cols)
+
+
+@pytest.mark.parametrize("cols", [640, 70003])
+@pytest.mark.parametrize("which", ["x", "res"])
+def test_norm_in_place(cols, which):
+    rows, xt = 4, amp.BF16
+    x, res = Mat(rows, cols, xt, 3, rand(1, rows, cols)), Mat(rows, cols, xt, 6, rand(2, rows, cols))
+    into = x if which == "x" else res
+    yq = Tiles(rows, cols)
+    amp.amp_rmsnorm(x.d, xt, rows, cols, x.ld, res.d, res.ld, None, xt, EPS, into.d, into.ld, yq=yq.arg)
+    wh = B.residual_add(x.v, res.v, FMT[xt])
+    wy, _ = B.rmsnorm(wh, np.ones(cols), EPS)
+    assert np.array_equal(into.values(), wh)
+    yq.check(wy, np.abs(wy) * (norm_err(cols) + 3 * U), "yq")
+
+
+@pytest.mark.parametrize("yt", [amp.E4M3, amp.E5M2, amp.F16, amp.BF16])
+@pytest.mark.parametrize("op", ["norm", "swiglu"])
+def test_delayed_scaling_saturates_and_accumulates_amax(op, yt):
+    rows, cols, xt = 37, 1300, amp.F32
+    sc = np.float32(300.0 if yt in (amp.E4M3, amp.F16) else 40000.0)
+    x = Mat(rows, cols * (2 if op == "swiglu" else 1), xt, 1, loud(3, rows, cols * (2 if op == "swiglu" else 1)))
+    y = Mat(rows, cols, yt, 2)
+    am = torch.full((1,), 1e-3, device="cuda")
+    if op == "norm":
+        amp.amp_rmsnorm(x.d, xt, rows, cols, x.ld, None, 0, None, xt, EPS, None, 0, y.d, yt, y.ld, dev(sc.reshape(1)), am)
+        wy, _ = B.rmsnorm(x.v, np.ones(cols), EPS)
+        err = np.abs(wy) * (norm_err(cols) + 3 * U)
+    else:
+        amp.amp_swiglu(x.d, xt, rows, cols, x.ld, y.d, yt, y.ld, dev(sc.reshape(1)), am)
+        g, u = x.v[:, :cols], x.v[:, cols:]
+        wy, err = B.swiglu(g, u), swiglu_err(g, u)
+    top = np.abs(wy).max()
+    if yt in (amp.E4M3, amp.E5M2):
+        assert top * sc > F.E4M3.max_finite            # something saturates
+        check_scaled(y.codes(), FMT[yt], wy, err, sc, sc, "y")
+    else:
+        check_values(y.values(), FMT[yt], wy * sc, err * sc + 2 * U * np.abs(wy * sc), "y")
+    check_values(am.cpu().numpy(), F.F32, np.array([top]), err.max(), "amax")
+    big = torch.full((1,), 1e9, device="cuda")         # a larger prior value stays
+    if op == "norm":
+        amp.amp_rmsnorm(x.d, xt, rows, cols, x.ld, None, 0, None, xt, EPS, d_amax=big)
+    else:
+        amp.amp_swiglu(x.d, xt, rows, cols, x.ld, d_amax=big)
+    assert float(big) == 1e9
+
+
+@pytest.mark.parametrize("xt", [amp.BF16, amp.F32])
+def test_norm_of_zero_tiny_and_non_finite_rows(xt):
+    rows, cols = 8, 300
+    v = rand(4, rows, cols)
+    v[1] = 0.0
+    v[2] *= 1e-30                    # h^2 underflows, eps rules; FP32 tiles of 1e-30 still scale
+    v[3] = 1e-38                     # 448 / amax overflows: scale 1
+    v[4, 7] = np.inf
+    v[5, 140] = np.nan
+    v[6, 299] = -np.inf
+    x = Mat(rows, cols, xt, 0, v)
+    yq, ck, y = Tiles(rows, cols), Tiles(rows, cols), Mat(rows, cols, amp.E4M3)
+    am = torch.zeros(1, device="cuda")
+    sc = np.float32([2.0])
+    amp.amp_rmsnorm(x.d, xt, rows, cols, x.ld, None, 0, None, xt, EPS, None, 0, y.d, amp.E4M3, y.ld, dev(sc), am, yq.arg, ck.arg)
+    with np.errstate(all="ignore"):
+        wy, _ = B.rmsnorm(x.v, np.ones(cols), EPS)
+        err = np.where(np.isfinite(wy), np.abs(wy) * (norm_err(cols) + 3 * U) + 2.0 ** -149, 0.0)
+    yq.check(wy, err, "yq")
+    ck.check(x.v, 0.0, "checkpoint")
+    check_scaled(y.codes(), F.E4M3, wy, err, 2.0, 2.0, "y")
+    assert np.isnan(float(am))
+
+
+# x wider than 256 vectors, than 64, and less; odd; part of a tile
+GATE_SHAPES = [(1, 1), (3, 5), (2, 129), (5, 128), (37, 200), (130, 512), (9, 2047), (3, 4100)]
+
+
+@pytest.mark.parametrize("xt", TYPES)
+@pytest.mark.parametrize("rows,cols", GATE_SHAPES)
+def test_swiglu_every_output(xt, rows, cols):
+    pad = 3 if rows % 2 else 8
+    x = Mat(rows, 2 * cols, xt, pad, loud(rows + cols, rows, 2 * cols) * np.where(np.arange(2 * cols) < cols, 3, 1))
+    half = amp.F16 if xt == amp.F16 else amp.BF16
+    y, yq = Mat(rows, cols, half, pad), Tiles(rows, cols, amp.E5M2, pad)
+    ck = Tiles(rows, 2 * cols, amp.E4M3, pad, parts=2)
+    am = torch.zeros(1, device="cuda")
+    amp.amp_swiglu(x.d, xt, rows, cols, x.ld, y.d, half, y.ld, None, am, yq.arg, ck.arg)
+    g, u = x.v[:, :cols], x.v[:, cols:]
+    wy, err = B.swiglu(g, u), swiglu_err(g, u)
+    check_values(y.values(), FMT[half], wy, err, "y")
+    yq.check(wy, err, "yq")
+    ck.check(x.v, 0.0, "checkpoint")
+    check_values(am.cpu().numpy(), F.F32, np.array([np.abs(wy).max()]), err.max(), "amax")
+
+
+def test_swiglu_of_extreme_and_non_finite_gates():
+    vals = np.array([0.0, -0.0, 1e-30, 20.0, -20.0, 87.0, -87.0, 89.0, -89.0, 120.0, -120.0, 3e38, -3e38, np.inf, np.nan, -5.0])
+    rows, cols, xt = 16, 16, amp.F32
+    g, u = np.repeat(vals[:, None], cols, 1), np.repeat(np.array([[1.0, -2.0, 0.5, 1e-3] * 4]), rows, 0)
+    x = Mat(rows, 2 * cols, xt, 0, np.concatenate([g, u], 1))
+    y, dx = Mat(rows, cols, amp.BF16), Mat(rows, 2 * cols, xt)
+    dy = Mat(rows, cols, xt, 0, rand(5, rows, cols))
+    amp.amp_swiglu(x.d, xt, rows, cols, x.ld, y.d, amp.BF16, y.ld)
+    amp.amp_swiglu_backward(dy.d, xt, rows, cols, dy.ld, x.d, x.ld, None, dx.d, dx.ld)
+    ok = np.isfinite(vals)
+    got, grad = y.values(), dx.values()
+    # below -88 exp(-g) overflows and s is 0 (a product of 3e38 and a flushed 2^-127 stays below 2)
+    check_values(got[ok], F.BF16, B.swiglu(g, u)[ok], swiglu_err(g, u)[ok] + 2.0 ** -100, "y")
+    wg, wu = B.swiglu_backward(dy.v, g, u)
+    eg, eu = swiglu_back_err(dy.v, g, u)
+    check_values(grad[ok][:, :cols], F.F32, wg[ok], eg[ok] + 2.0 ** -100, "dg")
+    check_values(grad[ok][:, cols:], F.F32, wu[ok], eu[ok] + 2.0 ** -100, "du")
+    assert np.all(np.isnan(got[14])) and np.all(np.isnan(grad[14]))
+    assert np.array_equal(got[13], np.sign(u[13]) * np.inf)
+
+
+# --------------------------------------------------------------- backward ---
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("saved", ["stored", "checkpoint"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 5), (2, 129), (700, 40), (40, 512), (5, 1000), (33, 2047), (3, 4096),
+                                       (4, 7001), (2, 20483), (2, 40003)])
+def test_norm_backward(dt, saved, rows, cols):
+    pad = 3 if rows % 2 else 8
+    hv = loud(rows + cols, rows, cols)
+    h = Mat(rows, cols, dt, pad, hv) if saved == "stored" else None
+    ck = Tiles(rows, cols, amp.E4M3 if cols % 2 else amp.E5M2, pad, v=F.f32(hv)) if saved == "checkpoint" else None
+    hh = h.v if h else ck.v
+    dy, dres = Mat(rows, cols, dt, pad + 1, rand(2, rows, cols)), Mat(rows, cols, dt, pad + 2, rand(3, rows, cols))
+    gamma = Mat(1, cols, dt, 0, 1 + rand(7, 1, cols, scale=0.1))
+    r = F.f32(B.rmsnorm(hh, gamma.v[0], EPS)[1])
+    rstd = Mat(1, rows, amp.F32, 0, r[None])
+    dx, dgamma = Mat(rows, cols, dt, pad), Mat(1, cols, amp.F32)
+    work = Mat(min(rows, amp.RMSNORM_PARTIALS), cols, amp.F32)
+    args = (dy.d, dt, rows, cols, dy.ld, h.d if h else None, h.ld if h else 0, ck.arg if ck else None, gamma.d, dt, rstd.d)
+    amp.amp_rmsnorm_backward(*args, dres.d, dres.ld, dx.d, dx.ld, dgamma.d, work.d)
+    wx, wg = B.rmsnorm_backward(dy.v, hh, gamma.v[0], r, dres.v)
+    check_values(dx.values(), FMT[dt], wx, dx_err(dy.v, hh, gamma.v[0], r, dres.v, wx), "dx")
+    mass = np.abs(dy.v * hh * r[:, None]).sum(0)
+    check_values(dgamma.values()[0], F.F32, wg, (rows + 8) * U * mass, "dgamma")
+    work.codes()                                        # nothing behind the work area
+    first = dgamma.codes().copy()
+    dgamma2 = Mat(1, cols, amp.F32)
+    amp.amp_rmsnorm_backward(*args, dgamma=dgamma2.d, d_work=work.d)       # no dx; the same sums bit for bit
+    assert np.array_equal(dgamma2.codes(), first)
+    amp.amp_rmsnorm_backward(*args, None, 0, dy.d, dy.ld)                  # in place, no dgamma, no residual gradient
+    w0, _ = B.rmsnorm_backward(dy.v, hh, gamma.v[0], r)
+    check_values(dy.values(), FMT[dt], w0, dx_err(dy.v, hh, gamma.v[0], r, None, w0), "dx in place of dy")
+
+
+def test_norm_backward_over_many_rows_and_shared_gamma():
+    """More rows than partial sums: every block walks several."""
+    rows, cols, dt = 5003, 264, amp.BF16
+    h, dy = Mat(rows, cols, dt, 0, rand(1, rows, cols)), Mat(rows, cols, dt, 0, rand(2, rows, cols))
+    r = F.f32(B.rmsnorm(h.v, np.ones(cols), EPS)[1])
+    dx, dgamma, work = dy, Mat(1, cols, amp.F32), Mat(amp.RMSNORM_PARTIALS, cols, amp.F32)
+    dres = Mat(rows, cols, dt, 0, rand(3, rows, cols))
+    amp.amp_rmsnorm_backward(dy.d, dt, rows, cols, dy.ld, h.d, h.ld, None, None, dt, dev(r.astype(np.float32)), dres.d,
+                             dres.ld, dres.d, dres.ld, dgamma.d, work.d)
+    wx, wg = B.rmsnorm_backward(dy.v, h.v, np.ones(cols), r, dres.v)
+    check_values(dres.values(), F.BF16, wx, dx_err(dy.v, h.v, np.ones(cols), r, dres.v, wx), "dx in place of dres")
+    check_values(dgamma.values()[0], F.F32, wg, (rows + 8) * U * np.abs(dy.v * h.v * r[:, None]).sum(0), "dgamma")
+    dx.codes(), work.codes()
+
+
+def test_norm_gradient_of_the_forward_by_differences():
+    """The gradient that the GPU returns, along random directions, against
+    central differences of the float64 forward pass."""
+    rows, cols, dt = 4, 96, amp.F32
+    x, dy = Mat(rows, cols, dt, 0, rand(1, rows, cols)), Mat(rows, cols, dt, 0, rand(2, rows, cols))
+    gamma = Mat(1, cols, dt, 0, 1 + rand(3, 1, cols, scale=0.1))
+    rstd, dx, dgamma, work = Mat(1, rows, amp.F32), Mat(rows, cols, dt), Mat(1, cols, amp.F32), Mat(rows, cols, amp.F32)
+    amp.amp_rmsnorm(x.d, dt, rows, cols, x.ld, None, 0, gamma.d, dt, EPS, rstd=rstd.d)
+    amp.amp_rmsnorm_backward(dy.d, dt, rows, cols, dy.ld, x.d, x.ld, None, gamma.d, dt, rstd.d, None, 0, dx.d, dx.ld,
+                             dgamma.d, work.d)
+    t = 1e-4
+    for seed in range(3):
+        d, e = rand(10 + seed, rows, cols), rand(20 + seed, cols)
+        f = lambda a, b: (B.rmsnorm(x.v + a * d, gamma.v[0] + b * e, EPS)[0] * dy.v).sum()
+        for got, num in (((dx.values() * d).sum(), (f(t, 0) - f(-t, 0)) / (2 * t)),
+                         ((dgamma.values()[0] * e).sum(), (f(0, t) - f(0, -t)) / (2 * t))):
+            # FP32 roundings of ~400 terms of order 1 and the differences' t^2
+            assert abs(got - num) < 1e-4 * (1 + abs(num)), (got, num)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("saved", ["stored", "checkpoint"])
+@pytest.mark.parametrize("rows,cols", GATE_SHAPES)
+def test_swiglu_backward_in_the_gradients_type(dt, saved, rows, cols):
+    pad = 3 if rows % 2 else 8
+    xv = loud(rows + cols, rows, 2 * cols)
+    x = Mat(rows, 2 * cols, dt, pad, xv) if saved == "stored" else None
+    ck = Tiles(rows, 2 * cols, amp.E4M3, pad, parts=2, v=F.f32(xv)) if saved == "checkpoint" else None
+    xx = x.v if x else ck.v
+    g, u = xx[:, :cols], xx[:, cols:]
+    dy, dx = Mat(rows, cols, dt, pad + 1, rand(2, rows, cols)), Mat(rows, 2 * cols, dt, pad)
+    amp.amp_swiglu_backward(dy.d, dt, rows, cols, dy.ld, x.d if x else None, x.ld if x else 0, ck.arg if ck else None, dx.d, dx.ld)
+    w, e = np.concatenate(B.swiglu_backward(dy.v, g, u), 1), np.concatenate(swiglu_back_err(dy.v, g, u), 1)
+    check_values(dx.values(), FMT[dt], w, e, "dx")
+    if x:
+        amp.amp_swiglu_backward(dy.d, dt, rows, cols, dy.ld, x.d, x.ld, None, x.d, x.ld)
+        check_values(x.values(), FMT[dt], w, e, "dx in place of x")
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("saved", ["stored", "checkpoint"])
+@pytest.mark.parametrize("rows,cols", [(1, 128), (130, 256), (300, 384)])
+def test_swiglu_backward_every_fp8_operand(dt, saved, rows, cols):
+    pad = 3 if rows % 2 else 16
+    xv = loud(rows + cols, rows, 2 * cols)
+    if rows > 200:
+        xv[:128, 5] = 0.0                               # zero column tiles of g and so of du and y
+    x = Mat(rows, 2 * cols, dt, pad, xv) if saved == "stored" else None
+    ck = Tiles(rows, 2 * cols, amp.E5M2, pad, parts=2, v=F.f32(xv)) if saved == "checkpoint" else None
+    xx = x.v if x else ck.v
+    g, u = xx[:, :cols], xx[:, cols:]
+    dv = rand(2, rows, cols, scale=1e-2)
+    if rows > 200:
+        dv[140, 9], dv[141, 200] = np.nan, np.inf
+    dy, dx = Mat(rows, cols, dt, pad + 1), Mat(rows, 2 * cols, dt, pad)
+    codes = np.where(np.isinf(dv), F.encode(np.array(np.inf), FMT[dt]), stored(np.where(np.isinf(dv), 0, dv), dt)[0])
+    full = host(dy.d, NPT[dt]).copy()
+    full[:rows * dy.ld].reshape(rows, dy.ld)[:, :cols] = codes
+    dy.d, dy.v = dev(full), F.decode(codes, FMT[dt])
+    dxq, dxqt, yqt = Tiles(rows, 2 * cols, amp.E5M2, pad), Tiles(2 * cols, rows, amp.E4M3, pad), Tiles(cols, rows, amp.E4M3, pad)
+    args = (dy.d, dt, rows, cols, dy.ld, x.d if x else None, x.ld if x else 0, ck.arg if ck else None)
+    amp.amp_swiglu_backward(*args, dx.d, dx.ld, dxq.arg, dxqt.arg, yqt.arg)
+    with np.errstate(all="ignore"):
+        w, e = np.concatenate(B.swiglu_backward(dy.v, g, u), 1), np.concatenate(swiglu_back_err(dy.v, g, u), 1)
+    e = np.where(np.isfinite(e), e, 0.0)
+    check_values(dx.values(), FMT[dt], w, e, "dx")
+    dxq.check(w, e, "dxq")
+    dxqt.check(w.T, e.T, "dxqt")
+    yqt.check(B.swiglu(g, u).T, swiglu_err(g, u).T, "yqt")
+    for k, t in enumerate((dxq, dxqt, yqt)):            # each alone: the same codes
+        alone = Tiles(*t.q.codes().shape, t.t, pad)
+        amp.amp_swiglu_backward(*args, **{("dxq", "dxqt", "yqt")[k]: alone.arg})
+        assert np.array_equal(alone.q.codes(), t.q.codes()) and np.array_equal(alone.s.codes(), t.s.codes())
+
+
+@pytest.mark.parametrize("rows,cols", [(5, 7), (129, 200), (260, 333)])
+def test_swiglu_backward_transposed_operands_at_odd_widths(rows, cols):
+    dt = amp.BF16
+    x, dy = Mat(rows, 2 * cols, dt, 1, loud(1, rows, 2 * cols)), Mat(rows, cols, dt, 3, rand(2, rows, cols))
+    dxqt, yqt = Tiles(2 * cols, rows, amp.E4M3, 3), Tiles(cols, rows, amp.E5M2, 5)
+    amp.amp_swiglu_backward(dy.d, dt, rows, cols, dy.ld, x.d, x.ld, None, dxqt=dxqt.arg, yqt=yqt.arg)
+    g, u = x.v[:, :cols], x.v[:, cols:]
+    w, e = np.concatenate(B.swiglu_backward(dy.v, g, u), 1), np.concatenate(swiglu_back_err(dy.v, g, u), 1)
+    dxqt.check(w.T, e.T, "dxqt")
+    yqt.check(B.swiglu(g, u).T, swiglu_err(g, u).T, "yqt")
+
+
+# ---------------------------------------------------------- requantization ---
+
+@pytest.mark.parametrize("rows,cols", [(1, 1), (5, 7), (128, 128), (130, 200), (300, 1111), (1, 700), (700, 1)])
+@pytest.mark.parametrize("xt,yt", [(amp.E4M3, amp.E4M3), (amp.E5M2, amp.E4M3), (amp.E4M3, amp.E5M2)])
+@pytest.mark.parametrize("factors", [None, amp.F32, amp.BF16, amp.F16])
+def test_requantize(rows, cols, xt, yt, factors):
+    v = loud(rows + cols, rows, cols)
+    if rows > 200 and cols > 6:
+        v[129:, 3] = 0.0
+        v[150, 6] = np.nan
+    pad = 3 if rows % 2 else 16
+    x, qt = Tiles(rows, cols, xt, pad, v=F.f32(v)), Tiles(cols, rows, yt, pad)
+    w, err, row, col = x.v, U * np.abs(x.v), None, None
+    if factors is not None:
+        row, col = Mat(1, rows, amp.F32, 0, np.exp(rand(3, 1, rows))), Mat(1, cols, factors, 0, 1 + rand(4, 1, cols, scale=0.1))
+        w = w * row.v[0][:, None] * col.v[0]
+        err = 3 * U * np.abs(w)
+    amp.amp_requantize_blockwise(x.arg, rows, cols, row.d if row else None, col.d if col else None, factors or 0, qt.arg)
+    qt.check(w.T, err.T, "qt")
+
+
+def test_requantized_checkpoint_is_the_transposed_operand_of_the_norm():
+    """rstd and gamma as factors give the norm's output from the checkpoint of its input."""
+    rows, cols, xt = 200, 384, amp.BF16
+    x, gamma = Mat(rows, cols, xt, 0, rand(1, rows, cols)), Mat(1, cols, amp.F32, 0, 1 + rand(2, 1, cols, scale=0.1))
+    ck, rstd, qt = Tiles(rows, cols), Mat(1, rows, amp.F32), Tiles(cols, rows)
+    amp.amp_rmsnorm(x.d, xt, rows, cols, x.ld, None, 0, gamma.d, amp.F32, EPS, ckpt=ck.arg, rstd=rstd.d)
+    amp.amp_requantize_blockwise(ck.arg, rows, cols, rstd.d, gamma.d, amp.F32, qt.arg)
+    h = B.dequantize(ck.q.codes(), ck.s.values(), F.E4M3)
+    w = h * rstd.values()[0][:, None] * gamma.v[0]
+    qt.check(w.T, 3 * U * np.abs(w.T), "qt")
+    got = B.dequantize(qt.q.codes(), qt.s.values(), F.E4M3).T
+    y, _ = B.rmsnorm(x.v, gamma.v[0], EPS)
+    top = np.abs(y).max()
+    # two FP8 roundings (half a step each, 2^-4) of values at most `top`
+    assert np.all(np.abs(got - y) <= 2 * 2.0 ** -4 * 1.1 * np.abs(y) + top / 448 * 2.0 ** -9)
+
+
+# -------------------------------------------------------------- empty work ---
+
+def test_empty_work():
+    PAT = 0x5A
+    bufs = [empty(1 << 12, PAT) for _ in range(8)]
+    t = amp.Fp8Tiles(bufs[6], bufs[7], 256, 256)
+    for rows, cols in ((0, 64), (64, 0), (0, 0)):
+        amp.amp_rmsnorm(bufs[0], amp.BF16, rows, cols, 64, None, 0, None, 0, EPS, bufs[1], 64, bufs[2], amp.BF16, 64, None,
+                        bufs[3], t, t, bufs[4])
+        amp.amp_swiglu(bufs[0], amp.BF16, rows, cols, 128, bufs[1], amp.BF16, 64, None, bufs[2], t, t)
+        amp.amp_swiglu_backward(bufs[0], amp.BF16, rows, cols, 64, bufs[1], 128, None, bufs[2], 128, None, t, t)
+        amp.amp_requantize_blockwise(t, rows, cols, None, None, 0, t)
+        amp.amp_rmsnorm_backward(bufs[0], amp.BF16, rows, cols, 64, bufs[1], 64, None, None, 0, bufs[2], dx=bufs[3], lddx=64)
+    assert all(bool(np.all(host(b, np.uint8) == PAT)) for b in bufs)
+    # the empty sum is zero
+    amp.amp_rmsnorm_backward(bufs[0], amp.BF16, 0, 64, 64, bufs[1], 64, None, None, 0, bufs[2], dgamma=bufs[4], d_work=bufs[5])
+    got = host(bufs[4], np.uint8)
+    assert not got[:256].any() and np.all(got[256:] == PAT)
+
+
+# ------------------------------------------------ far offsets, streams, graphs ---
+
+def far(rows, ld, t):
+    """A device matrix whose rows lie far apart (allocated, mostly untouched)."""
+    return torch.empty(rows * ld, dtype=t, device="cuda")
+
+
+def test_offsets_past_32_bits():
+    """Row strides of over 2^31 elements: every index is 64-bit."""
+    rows, cols, ld = 3, 256, (1 << 31) + 24
+    bf = torch.bfloat16
+    xv, dv = stored(rand(1, rows, 2 * cols), amp.BF16), stored(rand(2, rows, cols), amp.BF16)
+
+    def put(codes, n):
+        t = far(rows, ld, bf)
+        t.view(rows, ld)[:, :n] = torch.from_numpy(codes.view(np.int16).copy()).cuda().view(bf)
+        return t
+
+    def take(t, n, np_t):
+        return t.view(rows, ld)[:, :n].contiguous().cpu().view(torch.uint8).numpy().view(np_t)
+
+    x, dy = put(xv[0], 2 * cols), put(dv[0], cols)
+    out = far(rows, ld, bf)
+    q, s = far(rows, ld, torch.uint8), far(4, ld, torch.float32)
+    tiles = amp.Fp8Tiles(q, s, ld, ld)
+    g, u = xv[1][:, :cols], xv[1][:, cols:]
+
+    def scales(nb):
+        return s.view(4, ld)[:nb, :rows].contiguous().cpu().numpy()
+
+    rstd = torch.empty(rows, device="cuda")
+    amp.amp_rmsnorm(x, amp.BF16, rows, cols, ld, dy, ld, None, 0, EPS, out, ld, yq=tiles, rstd=rstd)
+    h = B.residual_add(g, dv[1], F.BF16)
+    y, r = B.rmsnorm(h, np.ones(cols), EPS)
+    assert np.array_equal(F.decode(take(out, cols, np.uint16), F.BF16), h)
+    check_tiles(take(q, cols, np.uint8), scales(2), F.E4M3, y, np.abs(y) * (norm_err(cols) + 3 * U), "norm")
+    amp.amp_swiglu(x, amp.BF16, rows, cols, ld, out, amp.BF16, ld, ckpt=tiles)
+    check_values(F.decode(take(out, cols, np.uint16), F.BF16), F.BF16, B.swiglu(g, u), swiglu_err(g, u), "swiglu")
+    check_tiles(take(q, cols, np.uint8), scales(2), F.E4M3, g, 0.0, "checkpoint g")
+    ckv = B.dequantize(take(q, 2 * cols, np.uint8), scales(4), F.E4M3, 2)
+    gc, uc = ckv[:, :cols], ckv[:, cols:]
+    amp.amp_swiglu_backward(dy, amp.BF16, rows, cols, ld, None, 0, tiles, out, ld)
+    w, e = np.concatenate(B.swiglu_backward(dv[1], gc, uc), 1), np.concatenate(swiglu_back_err(dv[1], gc, uc), 1)
+    check_values(F.decode(take(out, 2 * cols, np.uint16), F.BF16), F.BF16, w, e, "swiglu backward")
+    amp.amp_rmsnorm_backward(dy, amp.BF16, rows, cols, ld, None, 0, tiles, None, 0, rstd, None, 0, out, ld)
+    rf = rstd.cpu().numpy().astype(np.float64)
+    wx, _ = B.rmsnorm_backward(dv[1], gc, np.ones(cols), rf)
+    check_values(F.decode(take(out, cols, np.uint16), F.BF16), F.BF16, wx, dx_err(dv[1], gc, np.ones(cols), rf, None, wx), "dx")
+    qt = Tiles(cols, rows)
+    amp.amp_requantize_blockwise(tiles, rows, cols, None, None, 0, qt.arg)
+    qt.check(gc.T, U * np.abs(gc.T), "requantized")
+
+
+def ffn_block(T, H, N, seed):
+    """One FFN block's buffers and a function that runs its forward and backward pass
+    in fine-grained FP8 through the public entry points."""
+    d = "cuda"
+    gen = torch.Generator(device=d).manual_seed(seed)
+    bf = torch.bfloat16
+
+    def t8(r, k):
+        return amp.Fp8Tiles(torch.zeros(r, k, dtype=torch.uint8, device=d), torch.zeros(-(-k // 128), r, device=d), k, r)
+
+    b = dict(x=torch.randn(T, H, generator=gen, device=d).to(bf), res=torch.randn(T, H, generator=gen, device=d).to(bf),
+             dy=(torch.randn(T, H, generator=gen, device=d) * 1e-2).to(bf),
+             gamma=1 + 0.1 * torch.randn(H, generator=gen, device=d))
+    w1, w2 = torch.randn(2 * N, H, generator=gen, device=d).to(bf) * 0.05, torch.randn(H, N, generator=gen, device=d).to(bf) * 0.05
+    for n, w in (("w1", w1), ("w2", w2)):
+        r, k = w.shape
+        q, qt = torch.empty(r, k, dtype=torch.uint8, device=d), torch.empty(k, r, dtype=torch.uint8, device=d)
+        s, st = torch.empty(k // 128, r // 128, device=d), torch.empty(r // 128, k // 128, device=d)
+        amp.amp_quantize_blockwise(w, amp.BF16, r, k, k, amp.E4M3, 1, q, k, s, r // 128, qt, r, st, k // 128)
+        b[n] = (q, s, qt, st)
+    b.update(h=torch.zeros(T, H, dtype=bf, device=d), rstd=torch.zeros(T, device=d), nq=t8(T, H), hck=t8(T, H),
+             up=torch.zeros(T, 2 * N, dtype=bf, device=d), aq=t8(T, N), upck=t8(T, 2 * N), out=torch.zeros(T, H, dtype=bf, device=d),
+             dyq=t8(T, H), dyqt=t8(H, T), da=torch.zeros(T, N, dtype=bf, device=d), duq=t8(T, 2 * N), duqt=t8(2 * N, T), aqt=t8(N, T),
+             dn=torch.zeros(T, H, dtype=bf, device=d), nqt=t8(H, T), dw1=torch.zeros(2 * N, H, device=d), dw2=torch.zeros(H, N, device=d),
+             dx=torch.zeros(T, H, dtype=bf, device=d), dgamma=torch.zeros(H, device=d),
+             work=torch.zeros(min(T, amp.RMSNORM_PARTIALS), H, device=d))
+
+    def gemm(M, Nn, K, a, w, c, ct, block):
+        q, s = (w[0], w[1]) if block else w.tensors
+        amp.amp_gemm_blockwise(M, Nn, K, a.tensors[0], amp.E4M3, K, a.tensors[1], M, 0, q, amp.E4M3, K, s,
+                               s.shape[1], int(block), c, ct, Nn)
+
+    def run():
+        amp.amp_rmsnorm(b["x"], amp.BF16, T, H, H, b["res"], H, b["gamma"], amp.F32, EPS, b["h"], H, yq=b["nq"], ckpt=b["hck"], rstd=b["rstd"])
+        gemm(T, 2 * N, H, b["nq"], b["w1"], b["up"], amp.BF16, True)
+        amp.amp_swiglu(b["up"], amp.BF16, T, N, 2 * N, yq=b["aq"], ckpt=b["upck"])
+        gemm(T, H, N, b["aq"], b["w2"], b["out"], amp.BF16, True)
+        q, qt = b["dyq"], b["dyqt"]
+        amp.amp_quantize_blockwise(b["dy"], amp.BF16, T, H, H, amp.E4M3, 0, q.tensors[0], H, q.tensors[1], T, qt.tensors[0], T, qt.tensors[1], H)
+        gemm(T, N, H, q, b["w2"][2:], b["da"], amp.BF16, True)
+        amp.amp_swiglu_backward(b["da"], amp.BF16, T, N, N, None, 0, b["upck"], dxq=b["duq"], dxqt=b["duqt"], yqt=b["aqt"])
+        gemm(H, N, T, qt, b["aqt"], b["dw2"], amp.F32, False)
+        gemm(T, H, 2 * N, b["duq"], b["w1"][2:], b["dn"], amp.BF16, True)
+        amp.amp_requantize_blockwise(b["hck"], T, H, b["rstd"], b["gamma"], amp.F32, b["nqt"])
+        gemm(2 * N, H, T, b["duqt"], b["nqt"], b["dw1"], amp.F32, False)
+        amp.amp_rmsnorm_backward(b["dn"], amp.BF16, T, H, H, None, 0, b["hck"], b["gamma"], amp.F32, b["rstd"], b["dy"], H, b["dx"], H,
+                                 b["dgamma"], b["work"])
+    return b, run, (w1, w2)
+
+
+RESULTS = ("h", "out", "dx", "dgamma", "dw1", "dw2")
+
+
+def test_ffn_block_forward_and_backward():
+    """The operators as they are used together: one FFN block in fine-grained
+    FP8 with FP8 checkpoints, against the float64 block.  Each tensor that
+    enters a product carries an FP8 rounding (2^-4 of each value at most, about
+    0.026 in the 2-norm for the 3 mantissa bits' uniform error); the gradients
+    pass through at most five such tensors in turn, whose relative 2-norm
+    errors add to 5 * 0.036 < 0.2 even where they are not independent."""
+    T, H, N = 384, 256, 384
+    b, run, (w1, w2) = ffn_block(T, H, N, 1)
+    run()
+    f = lambda t: t.float().cpu().numpy().astype(np.float64)
+    h = B.residual_add(f(b["x"]), f(b["res"]), F.BF16)
+    gamma, W1, W2, dy = f(b["gamma"]), f(w1), f(w2), f(b["dy"])
+    n, r = B.rmsnorm(h, gamma, EPS)
+    up = n @ W1.T
+    a = B.swiglu(up[:, :N], up[:, N:])
+    da = dy @ W2
+    dup = np.concatenate(B.swiglu_backward(da, up[:, :N], up[:, N:]), 1)
+    dx, dgamma = B.rmsnorm_backward(dup @ W1, h, gamma, r, dy)
+    want = dict(h=h, out=a @ W2.T, dx=dx, dgamma=dgamma, dw1=dup.T @ n, dw2=dy.T @ a)
+    assert np.array_equal(f(b["h"]), h)
+    for k in RESULTS[1:]:
+        rel = np.linalg.norm(f(b[k]) - want[k]) / np.linalg.norm(want[k])
+        assert rel < 0.2, (k, rel)
+
+
+def test_ffn_block_captured_and_replayed_on_another_stream():
+    """Two captured blocks, replayed in turn with new inputs between, on a side
+    stream: every replay equals the eager run bit for bit."""
+    T, H, N = 256, 128, 256
+    made = [ffn_block(T, H, N, 2 + k) for k in range(2)]
+    side = torch.cuda.Stream()
+    graphs = []
+    for b, run, _ in made:
+        run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        graphs.append(g)
+    for turn in range(3):
+        gen = torch.Generator(device="cuda").manual_seed(50 + turn)
+        want = []
+        for b, run, _ in made:
+            b["x"].copy_(torch.randn(T, H, generator=gen, device="cuda"))
+            run()
+            want.append({k: b[k].clone() for k in RESULTS})
+            for k in RESULTS:
+                b[k].zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for g in graphs:
+                g.replay()
+        torch.cuda.synchronize()
+        for (b, _, _), w in zip(made, want):
+            for k in RESULTS:
+                assert torch.equal(b[k], w[k]), (turn, k)
+        with torch.cuda.stream(side):                   # eager calls take the current stream
+            for b, run, _ in made:
+                run()
+        torch.cuda.synchronize()
+        for (b, _, _), w in zip(made, want):
+            assert all(torch.equal(b[k], w[k]) for k in RESULTS)
