@@ -25,119 +25,166 @@ struct NormArgs {
   int64_t rows, cols;
 };
 
-template <int XT>
-__device__ __forceinline__ const void* row_of(const void* p, int64_t i) {
-  return XT == AMP_F32 ? static_cast<const void*>(static_cast<const float*>(p) + i)
-                       : static_cast<const void*>(static_cast<const uint16_t*>(p) + i);
-}
-template <int XT>
-__device__ __forceinline__ void* row_of(void* p, int64_t i) {
-  return const_cast<void*>(row_of<XT>(const_cast<const void*>(p), i));
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+// Sum over the 16 lanes of a DPP row, in every lane (each adds the same pairs).
+__device__ __forceinline__ float sum16(float v) {
+#define AMP_ADD(ctl) v += bitsf(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(fbits(v)), ctl, 0xf, 0xf, false)));
+  AMP_ADD(0x128) AMP_ADD(0x124) AMP_ADD(0x122) AMP_ADD(0x121)
+#undef AMP_ADD
   return v;
 }
+// Sum over a wave, in every lane, without the LDS: rotations within rows of
+// 16, then the rows and the halves exchanged.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = sum16(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(fbits(v), fbits(v), false, false);
+  v = bitsf(a[0]) + bitsf(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(fbits(v), fbits(v), false, false);
+  return bitsf(b[0]) + bitsf(b[1]);
+}
 
-// Sum over the T threads of a row (T >= 64; every thread of the block calls).
-// `red` holds two sets of T / 64 words used in turn, so one barrier a row is
-// enough: a wave that runs ahead writes the other set.
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float* red, int turn) {
+// Sum over the T threads of a row, T a multiple of 64; with T == 64 a row is
+// one wave's, else every thread of the block calls.  `red` holds two sets of
+// 16 words; a caller that loops uses them in `turn`, so that one barrier a row
+// is enough: a wave that runs ahead writes the other set.
+__device__ __forceinline__ float row_sum(float v, int T, float* red, int turn) {
   v = wave_sum(v);
-  if constexpr (T > kWave) {
-    constexpr int W = T / kWave;
-    const int w = threadIdx.x / kWave, first = w / W * W;
-    float* set = red + turn * (blockDim.x / kWave);
+  if (T > kWave) {
+    const int w = threadIdx.x / kWave, W = T / kWave, first = w / W * W, k = threadIdx.x % 16;
+    float* set = red + turn * 16;
     if (threadIdx.x % kWave == 0) set[w] = v;
     __syncthreads();
-    v = 0.0f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) v += set[first + k];
+    v = sum16(k < W ? set[first + k] : 0.0f);
   }
   return v;
 }
 
 // x + res rounded to the stream's type, one vector.
 template <int XT>
-__device__ __forceinline__ u32x4 join(u32x4 w, const NormArgs& a, int64_t row, int64_t c) {
+__device__ __forceinline__ u32x4 join(u32x4 a, u32x4 b) {
   constexpr int E = kVec<XT>;
   float p[E], q[E];
-  widen<XT>(w, p);
-  widen<XT>(load_vec<XT>(row_of<XT>(a.res, row * a.ldr), c, a.cols), q);
+  widen<XT>(a, p);
+  widen<XT>(b, q);
 #pragma unroll
   for (int k = 0; k < E; ++k) p[k] += q[k];
   return narrow<XT>(p);
 }
 
-// Every output of one vector of h; returns its |y| maximum.
 template <int XT>
-__device__ __forceinline__ float norm_outputs(const NormArgs& a, u32x4 w, int64_t row, int64_t c, bool live, float r, float scale) {
+__device__ __forceinline__ float sum_squares(u32x4 w, float ss) {
   constexpr int E = kVec<XT>;
-  float h[E], gm[E], y[E];
+  float h[E];
   widen<XT>(w, h);
-  load_cols<E>(a.gamma, a.gt, c, a.cols, gm);
 #pragma unroll
-  for (int k = 0; k < E; ++k) y[k] = h[k] * r * gm[k];
-  const float am = abs_max<E>(0.0f, y);
-  if (a.yq.q) store_tile<E>(a.yq, row, c, a.cols, c / kTileK, live, y);
-  if (a.ck.q) store_tile<E>(a.ck, row, c, a.cols, c / kTileK, live, h);
-  if (a.y && live) store_plain<E>(a.y, a.yt, row * a.ldy, c, a.cols, scale, am, y);
+  for (int k = 0; k < E; ++k) ss = __builtin_fmaf(h[k], h[k], ss);
+  return ss;
+}
+
+// N <= 4 vectors of a row, `step` columns apart from column c on, in 1x128
+// tiles.  Lane k of a tile's lane group stores the scale of vector k's tile.
+template <int E, int N, bool FULL>
+__device__ __forceinline__ void store_tiles(const amp_fp8_tiles& o, int64_t row, int64_t c0, int c, int step, int n,
+                                            bool live, float (&v)[N][E]) {
+  constexpr int G = kTileK / E;
+  uint32_t m[N], top = 0, w[N][E / 4];
+  float sc[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    m[k] = group_max<G>(mag(abs_max<E>(0.0f, v[k])));
+    top = top > m[k] ? top : m[k];
+  }
+  const float inv = tile_scales<N>(m, fp8_max(o.type), sc);
+  const int mine = c / kTileK * kTileK + (threadIdx.x & 3) * step;   // where that tile begins
+  if (threadIdx.x % G < N && (FULL || mine < n) && live) o.s[(c0 + mine) / kTileK * o.lds + row] = inv;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[k][e] *= sc[k];
+  encode<N, E, false>(o.type, v, top >= kInfBits, w);
+  uint8_t* q = o.q + row * o.ldq + c0;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (live) store_codes<E, FULL>(q, c + k * step, n, w[k]);
+}
+
+// Every output of N vectors of h with their factors gm; returns their |y|
+// maximum.  c0: the first column of this chunk of the row, of which n are left.
+template <int XT, int N, bool FULL>
+__device__ __forceinline__ float norm_outputs(const NormArgs& a, const u32x4 (&w)[N], const float (&gm)[N][kVec<XT>], int64_t row,
+                                              int64_t c0, int c, int step, int n, bool live, float r, float scale) {
+  constexpr int E = kVec<XT>;
+  float y[N][E], am = 0.0f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    widen<XT>(w[k], y[k]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) y[k][e] = y[k][e] * r * gm[k][e];
+    am = abs_max<E>(am, y[k]);
+  }
+  if (a.y) {
+    const int yb = a.yt == AMP_F16 || a.yt == AMP_BF16 ? 2 : 1;
+    store_plain<N, E, FULL>(static_cast<uint8_t*>(a.y) + (row * a.ldy + c0) * yb, a.yt, c, step, n, live, scale, am, y);
+  }
+  if (a.yq.q) store_tiles<E, N, FULL>(a.yq, row, c0, c, step, n, live, y);
+  if (a.ck.q) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) widen<XT>(w[k], y[k]);
+    store_tiles<E, N, FULL>(a.ck, row, c0, c, step, n, live, y);
+  }
   return am;
 }
 
-// T threads hold a row in registers, V vectors each; B threads a block.
-template <int XT, int T, int V, int B>
-__global__ __launch_bounds__(B) void rmsnorm_rows(const NormArgs a) {
-  constexpr int E = kVec<XT>;
-  __shared__ float red[2 * (B / kWave)];
-  __shared__ uint32_t redm[B / kWave];
-  const int tid = threadIdx.x % T, sub = threadIdx.x / T;
+// T threads hold a row in registers, V vectors each.  WAVE: T is 64 and a
+// block of 256 works on four rows; else the block's T threads on one.  FULL:
+// the row is V T whole vectors.
+//
+// HBM-bound.  One row per wave or block and no loop over rows: in a loop the
+// next row's loads wait for this row's stores (one counter holds both) and
+// every stream's pointer stays in vector registers; 16381 x 5120 BF16 took
+// 124-166 us with the loop and 99 without.  T is a power of two: a block of 3
+// or 5 waves fills the four SIMDs unevenly (the same rows in 5 waves: 166 us).
+template <int XT, int V, bool WAVE, bool FULL>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_rows(const NormArgs a) {
+  constexpr int E = kVec<XT>, N = V % 2 == 0 ? 2 : V == 3 ? 3 : 1;
+  __shared__ float red[32];
+  __shared__ uint32_t redm[16];
+  const int T = WAVE ? kWave : blockDim.x;
+  const int64_t row = WAVE ? static_cast<int64_t>(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave)
+                           : static_cast<int64_t>(blockIdx.x);
+  const int c = (WAVE ? threadIdx.x % kWave : threadIdx.x) * E, step = T * E, n = left(a.cols);
+  const bool live = !WAVE || row < a.rows;
   const float scale = a.scale ? *a.scale : 1.0f;
+  const uint32_t seen = amax_seen(a.amax);
+  u32x4 h[V / N][N];
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    h[v / N][v % N] = live ? load_vec<XT, FULL>(elem<XT>(a.x, row * a.ldx), c + v * step, n) : u32x4{0u, 0u, 0u, 0u};
+  if (a.res) {
+    u32x4 q[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) q[v] = live ? load_vec<XT, FULL>(elem<XT>(a.res, row * a.ldr), c + v * step, n) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v / N][v % N] = join<XT>(h[v / N][v % N], q[v]);
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) ss = sum_squares<XT>(h[v / N][v % N], ss);
+  if (a.h && live) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) store_vec<XT, FULL>(elem<XT>(a.h, row * a.ldh), c + v * step, n, h[v / N][v % N]);
+  }
+  ss = row_sum(ss, T, red, 0);
+  const float r = 1.0f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
+  if (a.rstd && live && c == 0) a.rstd[row] = r;
   float am = 0.0f;
-  int turn = 0;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (B / T); r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * (B / T)) {
-    const int64_t row = r0 + sub;
-    const bool live = row < a.rows;
-    u32x4 w[V];
-    float ss = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int64_t c = static_cast<int64_t>(v * T + tid) * E;
-      w[v] = u32x4{0u, 0u, 0u, 0u};
-      if (live) w[v] = load_vec<XT>(row_of<XT>(a.x, row * a.ldx), c, a.cols);
-    }
-    if (a.res) {
+  for (int p = 0; p < V / N; ++p) {
+    float gm[N][E];
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (live) w[v] = join<XT>(w[v], a, row, static_cast<int64_t>(v * T + tid) * E);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float h[E];
-      widen<XT>(w[v], h);
-#pragma unroll
-      for (int k = 0; k < E; ++k) ss += h[k] * h[k];
-    }
-    if (a.h && live) {
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        store_vec<XT>(row_of<XT>(a.h, row * a.ldh), static_cast<int64_t>(v * T + tid) * E, a.cols, w[v]);
-    }
-    ss = row_sum<T>(ss, red, turn);
-    turn ^= 1;
-    const float r = 1.0f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
-    if (a.rstd && live && tid == 0) a.rstd[row] = r;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      am = __builtin_elementwise_maximum(am, norm_outputs<XT>(a, w[v], row, static_cast<int64_t>(v * T + tid) * E, live, r, scale));
+    for (int k = 0; k < N; ++k) load_cols<E, FULL>(a.gamma, a.gt, c + (p * N + k) * step, n, gm[k]);
+    am = __builtin_elementwise_maximum(am, norm_outputs<XT, N, FULL>(a, h[p], gm, row, 0, c + p * N * step, step, n, live, r, scale));
   }
-  if (a.amax) {
-    const uint32_t m = block_max_u32<B>(mag(am), redm);
-    if (threadIdx.x == 0 && m != 0) amax_update(a.amax, m);
-  }
+  if (a.amax) block_amax(am, seen, redm, a.amax);
 }
 
 // Rows too long for the registers: a block walks its row twice (the second
@@ -145,64 +192,104 @@ __global__ __launch_bounds__(B) void rmsnorm_rows(const NormArgs a) {
 template <int XT>
 __global__ __launch_bounds__(1024) void rmsnorm_long(const NormArgs a) {
   constexpr int E = kVec<XT>, T = 1024;
-  __shared__ float red[2 * (T / kWave)];
-  __shared__ uint32_t redm[T / kWave];
+  __shared__ float red[32];
+  __shared__ uint32_t redm[16];
+  const int c = threadIdx.x * E;
   const float scale = a.scale ? *a.scale : 1.0f;
+  const uint32_t seen = amax_seen(a.amax);
   float am = 0.0f;
-  int turn = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    float ss = 0.0f;
-    for (int64_t c = static_cast<int64_t>(threadIdx.x) * E; c < a.cols; c += T * E) {
-      u32x4 w = load_vec<XT>(row_of<XT>(a.x, row * a.ldx), c, a.cols);
-      if (a.res) w = join<XT>(w, a, row, c);
-      if (a.h) store_vec<XT>(row_of<XT>(a.h, row * a.ldh), c, a.cols, w);
-      float h[E];
-      widen<XT>(w, h);
-#pragma unroll
-      for (int k = 0; k < E; ++k) ss += h[k] * h[k];
-    }
-    ss = row_sum<T>(ss, red, turn);
-    turn ^= 1;
-    const float r = 1.0f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
-    if (a.rstd && threadIdx.x == 0) a.rstd[row] = r;
-    // whole waves stay in the loop: a tile's lanes exchange their maxima
-    for (int64_t c0 = 0; c0 < a.cols; c0 += T * E) {
-      const int64_t c = c0 + static_cast<int64_t>(threadIdx.x) * E;
-      u32x4 w;
-      if (a.h) {
-        w = load_vec<XT>(row_of<XT>(a.h, row * a.ldh), c, a.cols);
-      } else {
-        w = load_vec<XT>(row_of<XT>(a.x, row * a.ldx), c, a.cols);
-        if (a.res) w = join<XT>(w, a, row, c);
-      }
-      am = __builtin_elementwise_maximum(am, norm_outputs<XT>(a, w, row, c, true, r, scale));
-    }
+  const int64_t row = blockIdx.x;
+  float ss = 0.0f;
+  for (int64_t c0 = 0; c0 < a.cols; c0 += T * E) {
+    const int n = left(a.cols - c0);
+    u32x4 w = load_vec<XT>(elem<XT>(a.x, row * a.ldx + c0), c, n);
+    if (a.res) w = join<XT>(w, load_vec<XT>(elem<XT>(a.res, row * a.ldr + c0), c, n));
+    if (a.h) store_vec<XT>(elem<XT>(a.h, row * a.ldh + c0), c, n, w);
+    ss = sum_squares<XT>(w, ss);
   }
-  if (a.amax) {
-    const uint32_t m = block_max_u32<T>(mag(am), redm);
-    if (threadIdx.x == 0 && m != 0) amax_update(a.amax, m);
+  ss = row_sum(ss, T, red, 0);
+  const float r = 1.0f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
+  if (a.rstd && threadIdx.x == 0) a.rstd[row] = r;
+  for (int64_t c0 = 0; c0 < a.cols; c0 += T * E) {
+    const int n = left(a.cols - c0);
+    u32x4 w[1];
+    if (a.h) {
+      w[0] = load_vec<XT>(elem<XT>(a.h, row * a.ldh + c0), c, n);
+    } else {
+      w[0] = load_vec<XT>(elem<XT>(a.x, row * a.ldx + c0), c, n);
+      if (a.res) w[0] = join<XT>(w[0], load_vec<XT>(elem<XT>(a.res, row * a.ldr + c0), c, n));
+    }
+    float gm[1][E];
+    load_cols<E>(a.gamma ? elem_of(a.gt, a.gamma, c0) : nullptr, a.gt, c, n, gm[0]);
+    am = __builtin_elementwise_maximum(am, norm_outputs<XT, 1, false>(a, w, gm, row, c0, c, 0, n, true, r, scale));
+  }
+  if (a.amax) block_amax(am, seen, redm, a.amax);
+}
+
+// Threads per row and vectors per thread.  Many rows: the pair that covers
+// the row with the fewest idle slots, of those the one with the most threads
+// (4096 columns BF16, 8192 rows: 512 x 1, 256 x 2 and 128 x 4 within 2 %; 5120:
+// 128 x 5 99 us, 256 x 3 with a sixth of the slots idle 123).  Below 1024 rows
+// the machine is not full and a row's own latency counts, so as few vectors
+// per thread as 1024 threads allow (64 rows of 4096: 512 x 1 4.0 us, 128 x 4
+// 5.5).
+struct RowShape { int T, V; };
+RowShape row_shape(int64_t rows, int64_t nv) {
+  RowShape best{0, 0};
+  for (int T = 64; T <= 1024; T *= 2) {
+    const int64_t V = (nv + T - 1) / T;
+    if (V > (T == 64 ? 4 : 8)) continue;
+    if (best.T == 0 || (rows < 1024 ? V < best.V : V * T <= static_cast<int64_t>(best.V) * best.T)) best = {T, static_cast<int>(V)};
+  }
+  return best;
+}
+
+// Rows a launch: the threads of a grid are counted in 32 bits.
+constexpr int64_t kRowsPerLaunch = 1 << 21;
+
+template <int XT, int V>
+void launch_rows(const NormArgs& a, int T, bool full, hipStream_t s) {
+  const unsigned rows = static_cast<unsigned>(a.rows);
+  if (T == 64) {
+    if constexpr (V <= 4) {
+      if (full) rmsnorm_rows<XT, V, true, true><<<(rows + 3) / 4, 256, 0, s>>>(a);
+      else rmsnorm_rows<XT, V, true, false><<<(rows + 3) / 4, 256, 0, s>>>(a);
+    }
+  } else {
+    if (full) rmsnorm_rows<XT, V, false, true><<<rows, T, 0, s>>>(a);
+    else rmsnorm_rows<XT, V, false, false><<<rows, T, 0, s>>>(a);
   }
 }
 
 template <int XT>
-hipError_t dispatch_rmsnorm(const NormArgs& a, hipStream_t s) {
-  const int64_t nv = (a.cols + kVec<XT> - 1) / kVec<XT>;
-#define AMP_NORM(T, V, B)                                                                              \
-  do {                                                                                                 \
-    int64_t blocks = (a.rows + (B) / (T) - 1) / ((B) / (T));                                           \
-    if (blocks > (1 << 20)) blocks = 1 << 20;                                                          \
-    rmsnorm_rows<XT, T, V, B><<<static_cast<unsigned>(blocks), B, 0, s>>>(a);                          \
-  } while (0)
-  if (nv <= 64) AMP_NORM(64, 1, 256);
-  else if (nv <= 128) AMP_NORM(64, 2, 256);
-  else if (nv <= 256) AMP_NORM(64, 4, 256);
-  else if (nv <= 512) AMP_NORM(256, 2, 256);
-  else if (nv <= 1024) AMP_NORM(256, 4, 256);
-  else if (nv <= 2048) AMP_NORM(1024, 2, 1024);
-  else if (nv <= 8192) AMP_NORM(1024, 8, 1024);
-  else rmsnorm_long<XT><<<static_cast<unsigned>(a.rows < (1 << 20) ? a.rows : (1 << 20)), 1024, 0, s>>>(a);
-#undef AMP_NORM
-  return hipGetLastError();
+hipError_t dispatch_rmsnorm(const NormArgs& whole, hipStream_t s) {
+  constexpr int E = kVec<XT>;
+  const RowShape p = row_shape(whole.rows, (whole.cols + E - 1) / E);
+  for (int64_t r0 = 0; r0 < whole.rows; r0 += kRowsPerLaunch) {
+    NormArgs a = whole;
+    a.rows = whole.rows - r0 < kRowsPerLaunch ? whole.rows - r0 : kRowsPerLaunch;
+    a.x = elem<XT>(a.x, r0 * a.ldx);
+    if (a.res) a.res = elem<XT>(a.res, r0 * a.ldr);
+    if (a.h) a.h = elem<XT>(a.h, r0 * a.ldh);
+    if (a.y) a.y = static_cast<uint8_t*>(a.y) + r0 * a.ldy * dtype_bytes(a.yt);
+    if (a.yq.q) { a.yq.q += r0 * a.yq.ldq; a.yq.s += r0; }
+    if (a.ck.q) { a.ck.q += r0 * a.ck.ldq; a.ck.s += r0; }
+    if (a.rstd) a.rstd += r0;
+    const bool full = a.cols == static_cast<int64_t>(p.T) * p.V * E;
+    switch (p.V) {
+      case 0: rmsnorm_long<XT><<<static_cast<unsigned>(a.rows), 1024, 0, s>>>(a); break;
+      case 1: launch_rows<XT, 1>(a, p.T, full, s); break;
+      case 2: launch_rows<XT, 2>(a, p.T, full, s); break;
+      case 3: launch_rows<XT, 3>(a, p.T, full, s); break;
+      case 4: launch_rows<XT, 4>(a, p.T, full, s); break;
+      case 5: launch_rows<XT, 5>(a, p.T, full, s); break;
+      case 6: launch_rows<XT, 6>(a, p.T, full, s); break;
+      case 7: launch_rows<XT, 7>(a, p.T, full, s); break;
+      default: launch_rows<XT, 8>(a, p.T, full, s); break;
+    }
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
 }
 
 // ------------------------------------------------------------ backward ---
@@ -226,12 +313,15 @@ struct HRaw {
   u32x4 w;
   uint32_t q[E / 4];
   float s;
-  __device__ __forceinline__ void load(const NormBackArgs& a, int64_t row, int64_t c) {
+  // column c of the n that the row has from column c0 on
+  template <bool FULL>
+  __device__ __forceinline__ void load(const NormBackArgs& a, int64_t row, int64_t c0, int c, int n) {
     if constexpr (CK) {
-      load_codes<E>(a.ck.q + row * a.ck.ldq, c, a.cols, q);
-      s = c < a.cols ? a.ck.s[c / kTileK * a.ck.lds + row] : 0.0f;
+      load_codes<E, FULL>(a.ck.q + row * a.ck.ldq + c0, c, n, q);
+      // a lane past the row holds zero codes; it reads the last tile's scale
+      s = a.ck.s[(c0 + (FULL || c < n ? c : n - 1)) / kTileK * a.ck.lds + row];
     } else {
-      w = load_vec<XT>(row_of<XT>(a.h, row * a.ldh), c, a.cols);
+      w = load_vec<XT, FULL>(elem<XT>(a.h, row * a.ldh + c0), c, n);
     }
   }
   __device__ __forceinline__ void values(const NormBackArgs& a, float (&v)[E]) const {
@@ -240,70 +330,88 @@ struct HRaw {
   }
 };
 
-// T threads a row, V vectors each, B / T rows in flight a block; a block
-// strides over the rows with its sums of dy n in registers and writes one row
-// of partial sums at the end (no atomics: the result does not depend on the
-// order in which blocks run).
-template <int XT, bool CK, int T, int V, int B>
-__global__ __launch_bounds__(B) void rmsnorm_back_rows(const NormBackArgs a) {
-  constexpr int E = kVec<XT>, S = B / T;
-  __shared__ float red[2 * (B / kWave)];
-  __shared__ float sums[S > 1 ? T * V * E : 1];
-  const int tid = threadIdx.x % T, sub = threadIdx.x / T;
-  float dg[V][E] = {};
+// dx, one vector: m is the row's mean of g n.
+template <int E>
+__device__ __forceinline__ void dx_of(const float (&dy)[E], const float (&h)[E], const float (&gm)[E], float r, float m, float (&d)[E]) {
+#pragma unroll
+  for (int k = 0; k < E; ++k) d[k] = r * (dy[k] * gm[k] - h[k] * r * m);
+}
+
+// T threads a row, V vectors each, S rows at a time in a block of T S
+// threads; a block strides over the rows with its sums of dy n in registers
+// and writes one row of partial sums at the end (no atomics: the result does
+// not depend on the order in which blocks run).  FULL: the row is V T whole
+// vectors.
+//
+// HBM-bound.  The next row's loads go out before this row's stores: loads and
+// stores complete in one count, so loads issued behind the stores would wait
+// for them.  They are issued without a branch (dy stands in for an absent
+// dres), so that the wait for them can be counted.
+template <int XT, bool CK, int V, int S, bool FULL>
+__global__ __launch_bounds__(S > 1 ? 512 : 1024) void rmsnorm_back_rows(const NormBackArgs a) {
+  constexpr int E = kVec<XT>;
+  __shared__ float red[32];
+  __shared__ float sums[S > 1 ? (512 / S) * V * E : 1];
+  const int T = S > 1 ? 512 / S : blockDim.x;
+  const int sub = S > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / T) : 0;
+  const int tid = S > 1 ? threadIdx.x % T : threadIdx.x, n = left(a.cols);
   const float inv_n = 1.0f / static_cast<float>(a.cols);
+  const void* res = a.dres ? a.dres : a.dy;
+  const int64_t ldr = a.dres ? a.lddr : a.lddy, step = static_cast<int64_t>(gridDim.x) * S;
+  float dg[V][E] = {}, gm[V][E];
+  struct Row { u32x4 dy[V], res[V]; HRaw<XT, CK> h[V]; float r; };
+  auto fetch = [&](int64_t row) __attribute__((always_inline)) {
+    row = row < a.rows ? row : a.rows - 1;   // read again, not used
+    Row w;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = (v * T + tid) * E;
+      w.dy[v] = load_vec<XT, FULL>(elem<XT>(a.dy, row * a.lddy), c, n);
+      w.h[v].template load<FULL>(a, row, 0, c, n);
+      w.res[v] = load_vec<XT, FULL>(elem<XT>(res, row * ldr), c, n);
+    }
+    w.r = a.rstd[row];
+    return w;
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * S + sub;
+  Row w = fetch(row);
+#pragma unroll
+  for (int v = 0; v < V; ++v) load_cols<E, FULL>(a.gamma, a.gt, (v * T + tid) * E, n, gm[v]);
   int turn = 0;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * S; r0 < a.rows; r0 += static_cast<int64_t>(gridDim.x) * S) {
-    const int64_t row = r0 + sub;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * S; r0 < a.rows; r0 += step, row += step) {
     const bool live = row < a.rows;
-    u32x4 wd[V];
-    HRaw<XT, CK> hr[V];
-    if (live) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int64_t c = static_cast<int64_t>(v * T + tid) * E;
-        wd[v] = load_vec<XT>(row_of<XT>(a.dy, row * a.lddy), c, a.cols);
-        hr[v].load(a, row, c);
-      }
-    }
-    const float r = live ? a.rstd[row] : 0.0f;
     float dot = 0.0f;
-    if (live) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float dy[E], h[E];
+      widen<XT>(w.dy[v], dy);
+      w.h[v].values(a, h);
+#pragma unroll
+      for (int k = 0; k < E; ++k) {
+        const float t = dy[k] * (h[k] * w.r);
+        dot = __builtin_fmaf(t, gm[v][k], dot);
+        dg[v][k] += live ? t : 0.0f;
+      }
+    }
+    const Row next = fetch(row + step);
+    const float m = row_sum(dot, T, red, turn) * inv_n;
+    turn ^= 1;
+    if (a.dx && live) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float dy[E], h[E], gm[E];
-        widen<XT>(wd[v], dy);
-        hr[v].values(a, h);
-        load_cols<E>(a.gamma, a.gt, static_cast<int64_t>(v * T + tid) * E, a.cols, gm);
+        float dy[E], h[E], d[E];
+        widen<XT>(w.dy[v], dy);
+        w.h[v].values(a, h);
+        dx_of<E>(dy, h, gm[v], w.r, m, d);
+        if (a.dres) {
+          widen<XT>(w.res[v], dy);
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          const float n = h[k] * r;
-          dot += dy[k] * gm[k] * n;
-          dg[v][k] += dy[k] * n;
+          for (int k = 0; k < E; ++k) d[k] += dy[k];
         }
+        store_vec<XT, FULL>(elem<XT>(a.dx, row * a.lddx), (v * T + tid) * E, n, narrow<XT>(d));
       }
     }
-    if (a.dx) {
-      const float m = row_sum<T>(dot, red, turn) * inv_n;
-      turn ^= 1;
-      if (live) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int64_t c = static_cast<int64_t>(v * T + tid) * E;
-          float dy[E], h[E], gm[E], d[E] = {};
-          widen<XT>(wd[v], dy);
-          hr[v].values(a, h);
-          load_cols<E>(a.gamma, a.gt, c, a.cols, gm);
-          if (a.dres) widen<XT>(load_vec<XT>(row_of<XT>(a.dres, row * a.lddr), c, a.cols), d);
-#pragma unroll
-          for (int k = 0; k < E; ++k) {
-            const float t = r * (dy[k] * gm[k] - h[k] * r * m);
-            d[k] = a.dres ? t + d[k] : t;
-          }
-          store_vec<XT>(row_of<XT>(a.dx, row * a.lddx), c, a.cols, narrow<XT>(d));
-        }
-      }
-    }
+    w = next;
   }
   if (a.part == nullptr) return;
   if constexpr (S > 1) {
@@ -328,12 +436,10 @@ __global__ __launch_bounds__(B) void rmsnorm_back_rows(const NormBackArgs a) {
   float* p = a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int64_t c = static_cast<int64_t>(v * T + tid) * E;
 #pragma unroll
     for (int q = 0; q < E / 4; ++q) {
-      const float4 f = {dg[v][4 * q], dg[v][4 * q + 1], dg[v][4 * q + 2], dg[v][4 * q + 3]};
-      const u32x4 w = {fbits(f.x), fbits(f.y), fbits(f.z), fbits(f.w)};
-      store_vec<AMP_F32>(p, c + 4 * q, a.cols, w);
+      const u32x4 w4 = {fbits(dg[v][4 * q]), fbits(dg[v][4 * q + 1]), fbits(dg[v][4 * q + 2]), fbits(dg[v][4 * q + 3])};
+      store_vec<AMP_F32, FULL>(p, (v * T + tid) * E + 4 * q, n, w4);
     }
   }
 }
@@ -343,44 +449,44 @@ __global__ __launch_bounds__(B) void rmsnorm_back_rows(const NormBackArgs a) {
 template <int XT, bool CK>
 __global__ __launch_bounds__(1024) void rmsnorm_back_long(const NormBackArgs a) {
   constexpr int E = kVec<XT>, T = 1024;
-  __shared__ float red[2 * (T / kWave)];
+  __shared__ float red[32];
   const float inv_n = 1.0f / static_cast<float>(a.cols);
-  float* p = a.part ? a.part + static_cast<int64_t>(blockIdx.x) * a.cols : nullptr;
+  float* part = a.part ? a.part + static_cast<int64_t>(blockIdx.x) * a.cols : nullptr;
+  const int c = threadIdx.x * E;
   int turn = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const float r = a.rstd[row];
-    float dot = 0.0f;
-    for (int64_t c = static_cast<int64_t>(threadIdx.x) * E; c < a.cols; c += T * E) {
-      float dy[E], h[E], gm[E];
-      HRaw<XT, CK> hr;
-      widen<XT>(load_vec<XT>(row_of<XT>(a.dy, row * a.lddy), c, a.cols), dy);
-      hr.load(a, row, c);
-      hr.values(a, h);
-      load_cols<E>(a.gamma, a.gt, c, a.cols, gm);
-#pragma unroll
-      for (int k = 0; k < E; ++k) {
-        const float n = h[k] * r;
-        dot += dy[k] * gm[k] * n;
-        if (p && c + k < a.cols) p[c + k] = (row == blockIdx.x ? 0.0f : p[c + k]) + dy[k] * n;
-      }
-    }
-    if (a.dx) {
-      const float m = row_sum<T>(dot, red, turn) * inv_n;
-      turn ^= 1;
-      for (int64_t c = static_cast<int64_t>(threadIdx.x) * E; c < a.cols; c += T * E) {
-        float dy[E], h[E], gm[E], d[E] = {};
+    float dot = 0.0f, m = 0.0f;
+    for (int pass = 0; pass < (a.dx ? 2 : 1); ++pass) {
+      for (int64_t c0 = 0; c0 < a.cols; c0 += T * E) {
+        const int n = left(a.cols - c0);
+        if (c >= n) break;
+        float dy[E], h[E], gm[E], d[E];
         HRaw<XT, CK> hr;
-        widen<XT>(load_vec<XT>(row_of<XT>(a.dy, row * a.lddy), c, a.cols), dy);
-        hr.load(a, row, c);
+        widen<XT>(load_vec<XT>(elem<XT>(a.dy, row * a.lddy + c0), c, n), dy);
+        hr.template load<false>(a, row, c0, c, n);
         hr.values(a, h);
-        load_cols<E>(a.gamma, a.gt, c, a.cols, gm);
-        if (a.dres) widen<XT>(load_vec<XT>(row_of<XT>(a.dres, row * a.lddr), c, a.cols), d);
+        load_cols<E>(a.gamma ? elem_of(a.gt, a.gamma, c0) : nullptr, a.gt, c, n, gm);
+        if (pass == 0) {
 #pragma unroll
-        for (int k = 0; k < E; ++k) {
-          const float t = r * (dy[k] * gm[k] - h[k] * r * m);
-          d[k] = a.dres ? t + d[k] : t;
+          for (int k = 0; k < E; ++k) {
+            const float t = dy[k] * (h[k] * r);
+            dot = __builtin_fmaf(t, gm[k], dot);
+            if (part && c + k < n) part[c0 + c + k] = (row == blockIdx.x ? 0.0f : part[c0 + c + k]) + t;
+          }
+        } else {
+          dx_of<E>(dy, h, gm, r, m, d);
+          if (a.dres) {
+            widen<XT>(load_vec<XT>(elem<XT>(a.dres, row * a.lddr + c0), c, n), dy);
+#pragma unroll
+            for (int k = 0; k < E; ++k) d[k] += dy[k];
+          }
+          store_vec<XT>(elem<XT>(a.dx, row * a.lddx + c0), c, n, narrow<XT>(d));
         }
-        store_vec<XT>(row_of<XT>(a.dx, row * a.lddx), c, a.cols, narrow<XT>(d));
+      }
+      if (pass == 0 && a.dx) {
+        m = row_sum(dot, T, red, turn) * inv_n;
+        turn ^= 1;
       }
     }
   }
@@ -392,10 +498,11 @@ __global__ __launch_bounds__(256) void dgamma_sum(const float* __restrict__ part
                                                   float* __restrict__ dgamma) {
   __shared__ float sums[32][33];
   const int lane = threadIdx.x % 8, strand = threadIdx.x / 8;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + 4 * lane;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 32;
+  const int n = left(cols - c0);
   float t[4] = {};
   for (int64_t p = strand; p < P; p += 32) {
-    const u32x4 w = load_vec<AMP_F32>(part + p * cols, c, cols);
+    const u32x4 w = load_vec<AMP_F32>(part + p * cols + c0, 4 * lane, n);
 #pragma unroll
     for (int k = 0; k < 4; ++k) t[k] += bitsf(w[k]);
   }
@@ -406,8 +513,7 @@ __global__ __launch_bounds__(256) void dgamma_sum(const float* __restrict__ part
     float v = 0.0f;
 #pragma unroll
     for (int k = 0; k < 32; ++k) v += sums[k][threadIdx.x];
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
-    if (col < cols) dgamma[col] = v;
+    if (static_cast<int>(threadIdx.x) < n) dgamma[c0 + threadIdx.x] = v;
   }
 }
 
@@ -415,20 +521,23 @@ template <int XT, bool CK>
 hipError_t dispatch_back(const NormBackArgs& a, float* dgamma, hipStream_t s) {
   const int64_t nv = (a.cols + kVec<XT> - 1) / kVec<XT>;
   int64_t blocks = 0;
-#define AMP_BACK(T, V, B)                                                                              \
+#define AMP_BACK(V, S, B)                                                                              \
   do {                                                                                                 \
-    blocks = (a.rows + (B) / (T) - 1) / ((B) / (T));                                                   \
+    blocks = (a.rows + (S) - 1) / (S);                                                                 \
     if (blocks > AMP_RMSNORM_PARTIALS) blocks = AMP_RMSNORM_PARTIALS;                                  \
-    rmsnorm_back_rows<XT, CK, T, V, B><<<static_cast<unsigned>(blocks), B, 0, s>>>(a);                 \
+    if (a.cols == static_cast<int64_t>((B) / (S)) * (V) * kVec<XT>)                                    \
+      rmsnorm_back_rows<XT, CK, V, S, true><<<static_cast<unsigned>(blocks), B, 0, s>>>(a);            \
+    else                                                                                               \
+      rmsnorm_back_rows<XT, CK, V, S, false><<<static_cast<unsigned>(blocks), B, 0, s>>>(a);           \
   } while (0)
   if (a.rows > 0) {
-    if (nv <= 64) AMP_BACK(64, 1, 512);
-    else if (nv <= 128) AMP_BACK(64, 2, 512);
-    else if (nv <= 256) AMP_BACK(128, 2, 512);
-    else if (nv <= 512) AMP_BACK(256, 2, 512);
-    else if (nv <= 1024) AMP_BACK(512, 2, 512);
-    else if (nv <= 2048) AMP_BACK(1024, 2, 1024);
-    else if (nv <= 4096) AMP_BACK(1024, 4, 1024);
+    if (nv <= 64) AMP_BACK(1, 8, 512);
+    else if (nv <= 128) AMP_BACK(1, 4, 512);
+    else if (nv <= 256) AMP_BACK(1, 2, 512);
+    else if (nv <= 512) AMP_BACK(1, 1, 512);
+    else if (nv <= 1024) AMP_BACK(1, 1, 1024);
+    else if (nv <= 2048) AMP_BACK(2, 1, 1024);
+    else if (nv <= 4096) AMP_BACK(4, 1, 1024);
     else {
       blocks = a.rows < AMP_RMSNORM_PARTIALS ? a.rows : AMP_RMSNORM_PARTIALS;
       rmsnorm_back_long<XT, CK><<<static_cast<unsigned>(blocks), 1024, 0, s>>>(a);

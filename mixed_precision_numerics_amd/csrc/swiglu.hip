@@ -21,13 +21,6 @@ struct GateArgs {
   int64_t rows, cols;
 };
 
-template <int XT>
-__device__ __forceinline__ int64_t elem_bytes(int64_t i) { return i * (XT == AMP_F32 ? 4 : 2); }
-template <int XT>
-__device__ __forceinline__ const void* at(const void* p, int64_t i) { return static_cast<const uint8_t*>(p) + elem_bytes<XT>(i); }
-template <int XT>
-__device__ __forceinline__ void* at(void* p, int64_t i) { return static_cast<uint8_t*>(p) + elem_bytes<XT>(i); }
-
 // s = 1 / (1 + e), e = exp(-g), from the hardware's exponential and
 // reciprocal (each within an ulp; the scaled argument adds |g| 2^-24, so s is
 // good to a few 2^-23 over the range where it is not negligible).  g = -inf
@@ -45,93 +38,141 @@ __device__ __forceinline__ int64_t tile_of(int64_t c, int half, int64_t cols) {
   return c / kTileK + (half ? (cols + kTileK - 1) / kTileK : 0);
 }
 
+// One vector of R rows (S apart, from row0 on) in 1x128 tiles; `blk` is the
+// tile's index along K.  Lane i of a tile's lane group stores row i's scale.
+template <int E, int R, bool FULL>
+__device__ __forceinline__ void store_row_tiles(const amp_fp8_tiles& o, int64_t row0, int S, int64_t rows, int64_t c0, int c,
+                                                int n, int64_t blk, float (&v)[R][E]) {
+  constexpr int G = kTileK / E;
+  uint32_t m[R], top = 0, w[R][E / 4];
+  float sc[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    m[i] = group_max<G>(mag(abs_max<E>(0.0f, v[i])));
+    top = top > m[i] ? top : m[i];
+  }
+  const float inv = tile_scales<R>(m, fp8_max(o.type), sc);
+  const int64_t mine = row0 + (threadIdx.x & 3) * S;
+  if (threadIdx.x % G < R && mine < rows && (FULL || c / kTileK * kTileK < n)) o.s[blk * o.lds + mine] = inv;
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int k = 0; k < E; ++k) v[i][k] *= sc[i];
+  encode<R, E, false>(o.type, v, top >= kInfBits, w);
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (row0 + i * S < rows) store_codes<E, FULL>(o.q + (row0 + i * S) * o.ldq + c0, c, n, w[i]);
+}
+
 // W threads cover W vectors of a row, 256 / W rows side by side and R of
-// those groups one after the other; blockIdx.x runs along the row.
-template <int XT, int W, int R>
+// those groups one after the other; blockIdx.x runs along the row.  FULL: the
+// row is whole spans of W vectors.
+template <int XT, int W, int R, bool FULL>
 __global__ __launch_bounds__(256) void swiglu_rows(const GateArgs a) {
   constexpr int E = kVec<XT>, S = 256 / W;
   __shared__ uint32_t redm[256 / kWave];
-  const int64_t c = (static_cast<int64_t>(blockIdx.x) * W + threadIdx.x % W) * E;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * (W * E);   // the block's first column
+  const int c = threadIdx.x % W * E, n = left(a.cols - c0);
+  const int sub = W >= kWave ? __builtin_amdgcn_readfirstlane(threadIdx.x / W) : threadIdx.x / W;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * (S * R) + sub;
   const float scale = a.scale ? *a.scale : 1.0f;
-  float am = 0.0f;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * (S * R); r0 < a.rows; r0 += static_cast<int64_t>(gridDim.y) * (S * R)) {
-    u32x4 wg[R], wu[R];
+  const uint32_t seen = amax_seen(a.amax);
+  u32x4 wg[R], wu[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int64_t row = r0 + i * S + threadIdx.x / W;
-      wg[i] = wu[i] = u32x4{0u, 0u, 0u, 0u};
-      if (row < a.rows) {
-        wg[i] = load_vec<XT>(at<XT>(a.x, row * a.ldx), c, a.cols);
-        wu[i] = load_vec<XT>(at<XT>(a.x, row * a.ldx + a.cols), c, a.cols);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int64_t row = r0 + i * S + threadIdx.x / W;
-      const bool live = row < a.rows;
-      float g[E], u[E], y[E];
-      widen<XT>(wg[i], g);
-      widen<XT>(wu[i], u);
-#pragma unroll
-      for (int k = 0; k < E; ++k) y[k] = g[k] * gate(g[k]).s * u[k];
-      const float m = abs_max<E>(0.0f, y);
-      am = __builtin_elementwise_maximum(am, m);
-      if (a.yq.q) store_tile<E>(a.yq, row, c, a.cols, c / kTileK, live, y);
-      if (a.ck.q) {
-        store_tile<E>(a.ck, row, c, a.cols, tile_of(c, 0, a.cols), live, g);
-        amp_fp8_tiles up = a.ck;
-        up.q += a.cols;
-        store_tile<E>(up, row, c, a.cols, tile_of(c, 1, a.cols), live, u);
-      }
-      if (a.y && live) store_plain<E>(a.y, a.yt, row * a.ldy, c, a.cols, scale, m, y);
+  for (int i = 0; i < R; ++i) {
+    const int64_t row = row0 + i * S;
+    wg[i] = wu[i] = u32x4{0u, 0u, 0u, 0u};
+    if (row < a.rows) {
+      const void* p = elem<XT>(a.x, row * a.ldx + c0);
+      wg[i] = load_vec<XT, FULL>(p, c, n);
+      wu[i] = load_vec<XT, FULL>(elem<XT>(p, a.cols), c, n);
     }
   }
-  if (a.amax) {
-    const uint32_t m = block_max_u32<256>(mag(am), redm);
-    if (threadIdx.x == 0 && m != 0) amax_update(a.amax, m);
+  float y[R][E], am = 0.0f;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    float g[E], u[E];
+    widen<XT>(wg[i], g);
+    widen<XT>(wu[i], u);
+#pragma unroll
+    for (int k = 0; k < E; ++k) y[i][k] = g[k] * gate(g[k]).s * u[k];
+    am = abs_max<E>(am, y[i]);
   }
+  if (a.y) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int64_t row = row0 + i * S, at = (row * a.ldy + c0) * (a.yt == AMP_F16 || a.yt == AMP_BF16 ? 2 : 1);
+      store_plain<1, E, FULL>(static_cast<uint8_t*>(a.y) + at, a.yt, c, 0, n, row < a.rows, scale, am,
+                              reinterpret_cast<const float(&)[1][E]>(y[i]));
+    }
+  }
+  if (a.yq.q) store_row_tiles<E, R, FULL>(a.yq, row0, S, a.rows, c0, c, n, (c0 + c) / kTileK, y);
+  if (a.ck.q) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) widen<XT>(wg[i], y[i]);
+    store_row_tiles<E, R, FULL>(a.ck, row0, S, a.rows, c0, c, n, tile_of(c0 + c, 0, a.cols), y);
+#pragma unroll
+    for (int i = 0; i < R; ++i) widen<XT>(wu[i], y[i]);
+    amp_fp8_tiles up = a.ck;
+    up.q += a.cols;
+    store_row_tiles<E, R, FULL>(up, row0, S, a.rows, c0, c, n, tile_of(c0 + c, 1, a.cols), y);
+  }
+  if (a.amax) block_amax(am, seen, redm, a.amax);
 }
 
-// Backward with dx in the gradient's own type only: element-wise, as above.
-template <int XT, bool CK, int W, int R>
+// Backward with dx in the gradient's own type only: element-wise, laid out
+// as above.
+template <int XT, bool CK, int W, int R, bool FULL>
 __global__ __launch_bounds__(256) void swiglu_back_rows(const GateArgs a) {
   constexpr int E = kVec<XT>, S = 256 / W;
-  const int64_t c = (static_cast<int64_t>(blockIdx.x) * W + threadIdx.x % W) * E;
-  if (c >= a.cols) return;
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * (S * R); r0 < a.rows; r0 += static_cast<int64_t>(gridDim.y) * (S * R)) {
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * (W * E);
+  const int c = threadIdx.x % W * E, n = left(a.cols - c0);
+  const int sub = W >= kWave ? __builtin_amdgcn_readfirstlane(threadIdx.x / W) : threadIdx.x / W;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * (S * R) + sub;
+  if (!FULL && c >= n) return;
+  u32x4 wd[R], wg[R], wu[R];
+  uint32_t qg[R][E / 4], qu[R][E / 4];
+  float sg[R], su[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int64_t row = r0 + i * S + threadIdx.x / W;
-      if (row >= a.rows) continue;
-      float g[E], u[E], dy[E], dg[E], du[E];
-      widen<XT>(load_vec<XT>(at<XT>(a.dy, row * a.lddy), c, a.cols), dy);
-      if constexpr (CK) {
-        uint32_t q[E / 4];
-        load_codes<E>(a.ck.q + row * a.ck.ldq, c, a.cols, q);
-        decode<E>(a.ck.type, q, a.ck.s[tile_of(c, 0, a.cols) * a.ck.lds + row], g);
-        load_codes<E>(a.ck.q + row * a.ck.ldq + a.cols, c, a.cols, q);
-        decode<E>(a.ck.type, q, a.ck.s[tile_of(c, 1, a.cols) * a.ck.lds + row], u);
-      } else {
-        widen<XT>(load_vec<XT>(at<XT>(a.x, row * a.ldx), c, a.cols), g);
-        widen<XT>(load_vec<XT>(at<XT>(a.x, row * a.ldx + a.cols), c, a.cols), u);
-      }
-#pragma unroll
-      for (int k = 0; k < E; ++k) {
-        const Gate p = gate(g[k]);
-        const float t = dy[k] * p.s;
-        du[k] = t * g[k];
-        dg[k] = t * u[k] * (1.0f + g[k] * p.om);
-      }
-      store_vec<XT>(at<XT>(a.y, row * a.ldy), c, a.cols, narrow<XT>(dg));
-      store_vec<XT>(at<XT>(a.y, row * a.ldy + a.cols), c, a.cols, narrow<XT>(du));
+  for (int i = 0; i < R; ++i) {
+    const int64_t row = row0 + i * S < a.rows ? row0 + i * S : a.rows - 1;   // read again, not used
+    wd[i] = load_vec<XT, FULL>(elem<XT>(a.dy, row * a.lddy + c0), c, n);
+    if constexpr (CK) {
+      const uint8_t* q = a.ck.q + row * a.ck.ldq + c0;
+      load_codes<E, FULL>(q, c, n, qg[i]);
+      load_codes<E, FULL>(q + a.cols, c, n, qu[i]);
+      sg[i] = a.ck.s[tile_of(c0 + c, 0, a.cols) * a.ck.lds + row];
+      su[i] = a.ck.s[tile_of(c0 + c, 1, a.cols) * a.ck.lds + row];
+    } else {
+      const void* p = elem<XT>(a.x, row * a.ldx + c0);
+      wg[i] = load_vec<XT, FULL>(p, c, n);
+      wu[i] = load_vec<XT, FULL>(elem<XT>(p, a.cols), c, n);
     }
   }
-}
-
-// 4 elements of a row of the type XT.
-template <int XT>
-__device__ __forceinline__ void load4(const void* p, int64_t c, int64_t cols, float (&v)[4]) {
-  load_cols<4>(p, XT, c, cols, v);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t row = row0 + i * S;
+    if (row >= a.rows) return;
+    float g[E], u[E], dy[E], dg[E], du[E];
+    widen<XT>(wd[i], dy);
+    if constexpr (CK) {
+      decode<E>(a.ck.type, qg[i], sg[i], g);
+      decode<E>(a.ck.type, qu[i], su[i], u);
+    } else {
+      widen<XT>(wg[i], g);
+      widen<XT>(wu[i], u);
+    }
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const Gate p = gate(g[k]);
+      const float t = dy[k] * p.s;
+      du[k] = t * g[k];
+      dg[k] = t * u[k] * (1.0f + g[k] * p.om);
+    }
+    void* p = elem<XT>(a.y, row * a.ldy + c0);
+    store_vec<XT, FULL>(p, c, n, narrow<XT>(dg));
+    store_vec<XT, FULL>(elem<XT>(p, a.cols), c, n, narrow<XT>(du));
+  }
 }
 
 // Backward with FP8 operands: one 128x128 region of dy, g and u per block.
@@ -145,23 +186,24 @@ __global__ __launch_bounds__(kRegThreads) void swiglu_back_region(const GateArgs
   __shared__ float rscale[2][kTileK];
   const int t = threadIdx.x, cg = t % 32, rg = t / 32;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kTileK, r0 = static_cast<int64_t>(blockIdx.y) * kTileK;
-  const int64_t c = c0 + 4 * cg, r = r0 + kRegRows * rg;
+  const int c = 4 * cg, r = kRegRows * rg;
+  const int ncols = left(a.cols - c0) < kTileK ? left(a.cols - c0) : kTileK, nrows = left(a.rows - r0);
   float v[3][kRegRows][kRegCols];   // dg, du, y
 #pragma unroll
   for (int i = 0; i < kRegRows; ++i) {
-    const int64_t row = r + i;
+    const int64_t row = r0 + r + i;
     float g[4] = {}, u[4] = {}, dy[4] = {};
-    if (row < a.rows) {
-      load4<XT>(at<XT>(a.dy, row * a.lddy), c, a.cols, dy);
+    if (r + i < nrows) {
+      load_cols<4>(elem<XT>(a.dy, row * a.lddy + c0), XT, c, ncols, dy);
       if constexpr (CK) {
         uint32_t q[1];
-        load_codes<4>(a.ck.q + row * a.ck.ldq, c, a.cols, q);
+        load_codes<4>(a.ck.q + row * a.ck.ldq + c0, c, ncols, q);
         decode<4>(a.ck.type, q, a.ck.s[tile_of(c0, 0, a.cols) * a.ck.lds + row], g);
-        load_codes<4>(a.ck.q + row * a.ck.ldq + a.cols, c, a.cols, q);
+        load_codes<4>(a.ck.q + row * a.ck.ldq + a.cols + c0, c, ncols, q);
         decode<4>(a.ck.type, q, a.ck.s[tile_of(c0, 1, a.cols) * a.ck.lds + row], u);
       } else {
-        load4<XT>(at<XT>(a.x, row * a.ldx), c, a.cols, g);
-        load4<XT>(at<XT>(a.x, row * a.ldx + a.cols), c, a.cols, u);
+        load_cols<4>(elem<XT>(a.x, row * a.ldx + c0), XT, c, ncols, g);
+        load_cols<4>(elem<XT>(a.x, row * a.ldx + a.cols + c0), XT, c, ncols, u);
       }
     }
 #pragma unroll
@@ -172,15 +214,16 @@ __global__ __launch_bounds__(kRegThreads) void swiglu_back_region(const GateArgs
       v[1][i][k] = d * g[k];
       v[2][i][k] = gu * u[k];
     }
-    if (a.y && row < a.rows) {
+    if (a.y && r + i < nrows) {
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        float f[4] = {v[n][i][0], v[n][i][1], v[n][i][2], v[n][i][3]};
-        const int64_t base = row * a.ldy + (n ? a.cols : 0);
+        void* p = elem<XT>(a.y, row * a.ldy + (n ? a.cols : 0) + c0);
+        const float(&f)[4] = v[n][i];
         if constexpr (XT == AMP_F32) {
-          store_vec<AMP_F32>(at<XT>(a.y, base), c, a.cols, narrow<AMP_F32>(f));
+          store_vec<AMP_F32>(p, c, ncols, narrow<AMP_F32>(f));
         } else {
-          store_plain<4>(a.y, XT, base, c, a.cols, 1.0f, 0.0f, f);
+          const uint32_t h[2] = {pack16(XT == AMP_BF16, f[0], f[1]), pack16(XT == AMP_BF16, f[2], f[3])};
+          store16<2>(p, c, ncols, h);
         }
       }
     }
@@ -191,34 +234,34 @@ __global__ __launch_bounds__(kRegThreads) void swiglu_back_region(const GateArgs
 #pragma unroll
       for (int i = 0; i < kRegRows; ++i) {
         const uint32_t m = group_max<32>(mag(abs_max<4>(0.0f, v[n][i])));
-        if (cg == 0) rmax[n][kRegRows * rg + i] = m;
+        if (cg == 0) rmax[n][r + i] = m;
       }
     __syncthreads();
     if (t < 2 * kTileK) {
       const int n = t / kTileK, i = t % kTileK;
       const uint32_t m = rmax[n][i];
       const float sc = scale_of(m, fp8_max(a.dxq.type));
-      rscale[n][i] = m >= 0x7f800000u ? -sc : sc;   // sign: the tile holds a NaN or infinity
-      if (r0 + i < a.rows) a.dxq.s[tile_of(c0, n, a.cols) * a.dxq.lds + r0 + i] = 1.0f / sc;
+      rscale[n][i] = m >= kInfBits ? -sc : sc;   // sign: the tile holds a NaN or infinity
+      if (i < nrows) a.dxq.s[tile_of(c0, n, a.cols) * a.dxq.lds + r0 + i] = 1.0f / sc;
     }
     __syncthreads();
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int i = 0; i < kRegRows; ++i) {
-        const float sc = rscale[n][kRegRows * rg + i];
-        float f[4];
+        const float sc = rscale[n][r + i];
+        float f[1][4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) f[k] = v[n][i][k] * fabsf(sc);
-        uint32_t w[1];
-        encode<4>(a.dxq.type, f, sc < 0.0f, w);
-        if (r + i < a.rows) store_codes<4>(a.dxq.q + (r + i) * a.dxq.ldq + (n ? a.cols : 0), c, a.cols, w);
+        for (int k = 0; k < 4; ++k) f[0][k] = v[n][i][k] * fabsf(sc);
+        uint32_t w[1][1];
+        encode<1, 4, false>(a.dxq.type, f, sc < 0.0f, w);
+        if (r + i < nrows) store_codes<4>(a.dxq.q + (r0 + r + i) * a.dxq.ldq + (n ? a.cols : 0) + c0, c, ncols, w[0]);
       }
   }
   if (a.dxqt.q || a.yqt.q) {
     const amp_fp8_tiles o[3] = {a.dxqt, a.dxqt, a.yqt};
     const int64_t first[3] = {c0, a.cols + c0, c0};
-    store_regions_t<3>(l, o, first, r0, a.rows, static_cast<int>(a.cols - c0 < kTileK ? a.cols - c0 : kTileK), v);
+    store_regions_t<3>(l, o, first, r0, a.rows, ncols, v);
   }
 }
 
@@ -232,38 +275,83 @@ int row_width(int64_t cols, int e) {
   return 32;
 }
 
-dim3 row_grid(int64_t rows, int64_t cols, int w, int e, int per) {
-  const int64_t x = (cols + w * e - 1) / (w * e);
-  int64_t y = (rows + per - 1) / per;
-  if (y > 65535) y = 65535;
-  return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
+// Calls f(first row, rows) for slices of at most `most` rows.
+template <typename F>
+hipError_t in_slices(int64_t rows, int64_t most, F f) {
+  for (int64_t r0 = 0; r0 < rows; r0 += most) {
+    f(r0, rows - r0 < most ? rows - r0 : most);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
+}
+
+constexpr int kGridY = 65535;
+
+template <int XT, int W, int R>
+hipError_t run_swiglu(const GateArgs& whole, hipStream_t s) {
+  constexpr int E = kVec<XT>, per = 256 / W * R;
+  const bool full = whole.cols % (W * E) == 0;
+  return in_slices(whole.rows, static_cast<int64_t>(kGridY) * per, [&](int64_t r0, int64_t rows) {
+    GateArgs a = whole;
+    a.rows = rows;
+    a.x = elem<XT>(a.x, r0 * a.ldx);
+    if (a.y) a.y = static_cast<uint8_t*>(a.y) + r0 * a.ldy * dtype_bytes(a.yt);
+    if (a.yq.q) { a.yq.q += r0 * a.yq.ldq; a.yq.s += r0; }
+    if (a.ck.q) { a.ck.q += r0 * a.ck.ldq; a.ck.s += r0; }
+    const dim3 grid(static_cast<unsigned>((a.cols + W * E - 1) / (W * E)), static_cast<unsigned>((rows + per - 1) / per));
+    if (full) swiglu_rows<XT, W, R, true><<<grid, 256, 0, s>>>(a);
+    else swiglu_rows<XT, W, R, false><<<grid, 256, 0, s>>>(a);
+  });
 }
 
 template <int XT>
 hipError_t dispatch_swiglu(const GateArgs& a, hipStream_t s) {
-  constexpr int E = kVec<XT>, R = 2;
-  const int w = row_width(a.cols, E);
-  const dim3 grid = row_grid(a.rows, a.cols, w, E, 256 / w * R);
-  if (w == 256) swiglu_rows<XT, 256, R><<<grid, 256, 0, s>>>(a);
-  else if (w == 64) swiglu_rows<XT, 64, R><<<grid, 256, 0, s>>>(a);
-  else swiglu_rows<XT, 32, R><<<grid, 256, 0, s>>>(a);
-  return hipGetLastError();
+  switch (row_width(a.cols, kVec<XT>)) {
+    case 256: return run_swiglu<XT, 256, 2>(a, s);
+    case 64: return run_swiglu<XT, 64, 2>(a, s);
+    default: return run_swiglu<XT, 32, 2>(a, s);
+  }
+}
+
+template <int XT, bool CK, int W, int R>
+hipError_t run_swiglu_back(const GateArgs& whole, hipStream_t s) {
+  constexpr int E = kVec<XT>, per = 256 / W * R;
+  const bool full = whole.cols % (W * E) == 0;
+  return in_slices(whole.rows, static_cast<int64_t>(kGridY) * per, [&](int64_t r0, int64_t rows) {
+    GateArgs a = whole;
+    a.rows = rows;
+    a.dy = elem<XT>(a.dy, r0 * a.lddy);
+    a.y = elem<XT>(a.y, r0 * a.ldy);
+    if (CK) { a.ck.q += r0 * a.ck.ldq; a.ck.s += r0; }
+    else a.x = elem<XT>(a.x, r0 * a.ldx);
+    const dim3 grid(static_cast<unsigned>((a.cols + W * E - 1) / (W * E)), static_cast<unsigned>((rows + per - 1) / per));
+    if (full) swiglu_back_rows<XT, CK, W, R, true><<<grid, 256, 0, s>>>(a);
+    else swiglu_back_rows<XT, CK, W, R, false><<<grid, 256, 0, s>>>(a);
+  });
 }
 
 template <int XT, bool CK>
-hipError_t dispatch_swiglu_back(const GateArgs& a, hipStream_t s) {
-  if (a.dxq.q || a.dxqt.q || a.yqt.q) {
-    const dim3 grid(static_cast<unsigned>((a.cols + kTileK - 1) / kTileK), static_cast<unsigned>((a.rows + kTileK - 1) / kTileK));
-    swiglu_back_region<XT, CK><<<grid, kRegThreads, 0, s>>>(a);
-    return hipGetLastError();
+hipError_t dispatch_swiglu_back(const GateArgs& whole, hipStream_t s) {
+  if (whole.dxq.q || whole.dxqt.q || whole.yqt.q) {
+    return in_slices(whole.rows, static_cast<int64_t>(kGridY) * kTileK, [&](int64_t r0, int64_t rows) {
+      GateArgs a = whole;
+      a.rows = rows;
+      a.dy = elem<XT>(a.dy, r0 * a.lddy);
+      if (a.y) a.y = elem<XT>(a.y, r0 * a.ldy);
+      if (CK) { a.ck.q += r0 * a.ck.ldq; a.ck.s += r0; }
+      else a.x = elem<XT>(a.x, r0 * a.ldx);
+      if (a.dxq.q) { a.dxq.q += r0 * a.dxq.ldq; a.dxq.s += r0; }
+      if (a.dxqt.q) { a.dxqt.q += r0; a.dxqt.s += r0 / kTileK * a.dxqt.lds; }
+      if (a.yqt.q) { a.yqt.q += r0; a.yqt.s += r0 / kTileK * a.yqt.lds; }
+      const dim3 grid(static_cast<unsigned>((a.cols + kTileK - 1) / kTileK), static_cast<unsigned>((rows + kTileK - 1) / kTileK));
+      swiglu_back_region<XT, CK><<<grid, kRegThreads, 0, s>>>(a);
+    });
   }
-  constexpr int E = kVec<XT>, R = 2;
-  const int w = row_width(a.cols, E);
-  const dim3 grid = row_grid(a.rows, a.cols, w, E, 256 / w * R);
-  if (w == 256) swiglu_back_rows<XT, CK, 256, R><<<grid, 256, 0, s>>>(a);
-  else if (w == 64) swiglu_back_rows<XT, CK, 64, R><<<grid, 256, 0, s>>>(a);
-  else swiglu_back_rows<XT, CK, 32, R><<<grid, 256, 0, s>>>(a);
-  return hipGetLastError();
+  switch (row_width(whole.cols, kVec<XT>)) {
+    case 256: return run_swiglu_back<XT, CK, 256, 2>(whole, s);
+    case 64: return run_swiglu_back<XT, CK, 64, 2>(whole, s);
+    default: return run_swiglu_back<XT, CK, 32, 2>(whole, s);
+  }
 }
 
 template <int XT>

@@ -5,6 +5,11 @@
 // Rows need no alignment: gfx950 loads and stores dwords and wider at any
 // byte address, so a row of odd length costs extra cache lines, not another
 // code path.  Only a row's last, partial vector goes element by element.
+//
+// The operators are HBM-bound only as long as the vector ALUs keep up (about
+// 50 operations per element at one 16-bit stream's rate), so addresses are a
+// wave-uniform row pointer plus a 32-bit offset, and a tile's two divisions
+// are shared out over the lanes of a quad.
 #pragma once
 #include "common.hpp"
 #include "formats.hpp"
@@ -20,25 +25,63 @@ typedef uint32_t u32_any __attribute__((aligned(1)));
 // Elements of a 16-byte vector of an input type; a 1x128 tile is 128 / kVec
 // adjacent lanes.
 template <int XT> constexpr int kVec = XT == AMP_F32 ? 4 : 8;
+template <int XT> constexpr int kBytes = XT == AMP_F32 ? 4 : 2;
 
-// One vector of row `p` from column c on; columns past `cols` read as zero.
+// p advanced by i elements of type XT.
 template <int XT>
-__device__ __forceinline__ u32x4 load_vec(const void* p, int64_t c, int64_t cols) {
+__host__ __device__ __forceinline__ const void* elem(const void* p, int64_t i) { return static_cast<const uint8_t*>(p) + i * kBytes<XT>; }
+template <int XT>
+__host__ __device__ __forceinline__ void* elem(void* p, int64_t i) { return static_cast<uint8_t*>(p) + i * kBytes<XT>; }
+// p advanced by i elements of the run-time type t.
+__device__ __forceinline__ const void* elem_of(int t, const void* p, int64_t i) {
+  return static_cast<const uint8_t*>(p) + i * (t == AMP_F32 ? 4 : 2);
+}
+
+// The number of columns left, as the 32-bit bound that the helpers take (they
+// see at most one chunk of a row).
+__device__ __forceinline__ int left(int64_t n) { return n > (1 << 24) ? 1 << 24 : static_cast<int>(n); }
+
+// Loads and stores of 16, 8 and 4 bytes at p + off, of any alignment (the
+// under-aligned types are named in the casts: as template arguments they
+// would lose the attribute).
+__device__ __forceinline__ const uint8_t* at(const void* p, uint32_t off) { return static_cast<const uint8_t*>(p) + off; }
+__device__ __forceinline__ uint8_t* at(void* p, uint32_t off) { return static_cast<uint8_t*>(p) + off; }
+__device__ __forceinline__ u32x4 ld16(const void* p, uint32_t off) { return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(at(p, off))); }
+__device__ __forceinline__ u32x2 ld8(const void* p, uint32_t off) { return __builtin_nontemporal_load(reinterpret_cast<const u32x2_any*>(at(p, off))); }
+__device__ __forceinline__ uint32_t ld4(const void* p, uint32_t off) { return __builtin_nontemporal_load(reinterpret_cast<const u32_any*>(at(p, off))); }
+__device__ __forceinline__ void st16(void* p, uint32_t off, u32x4 v) { __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(at(p, off))); }
+__device__ __forceinline__ void st8(void* p, uint32_t off, u32x2 v) { __builtin_nontemporal_store(v, reinterpret_cast<u32x2_any*>(at(p, off))); }
+__device__ __forceinline__ void st4(void* p, uint32_t off, uint32_t v) { __builtin_nontemporal_store(v, reinterpret_cast<u32_any*>(at(p, off))); }
+
+// The 16 bytes of w moved down by `bytes` (1..15), zeros moved in: a row's
+// last, partial vector comes from a whole one that ends with the row (one
+// load; a load per element would wait for each).
+__device__ __forceinline__ u32x4 drop_low(u32x4 w, int bytes) {
+  if (bytes & 8) w = u32x4{w[2], w[3], 0u, 0u};
+  if (bytes & 4) w = u32x4{w[1], w[2], w[3], 0u};
+  const int s = 8 * (bytes & 3);
+  return u32x4{__builtin_amdgcn_alignbit(w[1], w[0], s), __builtin_amdgcn_alignbit(w[2], w[1], s),
+               __builtin_amdgcn_alignbit(w[3], w[2], s), w[3] >> s};
+}
+
+// One vector at column c of the n columns at p; columns from n on read as
+// zero.  FULL: the caller knows that the vector lies within the row (each
+// bound that is checked is a branch, and a row has dozens of vectors).
+// Non-temporal: these tensors are read once.
+template <int XT, bool FULL = false>
+__device__ __forceinline__ u32x4 load_vec(const void* p, int c, int n) {
   constexpr int E = kVec<XT>;
+  const uint32_t off = static_cast<uint32_t>(c) * kBytes<XT>;
+  if (FULL || c + E <= n) return ld16(p, off);
   u32x4 w = {0u, 0u, 0u, 0u};
-  if constexpr (XT == AMP_F32) {
-    const float* x = static_cast<const float*>(p) + c;
-    if (c + E <= cols) return *reinterpret_cast<const u32x4_any*>(x);
+  if (c >= n) return w;
+  if (n >= E) return drop_low(ld16(p, static_cast<uint32_t>(n - E) * kBytes<XT>), (c + E - n) * kBytes<XT>);
 #pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (c + k < cols) w[k] = fbits(x[k]);
-  } else {
-    const uint16_t* x = static_cast<const uint16_t*>(p) + c;
-    if (c + E <= cols) return *reinterpret_cast<const u32x4_any*>(x);
-#pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (c + k < cols) w[k / 2] |= static_cast<uint32_t>(x[k]) << (16 * (k & 1));
-  }
+  for (int k = 0; k < E; ++k)   // a row shorter than one vector
+    if (c + k < n) {
+      if constexpr (XT == AMP_F32) w[k] = static_cast<const uint32_t*>(p)[c + k];
+      else w[k / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[c + k]) << (16 * (k & 1));
+    }
   return w;
 }
 
@@ -56,6 +99,17 @@ __device__ __forceinline__ void widen(u32x4 w, float (&v)[kVec<XT>]) {
   }
 }
 
+// Two values rounded to 16 bits, nearest even (a NaN stays one; its payload
+// is the hardware's).
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack16(bool bf16, float a, float b) {
+  const f32x2 v = {a, b};
+  return bf16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2))
+              : __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+}
+
 // Values rounded to XT and packed as load_vec returns them.
 template <int XT>
 __device__ __forceinline__ u32x4 narrow(const float (&v)[kVec<XT>]) {
@@ -63,64 +117,82 @@ __device__ __forceinline__ u32x4 narrow(const float (&v)[kVec<XT>]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if constexpr (XT == AMP_F32) w[k] = fbits(v[k]);
-    else if constexpr (XT == AMP_BF16) w[k] = f32_to_bf16(v[2 * k]) | (f32_to_bf16(v[2 * k + 1]) << 16);
-    else w[k] = f32_to_f16(v[2 * k]) | (f32_to_f16(v[2 * k + 1]) << 16);
+    else w[k] = pack16(XT == AMP_BF16, v[2 * k], v[2 * k + 1]);
   }
   return w;
 }
 
-template <int XT>
-__device__ __forceinline__ void store_vec(void* p, int64_t c, int64_t cols, u32x4 w) {
-  constexpr int E = kVec<XT>;
-  if constexpr (XT == AMP_F32) {
-    float* x = static_cast<float*>(p) + c;
-    if (c + E <= cols) { *reinterpret_cast<u32x4_any*>(x) = w; return; }
-#pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (c + k < cols) x[k] = bitsf(w[k]);
+// W 32-bit words holding 2 W 16-bit elements, to column c of the n at p.
+template <int W, bool FULL = false>
+__device__ __forceinline__ void store16(void* p, int c, int n, const uint32_t (&h)[W]) {
+  if (FULL || c + 2 * W <= n) {
+    if constexpr (W == 4) st16(p, 2u * c, u32x4{h[0], h[1], h[2], h[3]});
+    else st8(p, 2u * c, u32x2{h[0], h[1]});
   } else {
-    uint16_t* x = static_cast<uint16_t*>(p) + c;
-    if (c + E <= cols) { *reinterpret_cast<u32x4_any*>(x) = w; return; }
 #pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (c + k < cols) x[k] = static_cast<uint16_t>(w[k / 2] >> (16 * (k & 1)));
+    for (int k = 0; k < 2 * W; ++k)
+      if (c + k < n) static_cast<uint16_t*>(p)[c + k] = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
   }
 }
 
-// E per-column factors of type ct in {F32, F16, BF16} (p NULL: 1).
-template <int E>
-__device__ __forceinline__ void load_cols(const void* p, int ct, int64_t c, int64_t cols, float (&v)[E]) {
+template <int XT, bool FULL = false>
+__device__ __forceinline__ void store_vec(void* p, int c, int n, u32x4 w) {
+  if constexpr (XT == AMP_F32) {
+    if (FULL || c + 4 <= n) {
+      st16(p, 4u * c, w);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (c + k < n) static_cast<float*>(p)[c + k] = bitsf(w[k]);
+    }
+  } else {
+    const uint32_t h[4] = {w[0], w[1], w[2], w[3]};
+    store16<4, FULL>(p, c, n, h);
+  }
+}
+
+// E per-column factors of type ct in {F32, F16, BF16} (p NULL: 1), read by
+// every row and so through the caches.
+template <int E, bool FULL = false>
+__device__ __forceinline__ void load_cols(const void* p, int ct, int c, int n, float (&v)[E]) {
   if (p == nullptr) {
 #pragma unroll
     for (int k = 0; k < E; ++k) v[k] = 1.0f;
   } else if (ct == AMP_F32) {
-    const float* x = static_cast<const float*>(p) + c;
-    if (c + E <= cols) {
+    const float* x = static_cast<const float*>(p);
+    if (FULL || c + E <= n) {
 #pragma unroll
       for (int q = 0; q < E / 4; ++q) {
-        const u32x4 w = *reinterpret_cast<const u32x4_any*>(x + 4 * q);
+        const u32x4 w = *reinterpret_cast<const u32x4_any*>(x + static_cast<uint32_t>(c + 4 * q));
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[4 * q + k] = bitsf(w[k]);
       }
     } else {
+      // element loads with the index held inside the row: no branch, no wait between them
 #pragma unroll
-      for (int k = 0; k < E; ++k) v[k] = c + k < cols ? x[k] : 0.0f;
+      for (int k = 0; k < E; ++k) {
+        const float t = x[c + k < n ? c + k : n - 1];
+        v[k] = c + k < n ? t : 0.0f;
+      }
     }
   } else {
-    const uint16_t* x = static_cast<const uint16_t*>(p) + c;
+    const uint16_t* x = static_cast<const uint16_t*>(p);
     uint32_t h[E / 2];
-    if (c + E <= cols) {
+    if (FULL || c + E <= n) {
+      if constexpr (E == 8) {
+        const u32x4 w = *reinterpret_cast<const u32x4_any*>(x + static_cast<uint32_t>(c));
 #pragma unroll
-      for (int q = 0; q < E / 4; ++q) {
-        const u32x2 w = *reinterpret_cast<const u32x2_any*>(x + 4 * q);
-        h[2 * q] = w.x;
-        h[2 * q + 1] = w.y;
+        for (int k = 0; k < 4; ++k) h[k] = w[k];
+      } else {
+        const u32x2 w = *reinterpret_cast<const u32x2_any*>(x + static_cast<uint32_t>(c));
+        h[0] = w.x;
+        h[1] = w.y;
       }
     } else {
 #pragma unroll
       for (int q = 0; q < E / 2; ++q) {
-        h[q] = c + 2 * q < cols ? x[2 * q] : 0u;
-        if (c + 2 * q + 1 < cols) h[q] |= static_cast<uint32_t>(x[2 * q + 1]) << 16;
+        const uint32_t lo = x[c + 2 * q < n ? c + 2 * q : n - 1], hi = x[c + 2 * q + 1 < n ? c + 2 * q + 1 : n - 1];
+        h[q] = (c + 2 * q < n ? lo : 0u) | (c + 2 * q + 1 < n ? hi << 16 : 0u);
       }
     }
     if (ct == AMP_BF16) {
@@ -149,74 +221,98 @@ __device__ __forceinline__ float abs_max(float m, const float (&v)[E]) {
 // Bits of an abs_max result without a NaN's sign: their unsigned order is the
 // order of the values, NaN above infinity.
 __device__ __forceinline__ uint32_t mag(float m) { return fbits(m) & 0x7fffffffu; }
+constexpr uint32_t kInfBits = 0x7f800000u;
 
-// Codes of E scaled values, four to a word, as f32_to_e4m3 / f32_to_e5m2
-// would round each: `special` says that one of them may be NaN.  Without one
-// the clamp and half a conversion instruction per element are all there is.
-template <int E>
-__device__ __forceinline__ void encode(int yt, const float (&t)[E], bool special, uint32_t (&w)[E / 4]) {
-  if (special) {
+// Codes of N x E scaled values, four to a word, each as f32_to_e4m3 /
+// f32_to_e5m2 would round it.  `special`, for any lane of the wave, says that
+// one of the lane's values may be NaN or infinite (codes 0x7F and +-max).
+// CLAMP: they may lie beyond the format's range; values scaled by their own
+// tile's amax do not: they reach at most fp8_max (1 + 2^-22), which the
+// conversion rounds to fp8_max (measured).
+template <int N, int E, bool CLAMP>
+__device__ __forceinline__ void encode(int yt, const float (&t)[N][E], bool special, uint32_t (&w)[N][E / 4]) {
+  if (__builtin_amdgcn_ballot_w64(special)) {
 #pragma unroll
-    for (int q = 0; q < E / 4; ++q) {
-      w[q] = 0;
+    for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[q] |= (yt == AMP_E4M3 ? f32_to_e4m3(t[4 * q + k]) : f32_to_e5m2(t[4 * q + k])) << (8 * k);
-    }
+      for (int q = 0; q < E / 4; ++q) {
+        w[n][q] = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          w[n][q] |= (yt == AMP_E4M3 ? f32_to_e4m3(t[n][4 * q + k]) : f32_to_e5m2(t[n][4 * q + k])) << (8 * k);
+      }
     return;
   }
   const float m = fp8_max(yt);
+  auto y = [&](int n, int k) __attribute__((always_inline)) {
+    return CLAMP ? __builtin_amdgcn_fmed3f(t[n][k], -m, m) : t[n][k];
+  };
+  if (yt == AMP_E4M3) {
 #pragma unroll
-  for (int q = 0; q < E / 4; ++q) {
-    float y[4];
+    for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int k = 0; k < 4; ++k) y[k] = __builtin_amdgcn_fmed3f(t[4 * q + k], -m, m);
-    if (yt == AMP_E4M3) {
-      const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-      w[q] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], lo, true));
-    } else {
-      const int lo = __builtin_amdgcn_cvt_pk_bf8_f32(y[0], y[1], 0, false);
-      w[q] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_bf8_f32(y[2], y[3], lo, true));
-    }
+      for (int q = 0; q < E; q += 4) {
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y(n, q), y(n, q + 1), 0, false);
+        w[n][q / 4] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(y(n, q + 2), y(n, q + 3), lo, true));
+      }
+  } else {
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int q = 0; q < E; q += 4) {
+        const int lo = __builtin_amdgcn_cvt_pk_bf8_f32(y(n, q), y(n, q + 1), 0, false);
+        w[n][q / 4] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_bf8_f32(y(n, q + 2), y(n, q + 3), lo, true));
+      }
   }
 }
 
-template <int E>
-__device__ __forceinline__ void store_codes(uint8_t* p, int64_t c, int64_t cols, const uint32_t (&w)[E / 4]) {
-  if (c + E <= cols) {
-    if constexpr (E == 8) {
-      u32x2 d = {w[0], w[1]};
-      *reinterpret_cast<u32x2_any*>(p + c) = d;
-    } else {
-      *reinterpret_cast<u32_any*>(p + c) = w[0];
-    }
+// E codes to column c of the n at p.
+template <int E, bool FULL = false>
+__device__ __forceinline__ void store_codes(uint8_t* p, int c, int n, const uint32_t (&w)[E / 4]) {
+  if (FULL || c + E <= n) {
+    if constexpr (E == 8) st8(p, c, u32x2{w[0], w[1]});
+    else st4(p, c, w[0]);
   } else {
 #pragma unroll
     for (int k = 0; k < E; ++k)
-      if (c + k < cols) p[c + k] = static_cast<uint8_t>(w[k / 4] >> (8 * (k & 3)));
+      if (c + k < n) p[c + k] = static_cast<uint8_t>(w[k / 4] >> (8 * (k & 3)));
   }
 }
 
-// Values of E codes from column c on; columns past `cols` read as zero.
-template <int E>
-__device__ __forceinline__ void load_codes(const uint8_t* p, int64_t c, int64_t cols, uint32_t (&w)[E / 4]) {
-  if (c + E <= cols) {
+// E codes from column c of the n at p; columns from n on read as zero.
+template <int E, bool FULL = false>
+__device__ __forceinline__ void load_codes(const uint8_t* p, int c, int n, uint32_t (&w)[E / 4]) {
+  if (FULL || c + E <= n) {
     if constexpr (E == 8) {
-      const u32x2 d = *reinterpret_cast<const u32x2_any*>(p + c);
+      const u32x2 d = ld8(p, c);
       w[0] = d.x;
       w[1] = d.y;
     } else {
-      w[0] = *reinterpret_cast<const u32_any*>(p + c);
+      w[0] = ld4(p, c);
     }
   } else {
 #pragma unroll
     for (int q = 0; q < E / 4; ++q) w[q] = 0;
+    if (c >= n) return;
+    if (n >= E) {   // as load_vec
+      const int s = 8 * (c + E - n);
+      if constexpr (E == 8) {
+        const u32x2 d = ld8(p, n - E);
+        const uint64_t v = ((static_cast<uint64_t>(d.y) << 32) | d.x) >> s;
+        w[0] = static_cast<uint32_t>(v);
+        w[1] = static_cast<uint32_t>(v >> 32);
+      } else {
+        w[0] = ld4(p, n - E) >> s;
+      }
+      return;
+    }
 #pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (c + k < cols) w[k / 4] |= static_cast<uint32_t>(p[c + k]) << (8 * (k & 3));
+    for (int k = 0; k < E; ++k)   // a row shorter than E
+      if (c + k < n) w[k / 4] |= static_cast<uint32_t>(p[c + k]) << (8 * (k & 3));
   }
 }
 
+// Values of E codes times `mul`.
 template <int E>
 __device__ __forceinline__ void decode(int xt, const uint32_t (&w)[E / 4], float mul, float (&v)[E]) {
 #pragma unroll
@@ -256,58 +352,92 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
   return v;
 }
 
-// Quantize one vector of a row in 1x128 tiles: the 128 / E lanes of a tile
-// call together (lanes past `cols` hold zeros), `blk` is the tile's index
-// along K in the scale array.
-template <int E>
-__device__ __forceinline__ void store_tile(const amp_fp8_tiles& o, int64_t row, int64_t c, int64_t c_end, int64_t blk,
-                                           bool live, const float (&v)[E]) {
-  const uint32_t am = group_max<kTileK / E>(mag(abs_max<E>(0.0f, v)));
-  const float sc = scale_of(am, fp8_max(o.type));
-  float t[E];
-#pragma unroll
-  for (int k = 0; k < E; ++k) t[k] = v[k] * sc;
-  uint32_t w[E / 4];
-  encode<E>(o.type, t, am >= 0x7f800000u, w);
-  if (live) {
-    store_codes<E>(o.q + row * o.ldq, c, c_end, w);
-    if (threadIdx.x % (kTileK / E) == 0 && c < c_end) o.s[blk * o.lds + row] = 1.0f / sc;
-  }
+// Value of lane K of the quad in all its lanes.
+template <int K>
+__device__ __forceinline__ float quad(float v) {
+  return bitsf(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(fbits(v)), K * 0x55, 0xf, 0xf, true)));
 }
 
-// One vector of a plain output: 16 bits, or FP8 of the values times `scale`.
-template <int E>
-__device__ __forceinline__ void store_plain(void* y, int yt, int64_t at, int64_t c, int64_t cols, float scale, float am,
-                                            const float (&v)[E]) {
-  if (yt == AMP_E4M3 || yt == AMP_E5M2) {
-    float t[E];
+// Scales of N <= 4 tiles whose maxima am[] every lane of the tiles' lane group
+// holds: lane k of each quad divides for tile k (two divisions for up to four
+// tiles, in place of two each).  Returns 1 / scale of tile lane % 4.
+template <int N>
+__device__ __forceinline__ float tile_scales(const uint32_t (&am)[N], float fmax, float (&sc)[N]) {
+  const int k = threadIdx.x & 3;
+  uint32_t m = am[0];
+  if constexpr (N > 1) m = k == 1 ? am[1] : m;
+  if constexpr (N > 2) m = k == 2 ? am[2] : m;
+  if constexpr (N > 3) m = k == 3 ? am[3] : m;
+  const float s = scale_of(m, fmax);
+  sc[0] = N > 1 ? quad<0>(s) : s;
+  if constexpr (N > 1) sc[1] = quad<1>(s);
+  if constexpr (N > 2) sc[2] = quad<2>(s);
+  if constexpr (N > 3) sc[3] = quad<3>(s);
+  return 1.0f / s;
+}
+
+// N vectors, `step` columns apart, of a plain output at p (its row): 16 bits,
+// or FP8, of the values times `scale`; `am` is their abs_max before.  A
+// product is NaN or infinite only with such a factor or by overflow, which the
+// FP8 clamp and the 16-bit rounding handle without the special path.
+template <int N, int E, bool FULL = false>
+__device__ __forceinline__ void store_plain(void* p, int yt, int c, int step, int n, bool live, float scale, float am,
+                                            const float (&v)[N][E]) {
+  const bool special = mag(am) >= kInfBits || mag(scale) >= kInfBits;
+  float t[N][E];
 #pragma unroll
-    for (int k = 0; k < E; ++k) t[k] = v[k] * scale;
-    uint32_t w[E / 4];
-    // inf * 0-like scales aside, a product is NaN only for a NaN or infinite factor
-    encode<E>(yt, t, mag(am) >= 0x7f800000u || mag(scale) >= 0x7f800000u, w);
-    store_codes<E>(static_cast<uint8_t*>(y) + at, c, cols, w);
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int e = 0; e < E; ++e) t[k][e] = v[k][e] * scale;
+  if (yt == AMP_E4M3 || yt == AMP_E5M2) {
+    uint32_t w[N][E / 4];
+    encode<N, E, true>(yt, t, special, w);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (live) store_codes<E, FULL>(static_cast<uint8_t*>(p), c + k * step, n, w[k]);
     return;
   }
-  uint32_t h[E / 2];
+  uint32_t h[N][E / 2];
+  if (__builtin_amdgcn_ballot_w64(special)) {
 #pragma unroll
-  for (int q = 0; q < E / 2; ++q) {
-    const float a = v[2 * q] * scale, b = v[2 * q + 1] * scale;
-    h[q] = yt == AMP_BF16 ? f32_to_bf16(a) | (f32_to_bf16(b) << 16) : f32_to_f16(a) | (f32_to_f16(b) << 16);
-  }
-  uint16_t* p = static_cast<uint16_t*>(y) + at + c;
-  if (c + E <= cols) {
-    if constexpr (E == 8) {
-      const u32x4 w = {h[0], h[1], h[2], h[3]};
-      *reinterpret_cast<u32x4_any*>(p) = w;
-    } else {
-      const u32x2 w = {h[0], h[1]};
-      *reinterpret_cast<u32x2_any*>(p) = w;
-    }
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int q = 0; q < E / 2; ++q)
+        h[k][q] = yt == AMP_BF16 ? f32_to_bf16(t[k][2 * q]) | (f32_to_bf16(t[k][2 * q + 1]) << 16)
+                                 : f32_to_f16(t[k][2 * q]) | (f32_to_f16(t[k][2 * q + 1]) << 16);
   } else {
 #pragma unroll
-    for (int k = 0; k < E; ++k)
-      if (c + k < cols) p[k] = static_cast<uint16_t>(h[k / 2] >> (16 * (k & 1)));
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int q = 0; q < E / 2; ++q) h[k][q] = pack16(yt == AMP_BF16, t[k][2 * q], t[k][2 * q + 1]);
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (live) store16<E / 2, FULL>(p, c + k * step, n, h[k]);
+}
+
+// ---- amax of an output ------------------------------------------------------
+
+// A value that *d_amax holds or exceeds from now on, read ahead of the work
+// so that its latency is hidden (0 without d_amax).
+__device__ __forceinline__ uint32_t amax_seen(const float* d_amax) {
+  return d_amax ? __hip_atomic_load(reinterpret_cast<const uint32_t*>(d_amax), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP) : 0u;
+}
+
+// Maximum over a block of at most 16 waves into *d_amax; blocks that do not
+// exceed what they saw at their start leave without touching it.
+__device__ __forceinline__ void block_amax(float am, uint32_t seen, uint32_t* red, float* d_amax) {
+  uint32_t m = mag(am);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(m), off, kWave));
+    m = m > o ? m : o;
+  }
+  if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int k = 1; k < static_cast<int>(blockDim.x) / kWave; ++k) m = m > red[k] ? m : red[k];
+    if (canon_amax(m) > seen) amax_update(d_amax, m);
   }
 }
 
@@ -344,6 +474,7 @@ __device__ __forceinline__ void store_regions_t(RegLds<N>& l, const amp_fp8_tile
                                                 int64_t row0, int64_t rows, int ncols,
                                                 const float (&v)[N][kRegRows][kRegCols]) {
   const int t = threadIdx.x, cg = t % 32, rg = t / 32;
+  const int nrows = left(rows - row0);
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     u32x4 m;
@@ -368,7 +499,7 @@ __device__ __forceinline__ void store_regions_t(RegLds<N>& l, const amp_fp8_tile
       if (k != n) continue;
       const float sc = scale_of(m, fp8_max(o[k].type));
       // the sign carries whether the tile holds a NaN or infinity
-      l.scale[k][c] = m >= 0x7f800000u ? -sc : sc;
+      l.scale[k][c] = m >= kInfBits ? -sc : sc;
       if (o[k].q && c < ncols) o[k].s[row0 / kTileK * o[k].lds + col0[k] + c] = 1.0f / sc;
     }
   }
@@ -379,12 +510,12 @@ __device__ __forceinline__ void store_regions_t(RegLds<N>& l, const amp_fp8_tile
     const f32x4 sc = *reinterpret_cast<const f32x4*>(&l.scale[n][4 * cg]);
 #pragma unroll
     for (int j = 0; j < kRegCols; ++j) {
-      float f[kRegRows];
+      float f[1][kRegRows];
 #pragma unroll
-      for (int i = 0; i < kRegRows; ++i) f[i] = v[n][i][j] * fabsf(sc[j]);
-      uint32_t w[2];
-      encode<kRegRows>(o[n].type, f, sc[j] < 0.0f, w);
-      const u32x2 d = {w[0], w[1]};
+      for (int i = 0; i < kRegRows; ++i) f[0][i] = v[n][i][j] * fabsf(sc[j]);
+      uint32_t w[1][2];
+      encode<1, kRegRows, false>(o[n].type, f, sc[j] < 0.0f, w);
+      const u32x2 d = {w[0][0], w[0][1]};
       *reinterpret_cast<u32x2*>(&l.codes[n][reg_at(4 * cg + j, rg)]) = d;
     }
   }
@@ -397,13 +528,13 @@ __device__ __forceinline__ void store_regions_t(RegLds<N>& l, const amp_fp8_tile
       const int c = it * 64 + t / 8, b = t % 8 * 16;
       if (c >= ncols) continue;
       const u32x4 w = *reinterpret_cast<const u32x4*>(&l.codes[n][reg_at(c, b / 8)]);
-      uint8_t* p = o[n].q + (col0[n] + c) * o[n].ldq + row0 + b;
-      if (row0 + b + 16 <= rows) {
-        *reinterpret_cast<u32x4_any*>(p) = w;
+      uint8_t* p = o[n].q + (col0[n] + c) * o[n].ldq + row0;
+      if (b + 16 <= nrows) {
+        st16(p, b, w);
       } else {
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          if (row0 + b + k < rows) p[k] = static_cast<uint8_t>(w[k / 4] >> (8 * (k & 3)));
+          if (b + k < nrows) p[b + k] = static_cast<uint8_t>(w[k / 4] >> (8 * (k & 3)));
       }
     }
   }

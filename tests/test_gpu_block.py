@@ -121,6 +121,15 @@ def test_norm_every_output(xt, rows, cols):
     ck.check(wh, 0.0, "checkpoint")
 
 
+@pytest.mark.parametrize("xt,rows,cols", [
+    (amp.BF16, 2, 512), (amp.BF16, 1030, 1536), (amp.F16, 1027, 1400), (amp.BF16, 1025, 5120), (amp.F32, 1024, 2560), (amp.BF16, 1024, 7167),
+    (amp.BF16, 2, 16384), (amp.F16, 2, 24576), (amp.BF16, 2, 32768), (amp.BF16, 2, 40960), (amp.F32, 2, 20480), (amp.BF16, 2, 49152),
+    (amp.F16, 2, 57344), (amp.BF16, 2, 65536), (amp.F32, 2, 32768), (amp.F32, 2, 30001)])
+def test_norm_in_every_row_layout(xt, rows, cols):
+    """One to eight vectors a thread, in 64 to 1024 threads, rows that fill them and rows that do not."""
+    test_norm_every_output(xt, rows, cols)
+
+
 @pytest.mark.parametrize("xt,cols", [(amp.BF16, 70003), (amp.F32, 33001), (amp.F16, 66000)])
 def test_norm_of_rows_longer_than_the_registers_hold(xt, cols):
     test_norm_every_output(xt, 3, cols)
@@ -243,7 +252,7 @@ def test_swiglu_of_extreme_and_non_finite_gates():
 @pytest.mark.parametrize("dt", TYPES)
 @pytest.mark.parametrize("saved", ["stored", "checkpoint"])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (3, 5), (2, 129), (700, 40), (40, 512), (5, 1000), (33, 2047), (3, 4096),
-                                       (4, 7001), (2, 20483), (2, 40003)])
+                                       (4, 7001), (2, 20483), (2, 40003), (19, 1024), (9, 2048), (3, 8192), (3, 16384), (2, 32768), (2, 4100)])
 def test_norm_backward(dt, saved, rows, cols):
     pad = 3 if rows % 2 else 8
     hv = loud(rows + cols, rows, cols)
