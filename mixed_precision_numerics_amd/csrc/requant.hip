@@ -18,35 +18,36 @@ struct RequantArgs {
 
 __global__ __launch_bounds__(kRegThreads) void requant_region(const RequantArgs a) {
   __shared__ RegLds<1> l;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kTileK, r0 = static_cast<int64_t>(blockIdx.y) * kTileK;
-  const int c = 4 * (threadIdx.x % 32), r = kRegRows * (threadIdx.x / 32);
-  const int ncols = left(a.cols - c0) < kTileK ? left(a.cols - c0) : kTileK, nrows = left(a.rows - r0);
-  const uint8_t* q = a.x.q + (r0 + r) * a.x.ldq + c0;
-  const float* s = a.x.s + c0 / kTileK * a.x.lds + r0 + r;
-  float v[1][kRegRows][kRegCols], col[4];
-  load_cols<4>(elem_of(a.ct, a.col, a.col ? c0 : 0), a.ct, c, ncols, col);
+  const Region g(a.rows, a.cols, false);
+  RegRaw<1> x;
+  float f[kRegRows], row[kRegRows], col[kRegCols], v[1][kRegRows][kRegCols];
 #pragma unroll
   for (int i = 0; i < kRegRows; ++i) {
-    uint32_t w[1] = {0u};
-    float f = 0.0f;
-    if (r + i < nrows) {
-      load_codes<4>(q + i * a.x.ldq, c, ncols, w);
-      f = s[i];
-    }
-    decode<4>(a.x.type, w, f, v[0][i]);
-    if (a.row) {
-      f = r + i < nrows ? a.row[r0 + r + i] : 0.0f;
+    const int64_t r = g.row(i);
+    x.load(g, i, a.x.q + r * a.x.ldq + g.c0);
+    f[i] = a.x.s[g.c0 / kTileK * a.x.lds + r];
+    row[i] = a.row ? a.row[r] : 1.0f;
+  }
+  load_cols<kRegCols>(a.col ? elem_of(a.ct, a.col, g.c0) : nullptr, a.ct, g.c(), g.ncols, col);
+  x.trim(g);
 #pragma unroll
-      for (int j = 0; j < kRegCols; ++j) v[0][i][j] *= f;
-    }
-    if (a.col) {
+  for (int i = 0; i < kRegRows; ++i) {
+    // past the end: zeros, which a scale or factor of infinity would make NaN
+    const bool in = g.r() + i < g.nrows;
+    decode<kRegCols>(a.x.type, x.w[i], in ? f[i] : 0.0f, v[0][i]);
+    if (a.row || a.col) {
+      const float r = in ? row[i] : 0.0f;
 #pragma unroll
-      for (int j = 0; j < kRegCols; ++j) v[0][i][j] *= col[j];
+      for (int j = 0; j < kRegCols; ++j) v[0][i][j] = v[0][i][j] * r * col[j];
     }
   }
   const amp_fp8_tiles o[1] = {a.qt};
-  const int64_t first[1] = {c0};
-  store_regions_t<1>(l, o, first, r0, a.rows, ncols, v);
+  const int64_t first[1] = {g.c0};
+  reg_maxima<1>(l, g, v);
+  __syncthreads();
+  reg_scales<1>(l, g, o, first);
+  __syncthreads();
+  reg_codes<1>(l, g, o, first, v);
 }
 
 }  // namespace

@@ -84,7 +84,7 @@ __device__ __forceinline__ float sum_squares(u32x4 w, float ss) {
 // tiles.  Lane k of a tile's lane group stores the scale of vector k's tile.
 template <int E, int N, bool FULL>
 __device__ __forceinline__ void store_tiles(const amp_fp8_tiles& o, int64_t row, int64_t c0, int c, int step, int n,
-                                            bool live, float (&v)[N][E]) {
+                                            bool live, const float (&v)[N][E]) {
   constexpr int G = kTileK / E;
   uint32_t m[N], top = 0, w[N][E / 4];
   float sc[N];
@@ -96,11 +96,7 @@ __device__ __forceinline__ void store_tiles(const amp_fp8_tiles& o, int64_t row,
   const float inv = tile_scales<N>(m, fp8_max(o.type), sc);
   const int mine = c / kTileK * kTileK + (threadIdx.x & 3) * step;   // where that tile begins
   if (threadIdx.x % G < N && (FULL || mine < n) && live) o.s[(c0 + mine) / kTileK * o.lds + row] = inv;
-#pragma unroll
-  for (int k = 0; k < N; ++k)
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[k][e] *= sc[k];
-  encode<N, E, false>(o.type, v, top >= kInfBits, w);
+  encode<N, E, false>(o.type, top >= kInfBits, w, [&](int k, int e) __attribute__((always_inline)) { return v[k][e] * sc[k]; });
   uint8_t* q = o.q + row * o.ldq + c0;
 #pragma unroll
   for (int k = 0; k < N; ++k)

@@ -42,7 +42,7 @@ __device__ __forceinline__ int64_t tile_of(int64_t c, int half, int64_t cols) {
 // tile's index along K.  Lane i of a tile's lane group stores row i's scale.
 template <int E, int R, bool FULL>
 __device__ __forceinline__ void store_row_tiles(const amp_fp8_tiles& o, int64_t row0, int S, int64_t rows, int64_t c0, int c,
-                                                int n, int64_t blk, float (&v)[R][E]) {
+                                                int n, int64_t blk, const float (&v)[R][E]) {
   constexpr int G = kTileK / E;
   uint32_t m[R], top = 0, w[R][E / 4];
   float sc[R];
@@ -54,11 +54,7 @@ __device__ __forceinline__ void store_row_tiles(const amp_fp8_tiles& o, int64_t 
   const float inv = tile_scales<R>(m, fp8_max(o.type), sc);
   const int64_t mine = row0 + (threadIdx.x & 3) * S;
   if (threadIdx.x % G < R && mine < rows && (FULL || c / kTileK * kTileK < n)) o.s[blk * o.lds + mine] = inv;
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-#pragma unroll
-    for (int k = 0; k < E; ++k) v[i][k] *= sc[i];
-  encode<R, E, false>(o.type, v, top >= kInfBits, w);
+  encode<R, E, false>(o.type, top >= kInfBits, w, [&](int i, int k) __attribute__((always_inline)) { return v[i][k] * sc[i]; });
 #pragma unroll
   for (int i = 0; i < R; ++i)
     if (row0 + i * S < rows) store_codes<E, FULL>(o.q + (row0 + i * S) * o.ldq + c0, c, n, w[i]);
@@ -175,93 +171,140 @@ __global__ __launch_bounds__(256) void swiglu_back_rows(const GateArgs a) {
   }
 }
 
-// Backward with FP8 operands: one 128x128 region of dy, g and u per block.
-// dg, du and y are formed once in registers and leave from there in every
-// form asked for: dx in dy's type, dx in row tiles (dgrad), dx^T and y^T in
-// tiles along the rows (wgrad).
+// Backward with FP8 operands: one 128x128 region of dy, g and u per block,
+// read once.  dg and du are formed in registers and leave from there in every
+// form asked for: dx in dy's type, dx in row tiles (dgrad), dx^T in tiles
+// along the rows (wgrad); then y is recomputed from g and u for y^T, so that
+// no more than two of the three are held at a time and two blocks share a CU.
 template <int XT, bool CK>
-__global__ __launch_bounds__(kRegThreads) void swiglu_back_region(const GateArgs a) {
-  __shared__ RegLds<3> l;
+__global__ __launch_bounds__(kRegThreads, 4) void swiglu_back_region(const GateArgs a) {
+  __shared__ RegLds<2> l;
   __shared__ uint32_t rmax[2][kTileK];
-  __shared__ float rscale[2][kTileK];
-  const int t = threadIdx.x, cg = t % 32, rg = t / 32;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kTileK, r0 = static_cast<int64_t>(blockIdx.y) * kTileK;
-  const int c = 4 * cg, r = kRegRows * rg;
-  const int ncols = left(a.cols - c0) < kTileK ? left(a.cols - c0) : kTileK, nrows = left(a.rows - r0);
-  float v[3][kRegRows][kRegCols];   // dg, du, y
+  __shared__ float rscale[2][kTileK], gscale[2][kTileK];
+  constexpr int GB = CK ? 1 : kBytes<XT>;
+  const Region g(a.rows, a.cols, true);
+  const int t = threadIdx.x;
+  RegRaw<kBytes<XT>> xd;
+  RegRaw<GB> xg, xu;
 #pragma unroll
   for (int i = 0; i < kRegRows; ++i) {
-    const int64_t row = r0 + r + i;
-    float g[4] = {}, u[4] = {}, dy[4] = {};
-    if (r + i < nrows) {
-      load_cols<4>(elem<XT>(a.dy, row * a.lddy + c0), XT, c, ncols, dy);
-      if constexpr (CK) {
-        uint32_t q[1];
-        load_codes<4>(a.ck.q + row * a.ck.ldq + c0, c, ncols, q);
-        decode<4>(a.ck.type, q, a.ck.s[tile_of(c0, 0, a.cols) * a.ck.lds + row], g);
-        load_codes<4>(a.ck.q + row * a.ck.ldq + a.cols + c0, c, ncols, q);
-        decode<4>(a.ck.type, q, a.ck.s[tile_of(c0, 1, a.cols) * a.ck.lds + row], u);
-      } else {
-        load_cols<4>(elem<XT>(a.x, row * a.ldx + c0), XT, c, ncols, g);
-        load_cols<4>(elem<XT>(a.x, row * a.ldx + a.cols + c0), XT, c, ncols, u);
+    const int64_t row = g.row(i);
+    xd.load(g, i, elem<XT>(a.dy, row * a.lddy + g.c0));
+    const uint8_t* p = CK ? a.ck.q + row * a.ck.ldq + g.c0 : static_cast<const uint8_t*>(elem<XT>(a.x, row * a.ldx + g.c0));
+    xg.load(g, i, p);
+    xu.load(g, i, p + a.cols * GB);
+  }
+  if constexpr (CK) {
+    if (t < 2 * kTileK) {
+      const int r = t % kTileK;   // 0 past the last row: the zeros there stay zeros
+      gscale[t / kTileK][r] = r < g.nrows ? a.ck.s[tile_of(g.c0, t / kTileK, a.cols) * a.ck.lds + g.r0 + r] : 0.0f;
+    }
+  }
+  xd.trim(g);
+  xg.trim(g);
+  xu.trim(g);
+  if constexpr (CK) __syncthreads();
+  auto gu = [&](int i, float (&vg)[kRegCols], float (&vu)[kRegCols]) __attribute__((always_inline)) {
+    if constexpr (CK) {
+      decode<kRegCols>(a.ck.type, xg.w[i], gscale[0][g.r() + i], vg);
+      decode<kRegCols>(a.ck.type, xu.w[i], gscale[1][g.r() + i], vu);
+    } else {
+      reg_values<XT>(xg.w[i], vg);
+      reg_values<XT>(xu.w[i], vu);
+    }
+  };
+  if (a.y || a.dxq.q || a.dxqt.q) {
+    float v[2][kRegRows][kRegCols];   // dg, du
+#pragma unroll
+    for (int i = 0; i < kRegRows; ++i) {
+      float vg[kRegCols], vu[kRegCols], dy[kRegCols];
+      gu(i, vg, vu);
+      reg_values<XT>(xd.w[i], dy);
+#pragma unroll
+      for (int k = 0; k < kRegCols; ++k) {
+        const Gate p = gate(vg[k]);
+        const float d = dy[k] * p.s;
+        v[0][i][k] = d * vu[k] * (1.0f + vg[k] * p.om);
+        v[1][i][k] = d * vg[k];
       }
     }
+    if (a.y) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const Gate p = gate(g[k]);
-      const float d = dy[k] * p.s, gu = g[k] * p.s;
-      v[0][i][k] = d * u[k] * (1.0f + g[k] * p.om);
-      v[1][i][k] = d * g[k];
-      v[2][i][k] = gu * u[k];
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < kRegRows; ++i) {
+          if (g.r() + i >= g.nrows) continue;
+          void* p = elem<XT>(a.y, g.row(i) * a.ldy + (n ? a.cols : 0) + g.c0);
+          constexpr int E = kVec<XT>;
+#pragma unroll
+          for (int q = 0; q < kRegCols / E; ++q)
+            store_vec<XT>(p, g.c() + q * E, g.ncols, narrow<XT>(reinterpret_cast<const float(&)[E]>(v[n][i][q * E])));
+        }
     }
-    if (a.y && r + i < nrows) {
+    const amp_fp8_tiles o[2] = {a.dxqt, a.dxqt};
+    const int64_t first[2] = {g.c0, a.cols + g.c0};
+    if (a.dxq.q) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < kRegRows; ++i) {
+          const uint32_t m = group_max<16>(mag(abs_max<kRegCols>(0.0f, v[n][i])));
+          if (t % 16 == 0) rmax[n][g.r() + i] = m;
+        }
+    }
+    if (a.dxqt.q) reg_maxima<2>(l, g, v);
+    __syncthreads();
+    if (a.dxqt.q) reg_scales<2>(l, g, o, first);
+    if (a.dxq.q && t >= 2 * kTileK) {
+      const int n = (t - 2 * kTileK) / kTileK, r = t % kTileK;
+      const uint32_t m = rmax[n][r];
+      const float sc = scale_of(m, fp8_max(a.dxq.type));
+      rscale[n][r] = m >= kInfBits ? -sc : sc;   // sign: the tile holds a NaN or infinity
+      if (r < g.nrows) a.dxq.s[tile_of(g.c0, n, a.cols) * a.dxq.lds + g.r0 + r] = 1.0f / sc;
+    }
+    __syncthreads();
+    if (a.dxq.q) {
 #pragma unroll
       for (int n = 0; n < 2; ++n) {
-        void* p = elem<XT>(a.y, row * a.ldy + (n ? a.cols : 0) + c0);
-        const float(&f)[4] = v[n][i];
-        if constexpr (XT == AMP_F32) {
-          store_vec<AMP_F32>(p, c, ncols, narrow<AMP_F32>(f));
-        } else {
-          const uint32_t h[2] = {pack16(XT == AMP_BF16, f[0], f[1]), pack16(XT == AMP_BF16, f[2], f[3])};
-          store16<2>(p, c, ncols, h);
+        float sc[kRegRows];
+        uint32_t w[kRegRows][2];
+        bool special = false;
+#pragma unroll
+        for (int i = 0; i < kRegRows; ++i) {
+          sc[i] = rscale[n][g.r() + i];
+          special |= sc[i] < 0.0f;
         }
+        encode<kRegRows, kRegCols, false>(a.dxq.type, special, w,
+                                          [&](int i, int k) __attribute__((always_inline)) { return v[n][i][k] * fabsf(sc[i]); });
+        // cols is a multiple of 128 here
+#pragma unroll
+        for (int i = 0; i < kRegRows; ++i)
+          if (g.r() + i < g.nrows)
+            *reinterpret_cast<u32x2_any*>(a.dxq.q + g.row(i) * a.dxq.ldq + (n ? a.cols : 0) + g.c0 + g.c()) = u32x2{w[i][0], w[i][1]};
       }
     }
-  }
-  if (a.dxq.q) {
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int i = 0; i < kRegRows; ++i) {
-        const uint32_t m = group_max<32>(mag(abs_max<4>(0.0f, v[n][i])));
-        if (cg == 0) rmax[n][r + i] = m;
-      }
-    __syncthreads();
-    if (t < 2 * kTileK) {
-      const int n = t / kTileK, i = t % kTileK;
-      const uint32_t m = rmax[n][i];
-      const float sc = scale_of(m, fp8_max(a.dxq.type));
-      rscale[n][i] = m >= kInfBits ? -sc : sc;   // sign: the tile holds a NaN or infinity
-      if (i < nrows) a.dxq.s[tile_of(c0, n, a.cols) * a.dxq.lds + r0 + i] = 1.0f / sc;
+    if (a.dxqt.q) {
+      reg_codes<2>(l, g, o, first, v);
+      if (a.yqt.q) __syncthreads();
     }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int i = 0; i < kRegRows; ++i) {
-        const float sc = rscale[n][r + i];
-        float f[1][4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) f[0][k] = v[n][i][k] * fabsf(sc);
-        uint32_t w[1][1];
-        encode<1, 4, false>(a.dxq.type, f, sc < 0.0f, w);
-        if (r + i < nrows) store_codes<4>(a.dxq.q + (r0 + r + i) * a.dxq.ldq + (n ? a.cols : 0) + c0, c, ncols, w[0]);
-      }
   }
-  if (a.dxqt.q || a.yqt.q) {
-    const amp_fp8_tiles o[3] = {a.dxqt, a.dxqt, a.yqt};
-    const int64_t first[3] = {c0, a.cols + c0, c0};
-    store_regions_t<3>(l, o, first, r0, a.rows, ncols, v);
+  if (a.yqt.q) {
+    float v[1][kRegRows][kRegCols];
+#pragma unroll
+    for (int i = 0; i < kRegRows; ++i) {
+      float vg[kRegCols], vu[kRegCols];
+      gu(i, vg, vu);
+#pragma unroll
+      for (int k = 0; k < kRegCols; ++k) v[0][i][k] = vg[k] * gate(vg[k]).s * vu[k];
+    }
+    const amp_fp8_tiles o[1] = {a.yqt};
+    const int64_t first[1] = {g.c0};
+    RegLds<1>& l1 = reinterpret_cast<RegLds<1>&>(l);
+    reg_maxima<1>(l1, g, v);
+    __syncthreads();
+    reg_scales<1>(l1, g, o, first);
+    __syncthreads();
+    reg_codes<1>(l1, g, o, first, v);
   }
 }
 

@@ -223,47 +223,60 @@ __device__ __forceinline__ float abs_max(float m, const float (&v)[E]) {
 __device__ __forceinline__ uint32_t mag(float m) { return fbits(m) & 0x7fffffffu; }
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-// Codes of N x E scaled values, four to a word, each as f32_to_e4m3 /
-// f32_to_e5m2 would round it.  `special`, for any lane of the wave, says that
-// one of the lane's values may be NaN or infinite (codes 0x7F and +-max).
-// CLAMP: they may lie beyond the format's range; values scaled by their own
+// Codes of the N x E values val(n, k), four to a word.
+template <int YT, int N, int E, typename F>
+__device__ __forceinline__ void convert(uint32_t (&w)[N][E / 4], F val) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int q = 0; q < E; q += 4) {
+      if constexpr (YT == AMP_E4M3) {
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(val(n, q), val(n, q + 1), 0, false);
+        w[n][q / 4] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(val(n, q + 2), val(n, q + 3), lo, true));
+      } else {
+        const int lo = __builtin_amdgcn_cvt_pk_bf8_f32(val(n, q), val(n, q + 1), 0, false);
+        w[n][q / 4] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_bf8_f32(val(n, q + 2), val(n, q + 3), lo, true));
+      }
+    }
+}
+
+// Four codes with every NaN, whatever its sign and payload, as 0x7F: the
+// magnitudes above the format's largest (and, in E5M2, above infinity's 0x7C)
+// carry into the sign's place when the distance to 0x80 is added.
+template <int YT>
+__device__ __forceinline__ uint32_t canon_nan(uint32_t w) {
+  const uint32_t nan = ((w & 0x7f7f7f7fu) + (YT == AMP_E4M3 ? 0x01010101u : 0x03030303u)) & 0x80808080u;
+  return (w & ~nan) | (nan - (nan >> 7));
+}
+
+// The codes that f32_to_e4m3 / f32_to_e5m2 give.  `special`, for any lane of
+// the wave, says that one of the lane's values may be NaN or infinite (codes
+// 0x7F and +-max); without one a value costs half a conversion instruction.
+// CLAMP: values may lie beyond the format's range; those scaled by their own
 // tile's amax do not: they reach at most fp8_max (1 + 2^-22), which the
-// conversion rounds to fp8_max (measured).
-template <int N, int E, bool CLAMP>
-__device__ __forceinline__ void encode(int yt, const float (&t)[N][E], bool special, uint32_t (&w)[N][E / 4]) {
+// conversion rounds to fp8_max (measured).  val is evaluated on the path that
+// is taken, so that the values need no registers of their own.
+template <int N, int E, bool CLAMP, typename F>
+__device__ __forceinline__ void encode(int yt, bool special, uint32_t (&w)[N][E / 4], F val) {
+  const float m = fp8_max(yt);
   if (__builtin_amdgcn_ballot_w64(special)) {
+    // clamped with NaN kept
+    auto y = [&](int n, int k) __attribute__((always_inline)) {
+      return __builtin_elementwise_minimum(__builtin_elementwise_maximum(val(n, k), -m), m);
+    };
+    if (yt == AMP_E4M3) convert<AMP_E4M3, N, E>(w, y);
+    else convert<AMP_E5M2, N, E>(w, y);
 #pragma unroll
     for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int q = 0; q < E / 4; ++q) {
-        w[n][q] = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          w[n][q] |= (yt == AMP_E4M3 ? f32_to_e4m3(t[n][4 * q + k]) : f32_to_e5m2(t[n][4 * q + k])) << (8 * k);
-      }
+      for (int q = 0; q < E / 4; ++q) w[n][q] = yt == AMP_E4M3 ? canon_nan<AMP_E4M3>(w[n][q]) : canon_nan<AMP_E5M2>(w[n][q]);
     return;
   }
-  const float m = fp8_max(yt);
   auto y = [&](int n, int k) __attribute__((always_inline)) {
-    return CLAMP ? __builtin_amdgcn_fmed3f(t[n][k], -m, m) : t[n][k];
+    return CLAMP ? __builtin_amdgcn_fmed3f(val(n, k), -m, m) : val(n, k);
   };
-  if (yt == AMP_E4M3) {
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-      for (int q = 0; q < E; q += 4) {
-        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(y(n, q), y(n, q + 1), 0, false);
-        w[n][q / 4] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(y(n, q + 2), y(n, q + 3), lo, true));
-      }
-  } else {
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-      for (int q = 0; q < E; q += 4) {
-        const int lo = __builtin_amdgcn_cvt_pk_bf8_f32(y(n, q), y(n, q + 1), 0, false);
-        w[n][q / 4] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_bf8_f32(y(n, q + 2), y(n, q + 3), lo, true));
-      }
-  }
+  if (yt == AMP_E4M3) convert<AMP_E4M3, N, E>(w, y);
+  else convert<AMP_E5M2, N, E>(w, y);
 }
 
 // E codes to column c of the n at p.
@@ -384,14 +397,10 @@ template <int N, int E, bool FULL = false>
 __device__ __forceinline__ void store_plain(void* p, int yt, int c, int step, int n, bool live, float scale, float am,
                                             const float (&v)[N][E]) {
   const bool special = mag(am) >= kInfBits || mag(scale) >= kInfBits;
-  float t[N][E];
-#pragma unroll
-  for (int k = 0; k < N; ++k)
-#pragma unroll
-    for (int e = 0; e < E; ++e) t[k][e] = v[k][e] * scale;
+  auto t = [&](int k, int e) __attribute__((always_inline)) { return v[k][e] * scale; };
   if (yt == AMP_E4M3 || yt == AMP_E5M2) {
     uint32_t w[N][E / 4];
-    encode<N, E, true>(yt, t, special, w);
+    encode<N, E, true>(yt, special, w, t);
 #pragma unroll
     for (int k = 0; k < N; ++k)
       if (live) store_codes<E, FULL>(static_cast<uint8_t*>(p), c + k * step, n, w[k]);
@@ -403,13 +412,13 @@ __device__ __forceinline__ void store_plain(void* p, int yt, int c, int step, in
     for (int k = 0; k < N; ++k)
 #pragma unroll
       for (int q = 0; q < E / 2; ++q)
-        h[k][q] = yt == AMP_BF16 ? f32_to_bf16(t[k][2 * q]) | (f32_to_bf16(t[k][2 * q + 1]) << 16)
-                                 : f32_to_f16(t[k][2 * q]) | (f32_to_f16(t[k][2 * q + 1]) << 16);
+        h[k][q] = yt == AMP_BF16 ? f32_to_bf16(t(k, 2 * q)) | (f32_to_bf16(t(k, 2 * q + 1)) << 16)
+                                 : f32_to_f16(t(k, 2 * q)) | (f32_to_f16(t(k, 2 * q + 1)) << 16);
   } else {
 #pragma unroll
     for (int k = 0; k < N; ++k)
 #pragma unroll
-      for (int q = 0; q < E / 2; ++q) h[k][q] = pack16(yt == AMP_BF16, t[k][2 * q], t[k][2 * q + 1]);
+      for (int q = 0; q < E / 2; ++q) h[k][q] = pack16(yt == AMP_BF16, t(k, 2 * q), t(k, 2 * q + 1));
   }
 #pragma unroll
   for (int k = 0; k < N; ++k)
@@ -442,82 +451,192 @@ __device__ __forceinline__ void block_amax(float am, uint32_t seen, uint32_t* re
 }
 
 // ---- 128x128 regions written transposed -------------------------------------
-// 512 threads hold a region of a [rows, cols] tensor: thread t the 8 rows
-// 8 (t / 32) .. + 7 of the 4 columns 4 (t % 32) .. + 3, so that a row's 128
-// columns are 32 adjacent lanes and a thread's transposed codes are whole
-// 8-byte units.
+// 512 threads hold a region of a [rows, cols] tensor: thread t the 4 rows
+// 4 (t / 16) .. + 3 of the 8 columns 8 (t % 16) .. + 7, so that a row's 128
+// columns are 16 adjacent lanes and a thread's transposed codes whole words.
+// The pieces of 128 bytes that a region writes to each row are stored through
+// the caches (non-temporal: 2 % slower).
 constexpr int kRegThreads = 512;
-constexpr int kRegRows = 8, kRegCols = 4;
+constexpr int kRegRows = 4, kRegCols = 8;
 
-// Where the 8-byte unit `u` (rows 8u .. 8u+7) of column c lies among the 128
-// transposed rows of 128 bytes: the exclusive-ors spread one column of a
-// wave's 32 column groups over all 64 banks, and keep 16-byte pairs and whole
-// rows together for the reads.
+// The region's place: its first row and column, and what the tensor has of
+// it.  SPANS: each of the 8 XCDs (block b runs on b % 8) takes one contiguous
+// span of the regions, row by row.
+struct Region {
+  int64_t r0, c0;
+  int nrows, ncols;
+  __device__ __forceinline__ Region(int64_t rows, int64_t cols, bool spans) {
+    uint32_t k = blockIdx.y * gridDim.x + blockIdx.x;
+    if (spans) {
+      const uint32_t n = gridDim.x * gridDim.y, x = k % 8;
+      k = x * (n / 8) + (x < n % 8 ? x : n % 8) + k / 8;
+    }
+    r0 = static_cast<int64_t>(k / gridDim.x) * kTileK;
+    c0 = static_cast<int64_t>(k % gridDim.x) * kTileK;
+    nrows = left(rows - r0) < kTileK ? left(rows - r0) : kTileK;
+    ncols = left(cols - c0) < kTileK ? left(cols - c0) : kTileK;
+  }
+  __device__ __forceinline__ bool whole() const { return nrows == kTileK && ncols == kTileK; }
+  // this thread's first row and column in the region
+  __device__ __forceinline__ int r() const { return threadIdx.x / 16 * kRegRows; }
+  __device__ __forceinline__ int c() const { return threadIdx.x % 16 * kRegCols; }
+  // the tensor's row that stands for this thread's row i (the last one past the end)
+  __device__ __forceinline__ int64_t row(int i) const { return r0 + (r() + i < nrows ? r() + i : nrows - 1); }
+};
+
+// This thread's elements of a region of 32-, 16- or 8-bit elements, a row at a
+// time as D dwords.  The loads carry no branch and no dependence (a lane past
+// the edge reads the nearest place inside), so that all are in flight
+// together; trim() then drops what the lane does not hold.
+template <int BYTES>
+struct RegRaw {
+  static constexpr int D = kRegCols * BYTES / 4;
+  uint32_t w[kRegRows][D];
+
+  // row i, its columns at p (the row's element c0)
+  __device__ __forceinline__ void load(const Region& g, int i, const void* p) {
+    if (g.ncols < kRegCols) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) w[i][d] = 0;
+#pragma unroll
+      for (int k = 0; k < kRegCols; ++k) {
+        const int e = k < g.ncols ? k : g.ncols - 1;
+        const uint32_t v = BYTES == 4 ? static_cast<const uint32_t*>(p)[e] : BYTES == 2 ? static_cast<const uint16_t*>(p)[e]
+                                                                                       : static_cast<const uint8_t*>(p)[e];
+        w[i][k * BYTES / 4] |= k < g.ncols ? v << (8 * (k * BYTES % 4)) : 0u;
+      }
+      return;
+    }
+    const uint32_t e = static_cast<uint32_t>(g.c() < g.ncols - kRegCols ? g.c() : g.ncols - kRegCols) * BYTES;
+    if constexpr (D == 2) {
+      const u32x2 v = ld8(p, e);
+      w[i][0] = v.x;
+      w[i][1] = v.y;
+    } else {
+#pragma unroll
+      for (int q = 0; q < D / 4; ++q) {
+        const u32x4 v = ld16(p, e + 16 * q);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[i][4 * q + k] = v[k];
+      }
+    }
+  }
+
+  // zeros past the region's edges
+  __device__ __forceinline__ void trim(const Region& g) {
+    if (g.whole()) return;
+    const int drop = g.ncols < kRegCols ? (g.c() ? kRegCols : 0) : g.c() - (g.ncols - kRegCols);
+#pragma unroll
+    for (int i = 0; i < kRegRows; ++i) {
+      const bool in = g.r() + i < g.nrows && drop < kRegCols;
+      uint32_t v[D];
+#pragma unroll
+      for (int d = 0; d < D; ++d) v[d] = in ? w[i][d] : 0u;
+      if (drop > 0) {
+        // a shift down by drop * BYTES bytes, one power of two at a time
+#pragma unroll
+        for (int b = 4; b >= 1; b /= 2) {
+          const int by = b * BYTES;
+          if ((drop & b) == 0) continue;
+#pragma unroll
+          for (int d = 0; d < D; ++d) {
+            if (by >= 4) v[d] = d + by / 4 < D ? v[d + by / 4] : 0u;
+            else v[d] = __builtin_amdgcn_alignbit(d + 1 < D ? v[d + 1] : 0u, v[d], 8 * by);
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d) w[i][d] = v[d];
+    }
+  }
+};
+
+template <int XT>
+__device__ __forceinline__ void reg_values(const uint32_t (&w)[kRegCols * kBytes<XT> / 4], float (&v)[kRegCols]) {
+#pragma unroll
+  for (int k = 0; k < kRegCols; ++k) {
+    if constexpr (XT == AMP_F32) v[k] = bitsf(w[k]);
+    else if constexpr (XT == AMP_BF16) v[k] = bitsf(k & 1 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+    else v[k] = f16_to_f32(k & 1 ? w[k / 2] >> 16 : w[k / 2] & 0xffffu);
+  }
+}
+
+// Where the 4 transposed codes of rows 4u .. 4u+3 of column c lie: 128 rows
+// of 128 bytes, one per column, the exclusive-ors spread one column of a
+// wave's 16 column groups by 4 row groups over all 64 banks and keep 16-byte
+// pieces and whole rows together for the reads.
 __device__ __forceinline__ int reg_at(int c, int u) {
-  return (c ^ ((c >> 5) & 1)) * kTileK + 8 * (u ^ (2 * ((c >> 2) & 7)));
+  return (c ^ ((c >> 6) & 1)) * kTileK + 4 * (u ^ (4 * ((c >> 3) & 7)));
 }
 
 template <int N>
 struct RegLds {
   union {
-    uint32_t part[N][16][kTileK];                        // column maxima of the 16 thread rows
+    uint32_t part[N][32][kTileK];                        // column maxima of the 32 thread rows
     __align__(16) uint8_t codes[N][kTileK * kTileK];     // transposed codes
   };
   float scale[N][kTileK];
 };
 
-// Write N regions v[n] transposed: o[n] is the [cols, rows] output whose row
-// col0[n] + j is the region's column j (o[n].q NULL: none).  `rows` and
-// `ncols` bound the region.  Three block barriers.
+// Write N regions v[n] transposed in three steps with block barriers between
+// them: column maxima, scales, codes.  o[n] is the [cols, rows] output whose
+// row col0[n] + j is the region's column j (o[n].q NULL: none).
 template <int N>
-__device__ __forceinline__ void store_regions_t(RegLds<N>& l, const amp_fp8_tiles (&o)[N], const int64_t (&col0)[N],
-                                                int64_t row0, int64_t rows, int ncols,
-                                                const float (&v)[N][kRegRows][kRegCols]) {
-  const int t = threadIdx.x, cg = t % 32, rg = t / 32;
-  const int nrows = left(rows - row0);
+__device__ __forceinline__ void reg_maxima(RegLds<N>& l, const Region& g, const float (&v)[N][kRegRows][kRegCols]) {
 #pragma unroll
   for (int n = 0; n < N; ++n) {
-    u32x4 m;
+    u32x4 m[2];
 #pragma unroll
     for (int j = 0; j < kRegCols; ++j) {
       float a = 0.0f;
 #pragma unroll
       for (int i = 0; i < kRegRows; i += 2)
         a = __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, fabsf(v[n][i][j])), fabsf(v[n][i + 1][j]));
-      m[j] = mag(a);
+      m[j / 4][j % 4] = mag(a);
     }
-    *reinterpret_cast<u32x4*>(&l.part[n][rg][4 * cg]) = m;
+    u32x4* p = reinterpret_cast<u32x4*>(&l.part[n][threadIdx.x / 16][g.c()]);
+    p[0] = m[0];
+    p[1] = m[1];
   }
-  __syncthreads();
-  if (t < N * kTileK) {
-    const int n = t / kTileK, c = t % kTileK;
-    uint32_t m = 0;
+}
+
+template <int N>
+__device__ __forceinline__ void reg_scales(RegLds<N>& l, const Region& g, const amp_fp8_tiles (&o)[N], const int64_t (&col0)[N]) {
+  const int t = threadIdx.x;
+  if (t >= N * kTileK) return;
+  const int n = __builtin_amdgcn_readfirstlane(t / kTileK), c = t % kTileK;
+  uint32_t m = 0;
 #pragma unroll
-    for (int g = 0; g < 16; ++g) m = m > l.part[n][g][c] ? m : l.part[n][g][c];
+  for (int k = 0; k < 32; ++k) m = m > l.part[n][k][c] ? m : l.part[n][k][c];
+  amp_fp8_tiles ot = o[0];
+  int64_t first = col0[0];
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      if (k != n) continue;
-      const float sc = scale_of(m, fp8_max(o[k].type));
-      // the sign carries whether the tile holds a NaN or infinity
-      l.scale[k][c] = m >= kInfBits ? -sc : sc;
-      if (o[k].q && c < ncols) o[k].s[row0 / kTileK * o[k].lds + col0[k] + c] = 1.0f / sc;
-    }
-  }
-  __syncthreads();
+  for (int k = 1; k < N; ++k)
+    if (k == n) { ot = o[k]; first = col0[k]; }
+  const float sc = scale_of(m, fp8_max(ot.type));
+  // the sign carries whether the tile holds a NaN or infinity
+  l.scale[n][c] = m >= kInfBits ? -sc : sc;
+  if (ot.q && c < g.ncols) ot.s[g.r0 / kTileK * ot.lds + first + c] = 1.0f / sc;
+}
+
+template <int N>
+__device__ __forceinline__ void reg_codes(RegLds<N>& l, const Region& g, const amp_fp8_tiles (&o)[N], const int64_t (&col0)[N],
+                                          const float (&v)[N][kRegRows][kRegCols]) {
+  const int t = threadIdx.x;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     if (!o[n].q) continue;
-    const f32x4 sc = *reinterpret_cast<const f32x4*>(&l.scale[n][4 * cg]);
+    float sc[kRegCols];
+    bool special = false;
 #pragma unroll
     for (int j = 0; j < kRegCols; ++j) {
-      float f[1][kRegRows];
-#pragma unroll
-      for (int i = 0; i < kRegRows; ++i) f[0][i] = v[n][i][j] * fabsf(sc[j]);
-      uint32_t w[1][2];
-      encode<1, kRegRows, false>(o[n].type, f, sc[j] < 0.0f, w);
-      const u32x2 d = {w[0][0], w[0][1]};
-      *reinterpret_cast<u32x2*>(&l.codes[n][reg_at(4 * cg + j, rg)]) = d;
+      sc[j] = l.scale[n][g.c() + j];
+      special |= sc[j] < 0.0f;
     }
+    uint32_t w[kRegCols][1];
+    encode<kRegCols, kRegRows, false>(o[n].type, special, w, [&](int j, int i) __attribute__((always_inline)) { return v[n][i][j] * fabsf(sc[j]); });
+#pragma unroll
+    for (int j = 0; j < kRegCols; ++j) *reinterpret_cast<uint32_t*>(&l.codes[n][reg_at(g.c() + j, t / 16)]) = w[j][0];
   }
   __syncthreads();
 #pragma unroll
@@ -526,15 +645,15 @@ __device__ __forceinline__ void store_regions_t(RegLds<N>& l, const amp_fp8_tile
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
       const int c = it * 64 + t / 8, b = t % 8 * 16;
-      if (c >= ncols) continue;
-      const u32x4 w = *reinterpret_cast<const u32x4*>(&l.codes[n][reg_at(c, b / 8)]);
-      uint8_t* p = o[n].q + (col0[n] + c) * o[n].ldq + row0;
-      if (b + 16 <= nrows) {
-        st16(p, b, w);
+      if (c >= g.ncols) continue;
+      const u32x4 w = *reinterpret_cast<const u32x4*>(&l.codes[n][reg_at(c, b / 4)]);
+      uint8_t* p = o[n].q + (col0[n] + c) * o[n].ldq + g.r0;
+      if (b + 16 <= g.nrows) {
+        *reinterpret_cast<u32x4_any*>(p + b) = w;
       } else {
 #pragma unroll
         for (int k = 0; k < 16; ++k)
-          if (b + k < nrows) p[b + k] = static_cast<uint8_t>(w[k / 4] >> (8 * (k & 3)));
+          if (b + k < g.nrows) p[b + k] = static_cast<uint8_t>(w[k / 4] >> (8 * (k & 3)));
       }
     }
   }
