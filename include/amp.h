@@ -460,7 +460,7 @@ int amp_rmsnorm(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx,
  *    dgamma (needed with dgamma); calls that may overlap need one each.  The
  *    sums are added in a fixed order: the result is reproducible.
  * cols == 0 is a no-op. */
-#define AMP_RMSNORM_PARTIALS 512
+#define AMP_RMSNORM_PARTIALS 256
 int amp_rmsnorm_backward(const void* dy, int dt, int64_t rows, int64_t cols, int64_t lddy,
                          const void* h, int64_t ldh, const amp_fp8_tiles* ckpt,
                          const void* gamma, int gt, const float* rstd, const void* dres,

@@ -41,7 +41,7 @@ AMAX_MAX, AMAX_MOST_RECENT = 0, 1
 OPT_SKIP_CHECK = 1
 GEMM_FP8_NATIVE = 1
 GEMM_MX = 2
-RMSNORM_PARTIALS = 512                     # rows of amp_rmsnorm_backward's work area
+RMSNORM_PARTIALS = 256                     # rows of amp_rmsnorm_backward's work area
 
 # Device-resident state layouts (mirror the C structs; for reading back).
 SCALER_STATE_DTYPE = np.dtype([("scale", "<f4"), ("growth_tracker", "<i4"),

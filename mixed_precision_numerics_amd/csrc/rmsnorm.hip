@@ -162,6 +162,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_rows(const NormArgs
 #pragma unroll
     for (int v = 0; v < V; ++v) h[v / N][v % N] = join<XT>(h[v / N][v % N], q[v]);
   }
+  // (sums of two vectors are trimmed like one)
+#pragma unroll
+  for (int v = 0; v < V; ++v) h[v / N][v % N] = trim_vec<XT, FULL>(h[v / N][v % N], c + v * step, n);
   float ss = 0.0f;
 #pragma unroll
   for (int v = 0; v < V; ++v) ss = sum_squares<XT>(h[v / N][v % N], ss);
@@ -200,6 +203,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long(const NormArgs a) {
     const int n = left(a.cols - c0);
     u32x4 w = load_vec<XT>(elem<XT>(a.x, row * a.ldx + c0), c, n);
     if (a.res) w = join<XT>(w, load_vec<XT>(elem<XT>(a.res, row * a.ldr + c0), c, n));
+    w = trim_vec<XT>(w, c, n);
     if (a.h) store_vec<XT>(elem<XT>(a.h, row * a.ldh + c0), c, n, w);
     ss = sum_squares<XT>(w, ss);
   }
@@ -215,6 +219,7 @@ __global__ __launch_bounds__(1024) void rmsnorm_long(const NormArgs a) {
       w[0] = load_vec<XT>(elem<XT>(a.x, row * a.ldx + c0), c, n);
       if (a.res) w[0] = join<XT>(w[0], load_vec<XT>(elem<XT>(a.res, row * a.ldr + c0), c, n));
     }
+    w[0] = trim_vec<XT>(w[0], c, n);
     float gm[1][E];
     load_cols<E>(a.gamma ? elem_of(a.gt, a.gamma, c0) : nullptr, a.gt, c, n, gm[0]);
     am = __builtin_elementwise_maximum(am, norm_outputs<XT, 1, false>(a, w, gm, row, c0, c, 0, n, true, r, scale));
@@ -320,6 +325,11 @@ struct HRaw {
       w = load_vec<XT, FULL>(elem<XT>(a.h, row * a.ldh + c0), c, n);
     }
   }
+  template <bool FULL>
+  __device__ __forceinline__ void trim(int c, int n) {
+    if constexpr (CK) trim_codes<E, FULL>(q, c, n);
+    else w = trim_vec<XT, FULL>(w, c, n);
+  }
   __device__ __forceinline__ void values(const NormBackArgs& a, float (&v)[E]) const {
     if constexpr (CK) decode<E>(a.ck.type, q, s, v);
     else widen<XT>(w, v);
@@ -339,10 +349,13 @@ __device__ __forceinline__ void dx_of(const float (&dy)[E], const float (&h)[E],
 // not depend on the order in which blocks run).  FULL: the row is V T whole
 // vectors.
 //
-// HBM-bound.  The next row's loads go out before this row's stores: loads and
-// stores complete in one count, so loads issued behind the stores would wait
-// for them.  They are issued without a branch (dy stands in for an absent
-// dres), so that the wait for them can be counted.
+// HBM-bound (8192 x 4096 BF16 from a checkpoint with dres: 44 us = 5.4 TB/s,
+// and 4 us for dgamma_sum).  The next row's loads go out before this row's
+// stores: loads and stores complete in one count, so loads issued behind the
+// stores would wait for them.  They are issued without a branch (dy stands in
+// for an absent dres), so that the wait for them can be counted.  One block a CU: 128
+// partial rows keep half the machine idle, 512 cost more to write and add up
+// (1000 x 4096: 13 us with 256, 16 with 512, 15 with 128).
 template <int XT, bool CK, int V, int S, bool FULL>
 __global__ __launch_bounds__(S > 1 ? 512 : 1024) void rmsnorm_back_rows(const NormBackArgs a) {
   constexpr int E = kVec<XT>;
@@ -380,13 +393,16 @@ __global__ __launch_bounds__(S > 1 ? 512 : 1024) void rmsnorm_back_rows(const No
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float dy[E], h[E];
+      const int c = (v * T + tid) * E;
+      w.dy[v] = trim_vec<XT, FULL>(w.dy[v], c, n);
+      w.h[v].template trim<FULL>(c, n);
       widen<XT>(w.dy[v], dy);
       w.h[v].values(a, h);
 #pragma unroll
       for (int k = 0; k < E; ++k) {
-        const float t = dy[k] * (h[k] * w.r);
-        dot = __builtin_fmaf(t, gm[v][k], dot);
-        dg[v][k] += live ? t : 0.0f;
+        dy[k] *= h[k] * w.r;
+        dot = __builtin_fmaf(dy[k], gm[v][k], dot);
+        dg[v][k] += live ? dy[k] : 0.0f;
       }
     }
     const Row next = fetch(row + step);
@@ -396,11 +412,11 @@ __global__ __launch_bounds__(S > 1 ? 512 : 1024) void rmsnorm_back_rows(const No
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float dy[E], h[E], d[E];
-        widen<XT>(w.dy[v], dy);
+          widen<XT>(w.dy[v], dy);
         w.h[v].values(a, h);
         dx_of<E>(dy, h, gm[v], w.r, m, d);
         if (a.dres) {
-          widen<XT>(w.res[v], dy);
+          widen<XT>(trim_vec<XT, FULL>(w.res[v], (v * T + tid) * E, n), dy);
 #pragma unroll
           for (int k = 0; k < E; ++k) d[k] += dy[k];
         }
@@ -440,76 +456,168 @@ __global__ __launch_bounds__(S > 1 ? 512 : 1024) void rmsnorm_back_rows(const No
   }
 }
 
-// Rows too long for the registers: two walks, the partial sums kept in the
-// block's own row of the work area.
-template <int XT, bool CK>
-__global__ __launch_bounds__(1024) void rmsnorm_back_long(const NormBackArgs a) {
+// Rows of more than two vectors in each of 1024 threads, whose sums and next
+// row have no registers: dx by one block a row, and the sums of dy n in a pass
+// of their own, which reads dy and h again.  (Kept together with the sums in
+// the LDS, 2000 x 28672 BF16 took 238 us, and in the work area 440.)
+template <int XT, bool CK, int V>
+__global__ __launch_bounds__(1024) void rmsnorm_dx_rows(const NormBackArgs a) {
   constexpr int E = kVec<XT>, T = 1024;
   __shared__ float red[32];
-  const float inv_n = 1.0f / static_cast<float>(a.cols);
-  float* part = a.part ? a.part + static_cast<int64_t>(blockIdx.x) * a.cols : nullptr;
-  const int c = threadIdx.x * E;
-  int turn = 0;
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const float r = a.rstd[row];
-    float dot = 0.0f, m = 0.0f;
-    for (int pass = 0; pass < (a.dx ? 2 : 1); ++pass) {
-      for (int64_t c0 = 0; c0 < a.cols; c0 += T * E) {
-        const int n = left(a.cols - c0);
-        if (c >= n) break;
-        float dy[E], h[E], gm[E], d[E];
-        HRaw<XT, CK> hr;
-        widen<XT>(load_vec<XT>(elem<XT>(a.dy, row * a.lddy + c0), c, n), dy);
-        hr.template load<false>(a, row, c0, c, n);
-        hr.values(a, h);
-        load_cols<E>(a.gamma ? elem_of(a.gt, a.gamma, c0) : nullptr, a.gt, c, n, gm);
-        if (pass == 0) {
+  const int64_t row = blockIdx.x;
+  const int n = left(a.cols);
+  u32x4 wd[V], wr[V];
+  HRaw<XT, CK> hr[V];
 #pragma unroll
-          for (int k = 0; k < E; ++k) {
-            const float t = dy[k] * (h[k] * r);
-            dot = __builtin_fmaf(t, gm[k], dot);
-            if (part && c + k < n) part[c0 + c + k] = (row == blockIdx.x ? 0.0f : part[c0 + c + k]) + t;
-          }
-        } else {
-          dx_of<E>(dy, h, gm, r, m, d);
-          if (a.dres) {
-            widen<XT>(load_vec<XT>(elem<XT>(a.dres, row * a.lddr + c0), c, n), dy);
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * T + threadIdx.x) * E;
+    wd[v] = load_vec<XT>(elem<XT>(a.dy, row * a.lddy), c, n);
+    hr[v].template load<false>(a, row, 0, c, n);
+    if (a.dres) wr[v] = load_vec<XT>(elem<XT>(a.dres, row * a.lddr), c, n);
+  }
+  const float r = a.rstd[row];
+  float dot = 0.0f;
 #pragma unroll
-            for (int k = 0; k < E; ++k) d[k] += dy[k];
-          }
-          store_vec<XT>(elem<XT>(a.dx, row * a.lddx + c0), c, n, narrow<XT>(d));
-        }
-      }
-      if (pass == 0 && a.dx) {
-        m = row_sum(dot, T, red, turn) * inv_n;
-        turn ^= 1;
-      }
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * T + threadIdx.x) * E;
+    float dy[E], h[E], gm[E];
+    wd[v] = trim_vec<XT>(wd[v], c, n);
+    hr[v].template trim<false>(c, n);
+    widen<XT>(wd[v], dy);
+    hr[v].values(a, h);
+    load_cols<E>(a.gamma, a.gt, c, n, gm);
+#pragma unroll
+    for (int k = 0; k < E; ++k) dot = __builtin_fmaf(dy[k] * (h[k] * r), gm[k], dot);
+  }
+  const float m = row_sum(dot, T, red, 0) / static_cast<float>(a.cols);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int c = (v * T + threadIdx.x) * E;
+    float dy[E], h[E], gm[E], d[E];
+    widen<XT>(wd[v], dy);
+    hr[v].values(a, h);
+    load_cols<E>(a.gamma, a.gt, c, n, gm);
+    dx_of<E>(dy, h, gm, r, m, d);
+    if (a.dres) {
+      widen<XT>(trim_vec<XT>(wr[v], c, n), dy);
+#pragma unroll
+      for (int k = 0; k < E; ++k) d[k] += dy[k];
     }
+    store_vec<XT>(elem<XT>(a.dx, row * a.lddx), c, n, narrow<XT>(d));
   }
 }
 
-// dgamma[c] = sum over the P rows of partial sums, in a fixed order: 32
-// columns a block, 8 lanes of 4 columns by 32 strands of rows.
-__global__ __launch_bounds__(256) void dgamma_sum(const float* __restrict__ part, int64_t P, int64_t cols,
-                                                  float* __restrict__ dgamma) {
-  __shared__ float sums[32][33];
+// Longer rows still: the block walks its row twice.
+template <int XT, bool CK>
+__global__ __launch_bounds__(1024) void rmsnorm_dx_long(const NormBackArgs a) {
+  constexpr int E = kVec<XT>, T = 1024;
+  __shared__ float red[32];
+  const int64_t row = blockIdx.x;
+  const int c = threadIdx.x * E;
+  const float r = a.rstd[row];
+  float dot = 0.0f, m = 0.0f;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int64_t c0 = 0; c0 < a.cols; c0 += T * E) {
+      const int n = left(a.cols - c0);
+      if (c >= n) break;
+      float dy[E], h[E], gm[E], d[E];
+      HRaw<XT, CK> hr;
+      const u32x4 w = load_vec<XT>(elem<XT>(a.dy, row * a.lddy + c0), c, n);
+      hr.template load<false>(a, row, c0, c, n);
+      hr.template trim<false>(c, n);
+      widen<XT>(trim_vec<XT>(w, c, n), dy);
+      hr.values(a, h);
+      load_cols<E>(a.gamma ? elem_of(a.gt, a.gamma, c0) : nullptr, a.gt, c, n, gm);
+      if (pass == 0) {
+#pragma unroll
+        for (int k = 0; k < E; ++k) dot = __builtin_fmaf(dy[k] * (h[k] * r), gm[k], dot);
+      } else {
+        dx_of<E>(dy, h, gm, r, m, d);
+        if (a.dres) {
+          widen<XT>(trim_vec<XT>(load_vec<XT>(elem<XT>(a.dres, row * a.lddr + c0), c, n), c, n), dy);
+#pragma unroll
+          for (int k = 0; k < E; ++k) d[k] += dy[k];
+        }
+        store_vec<XT>(elem<XT>(a.dx, row * a.lddx + c0), c, n, narrow<XT>(d));
+      }
+    }
+    if (pass == 0) m = row_sum(dot, T, red, 0) / static_cast<float>(a.cols);
+  }
+}
+
+// Partial sums of dy n down the columns: 256 threads take 256 vectors of
+// every gridDim.y-th row, four rows in flight.
+template <int XT, bool CK>
+__global__ __launch_bounds__(256) void dgamma_part(const NormBackArgs a) {
+  constexpr int E = kVec<XT>, R = 4;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * (256 * E);
+  const int c = threadIdx.x * E, n = left(a.cols - c0);
+  const int64_t step = gridDim.y;
+  float dg[E] = {};
+  for (int64_t r0 = blockIdx.y; r0 < a.rows; r0 += step * R) {
+    u32x4 wd[R];
+    HRaw<XT, CK> hr[R];
+    float r[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int64_t row = r0 + i * step < a.rows ? r0 + i * step : a.rows - 1;   // read again, not used
+      wd[i] = load_vec<XT>(elem<XT>(a.dy, row * a.lddy + c0), c, n);
+      hr[i].template load<false>(a, row, c0, c, n);
+      r[i] = a.rstd[row];
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float dy[E], h[E];
+      hr[i].template trim<false>(c, n);
+      widen<XT>(trim_vec<XT>(wd[i], c, n), dy);
+      hr[i].values(a, h);
+#pragma unroll
+      for (int k = 0; k < E; ++k) dg[k] += r0 + i * step < a.rows ? dy[k] * (h[k] * r[i]) : 0.0f;
+    }
+  }
+  float* p = a.part + static_cast<int64_t>(blockIdx.y) * a.cols + c0;
+#pragma unroll
+  for (int q = 0; q < E / 4; ++q)
+    store_vec<AMP_F32>(p, c + 4 * q, n, u32x4{fbits(dg[4 * q]), fbits(dg[4 * q + 1]), fbits(dg[4 * q + 2]), fbits(dg[4 * q + 3])});
+}
+
+// dgamma[c] = sum over the P <= AMP_RMSNORM_PARTIALS rows of partial sums, in
+// a fixed order: 32 columns a block, 8 lanes of 4 columns by 128 strands of
+// rows, whose loads are all in flight together.
+__global__ __launch_bounds__(1024) void dgamma_sum(const float* __restrict__ part, int P, int64_t cols,
+                                                   float* __restrict__ dgamma) {
+  constexpr int kStrands = 128, kLoads = AMP_RMSNORM_PARTIALS / kStrands;
+  __shared__ float sums[kStrands][33], more[32][33];
   const int lane = threadIdx.x % 8, strand = threadIdx.x / 8;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 32;
   const int n = left(cols - c0);
-  float t[4] = {};
-  for (int64_t p = strand; p < P; p += 32) {
-    const u32x4 w = load_vec<AMP_F32>(part + p * cols + c0, 4 * lane, n);
+  u32x4 w[kLoads];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) t[k] += bitsf(w[k]);
+  for (int k = 0; k < kLoads; ++k) {
+    const int p = strand + k * kStrands;
+    w[k] = p < P ? load_vec<AMP_F32>(part + p * cols + c0, 4 * lane, n) : u32x4{0u, 0u, 0u, 0u};
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) sums[strand][4 * lane + k] = t[k];
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    float v = 0.0f;
+  for (int k = 0; k < kLoads; ++k) w[k] = trim_vec<AMP_F32>(w[k], 4 * lane, n);
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v += sums[k][threadIdx.x];
-    if (static_cast<int>(threadIdx.x) < n) dgamma[c0 + threadIdx.x] = v;
+  for (int e = 0; e < 4; ++e) {
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) t += bitsf(w[k][e]);
+    sums[strand][4 * lane + e] = t;
+  }
+  __syncthreads();
+  const int col = threadIdx.x % 32, group = threadIdx.x / 32;
+  float t = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kStrands / 32; ++k) t += sums[group * (kStrands / 32) + k][col];
+  more[group][col] = t;
+  __syncthreads();
+  if (threadIdx.x < 32 && col < n) {
+    t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) t += more[k][col];
+    dgamma[c0 + col] = t;
   }
 }
 
@@ -532,17 +640,38 @@ hipError_t dispatch_back(const NormBackArgs& a, float* dgamma, hipStream_t s) {
     else if (nv <= 256) AMP_BACK(1, 2, 512);
     else if (nv <= 512) AMP_BACK(1, 1, 512);
     else if (nv <= 1024) AMP_BACK(1, 1, 1024);
-    else if (nv <= 2048) AMP_BACK(2, 1, 1024);
-    else if (nv <= 4096) AMP_BACK(4, 1, 1024);
+    else if (nv <= 2 * 1024) AMP_BACK(2, 1, 1024);
     else {
-      blocks = a.rows < AMP_RMSNORM_PARTIALS ? a.rows : AMP_RMSNORM_PARTIALS;
-      rmsnorm_back_long<XT, CK><<<static_cast<unsigned>(blocks), 1024, 0, s>>>(a);
+      if (dgamma) {   // before dx, which may take the place of dy
+        // about eight blocks a CU, each with at least four rows
+        const int64_t x = (nv + 255) / 256;
+        blocks = (a.rows + 3) / 4 < 2048 / x + 1 ? (a.rows + 3) / 4 : 2048 / x + 1;
+        if (blocks > AMP_RMSNORM_PARTIALS) blocks = AMP_RMSNORM_PARTIALS;
+        dgamma_part<XT, CK><<<dim3(static_cast<unsigned>(x), static_cast<unsigned>(blocks)), 256, 0, s>>>(a);
+      }
+      // four vectors of 16-bit gradients and of codes with their scales do not
+      // fit the registers (2000 x 32768: 305 us)
+      constexpr bool kFour = !CK || XT == AMP_F32;
+      constexpr int64_t kMost = 1 << 21;   // rows a launch: a grid's threads are counted in 32 bits
+      for (int64_t r0 = 0; a.dx && r0 < a.rows; r0 += kMost) {
+        NormBackArgs b = a;
+        b.dy = elem<XT>(a.dy, r0 * a.lddy);
+        if (CK) { b.ck.q += r0 * a.ck.ldq; b.ck.s += r0; }
+        else b.h = elem<XT>(a.h, r0 * a.ldh);
+        b.rstd += r0;
+        if (a.dres) b.dres = elem<XT>(a.dres, r0 * a.lddr);
+        b.dx = elem<XT>(a.dx, r0 * a.lddx);
+        const unsigned rows = static_cast<unsigned>(a.rows - r0 < kMost ? a.rows - r0 : kMost);
+        if (nv <= 3 * 1024) rmsnorm_dx_rows<XT, CK, 3><<<rows, 1024, 0, s>>>(b);
+        else if (kFour && nv <= 4 * 1024) rmsnorm_dx_rows<XT, CK, kFour ? 4 : 3><<<rows, 1024, 0, s>>>(b);
+        else rmsnorm_dx_long<XT, CK><<<rows, 1024, 0, s>>>(b);
+      }
     }
     if (hipError_t e = hipGetLastError()) return e;
   }
 #undef AMP_BACK
   if (dgamma)
-    dgamma_sum<<<static_cast<unsigned>((a.cols + 31) / 32), 256, 0, s>>>(a.part, blocks, a.cols, dgamma);
+    dgamma_sum<<<static_cast<unsigned>((a.cols + 31) / 32), 1024, 0, s>>>(a.part, static_cast<int>(blocks), a.cols, dgamma);
   return hipGetLastError();
 }
 

@@ -88,6 +88,8 @@ __global__ __launch_bounds__(256) void swiglu_rows(const GateArgs a) {
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     float g[E], u[E];
+    wg[i] = trim_vec<XT, FULL>(wg[i], c, n);
+    wu[i] = trim_vec<XT, FULL>(wu[i], c, n);
     widen<XT>(wg[i], g);
     widen<XT>(wu[i], u);
 #pragma unroll
@@ -150,13 +152,15 @@ __global__ __launch_bounds__(256) void swiglu_back_rows(const GateArgs a) {
     const int64_t row = row0 + i * S;
     if (row >= a.rows) return;
     float g[E], u[E], dy[E], dg[E], du[E];
-    widen<XT>(wd[i], dy);
+    widen<XT>(trim_vec<XT, FULL>(wd[i], c, n), dy);
     if constexpr (CK) {
+      trim_codes<E, FULL>(qg[i], c, n);
+      trim_codes<E, FULL>(qu[i], c, n);
       decode<E>(a.ck.type, qg[i], sg[i], g);
       decode<E>(a.ck.type, qu[i], su[i], u);
     } else {
-      widen<XT>(wg[i], g);
-      widen<XT>(wu[i], u);
+      widen<XT>(trim_vec<XT, FULL>(wg[i], c, n), g);
+      widen<XT>(trim_vec<XT, FULL>(wu[i], c, n), u);
     }
 #pragma unroll
     for (int k = 0; k < E; ++k) {
@@ -175,9 +179,15 @@ __global__ __launch_bounds__(256) void swiglu_back_rows(const GateArgs a) {
 // read once.  dg and du are formed in registers and leave from there in every
 // form asked for: dx in dy's type, dx in row tiles (dgrad), dx^T in tiles
 // along the rows (wgrad); then y is recomputed from g and u for y^T, so that
-// no more than two of the three are held at a time and two blocks share a CU.
+// no more than two of the three are held at a time and two blocks share a CU
+// (stored inputs take twice the registers: one block there; held to two they
+// spilled, 4096 x 14336 BF16 330 us instead of 184).
+//
+// Bound by the vector ALUs (79 % busy at 8192 x 14336 from a checkpoint, 60
+// operations per element of y, 254 us = 4.3 TB/s): the sigmoid's two
+// quarter-rate instructions, formed twice, are a quarter of it.
 template <int XT, bool CK>
-__global__ __launch_bounds__(kRegThreads, 4) void swiglu_back_region(const GateArgs a) {
+__global__ __launch_bounds__(kRegThreads, CK ? 4 : 2) void swiglu_back_region(const GateArgs a) {
   __shared__ RegLds<2> l;
   __shared__ uint32_t rmax[2][kTileK];
   __shared__ float rscale[2][kTileK], gscale[2][kTileK];

@@ -53,9 +53,7 @@ __device__ __forceinline__ void st16(void* p, uint32_t off, u32x4 v) { __builtin
 __device__ __forceinline__ void st8(void* p, uint32_t off, u32x2 v) { __builtin_nontemporal_store(v, reinterpret_cast<u32x2_any*>(at(p, off))); }
 __device__ __forceinline__ void st4(void* p, uint32_t off, uint32_t v) { __builtin_nontemporal_store(v, reinterpret_cast<u32_any*>(at(p, off))); }
 
-// The 16 bytes of w moved down by `bytes` (1..15), zeros moved in: a row's
-// last, partial vector comes from a whole one that ends with the row (one
-// load; a load per element would wait for each).
+// The 16 bytes of w moved down by `bytes` (1..15), zeros moved in.
 __device__ __forceinline__ u32x4 drop_low(u32x4 w, int bytes) {
   if (bytes & 8) w = u32x4{w[2], w[3], 0u, 0u};
   if (bytes & 4) w = u32x4{w[1], w[2], w[3], 0u};
@@ -64,25 +62,33 @@ __device__ __forceinline__ u32x4 drop_low(u32x4 w, int bytes) {
                __builtin_amdgcn_alignbit(w[3], w[2], s), w[3] >> s};
 }
 
-// One vector at column c of the n columns at p; columns from n on read as
-// zero.  FULL: the caller knows that the vector lies within the row (each
-// bound that is checked is a branch, and a row has dozens of vectors).
-// Non-temporal: these tensors are read once.
+// One vector at column c of the n columns at p, to be passed through trim_vec
+// before use: near the row's end it is the row's last whole vector, and what
+// the lane does not hold is dropped later, so that no load waits for another.
+// FULL: the caller knows that the vector lies within the row (each bound that
+// is checked is a branch, and a row has dozens of vectors).  Non-temporal:
+// these tensors are read once.
 template <int XT, bool FULL = false>
 __device__ __forceinline__ u32x4 load_vec(const void* p, int c, int n) {
   constexpr int E = kVec<XT>;
-  const uint32_t off = static_cast<uint32_t>(c) * kBytes<XT>;
-  if (FULL || c + E <= n) return ld16(p, off);
-  u32x4 w = {0u, 0u, 0u, 0u};
-  if (c >= n) return w;
-  if (n >= E) return drop_low(ld16(p, static_cast<uint32_t>(n - E) * kBytes<XT>), (c + E - n) * kBytes<XT>);
+  if constexpr (FULL) return ld16(p, static_cast<uint32_t>(c) * kBytes<XT>);
+  if (n >= E) return ld16(p, static_cast<uint32_t>(c < n - E ? c : n - E) * kBytes<XT>);
+  u32x4 w = {0u, 0u, 0u, 0u};   // a row shorter than one vector
 #pragma unroll
-  for (int k = 0; k < E; ++k)   // a row shorter than one vector
+  for (int k = 0; k < E; ++k)
     if (c + k < n) {
       if constexpr (XT == AMP_F32) w[k] = static_cast<const uint32_t*>(p)[c + k];
       else w[k / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p)[c + k]) << (16 * (k & 1));
     }
   return w;
+}
+
+// What load_vec's vector holds of the row from column c on, zeros past its end.
+template <int XT, bool FULL = false>
+__device__ __forceinline__ u32x4 trim_vec(u32x4 w, int c, int n) {
+  constexpr int E = kVec<XT>;
+  if (FULL || n < E || c + E <= n) return w;
+  return c < n ? drop_low(w, (c + E - n) * kBytes<XT>) : u32x4{0u, 0u, 0u, 0u};
 }
 
 template <int XT>
@@ -292,36 +298,38 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int c, int n, const uint
   }
 }
 
-// E codes from column c of the n at p; columns from n on read as zero.
+// E codes at column c of the n at p, and what they hold of the row: as
+// load_vec and trim_vec.
 template <int E, bool FULL = false>
 __device__ __forceinline__ void load_codes(const uint8_t* p, int c, int n, uint32_t (&w)[E / 4]) {
-  if (FULL || c + E <= n) {
+  const int e = FULL || c <= n - E ? c : n - E;
+  if (FULL || n >= E) {
     if constexpr (E == 8) {
-      const u32x2 d = ld8(p, c);
+      const u32x2 d = ld8(p, e);
       w[0] = d.x;
       w[1] = d.y;
     } else {
-      w[0] = ld4(p, c);
+      w[0] = ld4(p, e);
     }
+    return;
+  }
+#pragma unroll
+  for (int q = 0; q < E / 4; ++q) w[q] = 0;
+#pragma unroll
+  for (int k = 0; k < E; ++k)   // a row shorter than E
+    if (c + k < n) w[k / 4] |= static_cast<uint32_t>(p[c + k]) << (8 * (k & 3));
+}
+
+template <int E, bool FULL = false>
+__device__ __forceinline__ void trim_codes(uint32_t (&w)[E / 4], int c, int n) {
+  if (FULL || n < E || c + E <= n) return;
+  const int s = 8 * (c + E - n);
+  if constexpr (E == 8) {
+    const uint64_t v = c < n ? ((static_cast<uint64_t>(w[1]) << 32) | w[0]) >> s : 0u;
+    w[0] = static_cast<uint32_t>(v);
+    w[1] = static_cast<uint32_t>(v >> 32);
   } else {
-#pragma unroll
-    for (int q = 0; q < E / 4; ++q) w[q] = 0;
-    if (c >= n) return;
-    if (n >= E) {   // as load_vec
-      const int s = 8 * (c + E - n);
-      if constexpr (E == 8) {
-        const u32x2 d = ld8(p, n - E);
-        const uint64_t v = ((static_cast<uint64_t>(d.y) << 32) | d.x) >> s;
-        w[0] = static_cast<uint32_t>(v);
-        w[1] = static_cast<uint32_t>(v >> 32);
-      } else {
-        w[0] = ld4(p, n - E) >> s;
-      }
-      return;
-    }
-#pragma unroll
-    for (int k = 0; k < E; ++k)   // a row shorter than E
-      if (c + k < n) w[k / 4] |= static_cast<uint32_t>(p[c + k]) << (8 * (k & 3));
+    w[0] = c < n ? w[0] >> s : 0u;
   }
 }
 
