@@ -172,19 +172,41 @@ def load():
 def _ptr(x) -> int | None:
     if x is None:
         return None
+    f = getattr(x, "data_ptr", None)
+    if f is not None:
+        return f()
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
-        return x.data_ptr()
     if isinstance(x, ctypes.Structure):
         return ctypes.addressof(x)
     raise TypeError(f"cannot take a device pointer from {type(x)!r}")
 
 
+_current = None
+
+
+def _now():
+    """(raw handle of the current stream, index of the current device) of torch,
+    without the objects around them where torch offers that."""
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.current_stream()
+        c = torch._C
+        if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+            def f():
+                d = c._cuda_getDevice()
+                return c._cuda_getCurrentRawStream(d), d
+        else:
+            def f():
+                return torch.cuda.current_stream().cuda_stream, torch.cuda.current_device()
+        _current = f
+    return _current()
+
+
 def _stream(s) -> int | None:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _now()[0]
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -217,6 +239,8 @@ def _room(fn: str, what: str, t, nbytes: int) -> None:
     points take bare pointers and cannot see allocation sizes; integer
     pointers stay the caller's responsibility."""
     if nbytes <= 0 or t is None or not hasattr(t, "untyped_storage"):
+        return
+    if t.nbytes >= nbytes and t.is_contiguous():   # its own elements already suffice
         return
     st = t.untyped_storage()
     have = st.nbytes() - (t.data_ptr() - st.data_ptr())
@@ -345,26 +369,57 @@ def amp_gemm_blockwise(M, N, K, A, at, lda, sA, ldsA, a_block, B, bt, ldb, sB, l
         ldsB, int(b_block), _ptr(C), ct, ldc, _stream(stream)))
 
 
+def _room_mat(fn: str, what: str, t, rows, cols, ld, dt) -> None:
+    """_room of a matrix; a tensor whose own elements suffice costs one comparison."""
+    if t is None:
+        return
+    need = _mat(rows, cols, ld, dt)
+    if getattr(t, "nbytes", 0) < need or not t.is_contiguous():
+        _room(fn, what, t, need)
+
+
+def _here(fn: str, *operands) -> None:
+    """Raise where a torch operand is not on the current device (a host tensor
+    or another GPU's would fault in the kernel)."""
+    dev = None
+    for t in operands:
+        where = getattr(t, "get_device", None)
+        if where is None:
+            if isinstance(t, Fp8Tiles):
+                _here(fn, *t.tensors)
+            continue
+        where = where()
+        if dev is None:
+            dev = _now()[1] if where >= 0 else None
+        if where != dev:
+            raise ValueError(f"{fn}: an operand is on {t.device}, not on the current GPU")
+
+
 def _room_tiles(fn: str, what: str, t, rows, cols, nb=None) -> None:
     """The same for an FP8 matrix [rows, cols] (``nb``: its tiles along K)."""
     if t is None or rows <= 0 or cols <= 0:
         return
     q, s = t.tensors
-    _room(fn, what + ".q", q, (rows - 1) * t.ldq + cols)
-    _room(fn, what + ".s", s, 4 * ((nb if nb else -(-cols // 128)) - 1) * t.lds + 4 * rows)
+    need = (rows - 1) * t.ldq + cols
+    if getattr(q, "nbytes", 0) < need or not q.is_contiguous():
+        _room(fn, what + ".q", q, need)
+    need = 4 * ((nb if nb else -(-cols // 128)) - 1) * t.lds + 4 * rows
+    if getattr(s, "nbytes", 0) < need or not s.is_contiguous():
+        _room(fn, what + ".s", s, need)
 
 
 def amp_rmsnorm(x, xt, rows, cols, ldx, res, ldr, gamma, gt, eps, h=None, ldh=0, y=None, yt=BF16,
                 ldy=0, d_scale=None, d_amax=None, yq=None, ckpt=None, rstd=None, stream=None):
     f = "amp_rmsnorm"
-    _room(f, "x", x, _mat(rows, cols, ldx, xt))
-    _room(f, "res", res, _mat(rows, cols, ldr, xt))
-    _room(f, "gamma", gamma, _vec(cols, gt))
-    _room(f, "h", h, _mat(rows, cols, ldh, xt))
-    _room(f, "y", y, _mat(rows, cols, ldy, yt))
-    _room(f, "rstd", rstd, _vec(rows, F32))
+    _room_mat(f, "x", x, rows, cols, ldx, xt)
+    _room_mat(f, "res", res, rows, cols, ldr, xt)
+    _room_mat(f, "gamma", gamma, 1, cols, cols, gt)
+    _room_mat(f, "h", h, rows, cols, ldh, xt)
+    _room_mat(f, "y", y, rows, cols, ldy, yt)
+    _room_mat(f, "rstd", rstd, 1, rows, rows, F32)
     _room_tiles(f, "yq", yq, rows, cols)
     _room_tiles(f, "ckpt", ckpt, rows, cols)
+    _here(f, x, res, gamma, h, y, d_scale, d_amax, yq, ckpt, rstd)
     _check(f, load().amp_rmsnorm(
         _ptr(x), xt, rows, cols, ldx, _ptr(res), ldr, _ptr(gamma), gt, eps, _ptr(h), ldh, _ptr(y),
         yt, ldy, _ptr(d_scale), _ptr(d_amax), _ptr(yq), _ptr(ckpt), _ptr(rstd), _stream(stream)))
@@ -373,16 +428,17 @@ def amp_rmsnorm(x, xt, rows, cols, ldx, res, ldr, gamma, gt, eps, h=None, ldh=0,
 def amp_rmsnorm_backward(dy, dt, rows, cols, lddy, h, ldh, ckpt, gamma, gt, rstd, dres=None, lddr=0,
                          dx=None, lddx=0, dgamma=None, d_work=None, stream=None):
     f = "amp_rmsnorm_backward"
-    _room(f, "dy", dy, _mat(rows, cols, lddy, dt))
-    _room(f, "h", h, _mat(rows, cols, ldh, dt))
+    _room_mat(f, "dy", dy, rows, cols, lddy, dt)
+    _room_mat(f, "h", h, rows, cols, ldh, dt)
     _room_tiles(f, "ckpt", ckpt, rows, cols)
-    _room(f, "gamma", gamma, _vec(cols, gt))
-    _room(f, "rstd", rstd, _vec(rows, F32))
-    _room(f, "dres", dres, _mat(rows, cols, lddr, dt))
-    _room(f, "dx", dx, _mat(rows, cols, lddx, dt))
+    _room_mat(f, "gamma", gamma, 1, cols, cols, gt)
+    _room_mat(f, "rstd", rstd, 1, rows, rows, F32)
+    _room_mat(f, "dres", dres, rows, cols, lddr, dt)
+    _room_mat(f, "dx", dx, rows, cols, lddx, dt)
     if dgamma is not None:
-        _room(f, "dgamma", dgamma, _vec(cols, F32))
+        _room_mat(f, "dgamma", dgamma, 1, cols, cols, F32)
         _room(f, "d_work", d_work, _vec(min(rows, RMSNORM_PARTIALS) * cols, F32))
+    _here(f, dy, h, ckpt, gamma, rstd, dres, dx, dgamma, d_work)
     _check(f, load().amp_rmsnorm_backward(
         _ptr(dy), dt, rows, cols, lddy, _ptr(h), ldh, _ptr(ckpt), _ptr(gamma), gt, _ptr(rstd),
         _ptr(dres), lddr, _ptr(dx), lddx, _ptr(dgamma), _ptr(d_work), _stream(stream)))
@@ -391,10 +447,11 @@ def amp_rmsnorm_backward(dy, dt, rows, cols, lddy, h, ldh, ckpt, gamma, gt, rstd
 def amp_swiglu(x, xt, rows, cols, ldx, y=None, yt=BF16, ldy=0, d_scale=None, d_amax=None, yq=None,
                ckpt=None, stream=None):
     f = "amp_swiglu"
-    _room(f, "x", x, _mat(rows, 2 * cols, ldx, xt))
-    _room(f, "y", y, _mat(rows, cols, ldy, yt))
+    _room_mat(f, "x", x, rows, 2 * cols, ldx, xt)
+    _room_mat(f, "y", y, rows, cols, ldy, yt)
     _room_tiles(f, "yq", yq, rows, cols)
     _room_tiles(f, "ckpt", ckpt, rows, 2 * cols, 2 * -(-cols // 128))
+    _here(f, x, y, d_scale, d_amax, yq, ckpt)
     _check(f, load().amp_swiglu(
         _ptr(x), xt, rows, cols, ldx, _ptr(y), yt, ldy, _ptr(d_scale), _ptr(d_amax), _ptr(yq),
         _ptr(ckpt), _stream(stream)))
@@ -403,13 +460,14 @@ def amp_swiglu(x, xt, rows, cols, ldx, y=None, yt=BF16, ldy=0, d_scale=None, d_a
 def amp_swiglu_backward(dy, dt, rows, cols, lddy, x, ldx, ckpt, dx=None, lddx=0, dxq=None,
                         dxqt=None, yqt=None, stream=None):
     f = "amp_swiglu_backward"
-    _room(f, "dy", dy, _mat(rows, cols, lddy, dt))
-    _room(f, "x", x, _mat(rows, 2 * cols, ldx, dt))
+    _room_mat(f, "dy", dy, rows, cols, lddy, dt)
+    _room_mat(f, "x", x, rows, 2 * cols, ldx, dt)
     _room_tiles(f, "ckpt", ckpt, rows, 2 * cols, 2 * -(-cols // 128))
-    _room(f, "dx", dx, _mat(rows, 2 * cols, lddx, dt))
+    _room_mat(f, "dx", dx, rows, 2 * cols, lddx, dt)
     _room_tiles(f, "dxq", dxq, rows, 2 * cols)
     _room_tiles(f, "dxqt", dxqt, 2 * cols, rows)
     _room_tiles(f, "yqt", yqt, cols, rows)
+    _here(f, dy, x, ckpt, dx, dxq, dxqt, yqt)
     _check(f, load().amp_swiglu_backward(
         _ptr(dy), dt, rows, cols, lddy, _ptr(x), ldx, _ptr(ckpt), _ptr(dx), lddx, _ptr(dxq),
         _ptr(dxqt), _ptr(yqt), _stream(stream)))
@@ -418,9 +476,10 @@ def amp_swiglu_backward(dy, dt, rows, cols, lddy, x, ldx, ckpt, dx=None, lddx=0,
 def amp_requantize_blockwise(x, rows, cols, d_row, col, ct, qt, stream=None):
     f = "amp_requantize_blockwise"
     _room_tiles(f, "x", x, rows, cols)
-    _room(f, "d_row", d_row, _vec(rows, F32))
-    _room(f, "col", col, _vec(cols, ct))
+    _room_mat(f, "d_row", d_row, 1, rows, rows, F32)
+    _room_mat(f, "col", col, 1, cols, cols, ct)
     _room_tiles(f, "qt", qt, cols, rows)
+    _here(f, x, d_row, col, qt)
     _check(f, load().amp_requantize_blockwise(_ptr(x), rows, cols, _ptr(d_row), _ptr(col), ct,
                                               _ptr(qt), _stream(stream)))
 

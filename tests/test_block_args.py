@@ -123,3 +123,18 @@ def test_binding_refuses_tensors_smaller_than_the_call_spans():
         torch.zeros(300, 4, dtype=u8), torch.zeros(300), 4, 300))
     refused("qt.s", amp.amp_requantize_blockwise, ok, 4, 300, None, None, 0, amp.Fp8Tiles(
         torch.zeros(300, 4, dtype=u8), torch.zeros(299), 4, 300))
+
+
+def test_binding_refuses_tensors_that_are_not_on_the_current_gpu():
+    """Big enough, but host memory: the kernel would fault."""
+    x, g, r = torch.zeros(4, 300, dtype=torch.bfloat16), torch.zeros(300), torch.zeros(4)
+    t = amp.Fp8Tiles(torch.zeros(4, 300, dtype=torch.uint8), torch.zeros(3, 4), 300, 4)
+    tt = amp.Fp8Tiles(torch.zeros(300, 4, dtype=torch.uint8), torch.zeros(1, 300), 4, 300)
+    gt = amp.Fp8Tiles(torch.zeros(4, 150, dtype=torch.uint8), torch.zeros(2, 4), 150, 4)
+    for fn, a, k in ((amp.amp_rmsnorm, (x, amp.BF16, 4, 300, 300, None, 0, g, amp.F32, 1e-5), dict(yq=t)),
+                     (amp.amp_rmsnorm_backward, (x, amp.BF16, 4, 300, 300, x, 300, None, g, amp.F32, r), dict(dx=x, lddx=300)),
+                     (amp.amp_swiglu, (x, amp.BF16, 4, 150, 300), dict(yq=gt)),
+                     (amp.amp_swiglu_backward, (x[:, :150], amp.BF16, 4, 150, 300, x, 300, None), dict(dx=x, lddx=300)),
+                     (amp.amp_requantize_blockwise, (t, 4, 300, None, None, 0, tt), {})):
+        with pytest.raises(ValueError, match="on cpu"):
+            fn(*a, **k)
