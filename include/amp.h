@@ -405,7 +405,7 @@ int amp_gemm_blockwise(int64_t M, int64_t N, int64_t K,
  * its result that a GEMM, the residual stream or the backward pass reads.
  * FP8 checkpoints are what the backward pass reads in place of 16-bit
  * activations.  Sums and statistics are FP32; each output is rounded once.
- * One token is rows == 1. */
+ * One token is rows == 1; cols is at most 2^26 (else AMP_EUNSUPPORTED). */
 
 /* A matrix in FP8 with one FP32 scale_inv per 1x128 tile along its contiguous
  * dimension, as amp_quantize_blockwise writes it with block == 0 and
@@ -459,7 +459,7 @@ int amp_rmsnorm(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx,
  * d_work: FP32 [min(rows, AMP_RMSNORM_PARTIALS), cols], the partial sums of
  *    dgamma (needed with dgamma); calls that may overlap need one each.  The
  *    sums are added in a fixed order: the result is reproducible.
- * cols == 0 is a no-op. */
+ * Apart from dx no output may overlap an input.  cols == 0 is a no-op. */
 #define AMP_RMSNORM_PARTIALS 256
 int amp_rmsnorm_backward(const void* dy, int dt, int64_t rows, int64_t cols, int64_t lddy,
                          const void* h, int64_t ldh, const amp_fp8_tiles* ckpt,
@@ -494,7 +494,9 @@ int amp_swiglu(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx, v
  *      operand of the product before the activation;
  *   yqt: y^T [cols, rows] in 1x128 tiles, y recomputed: the wgrad operand of
  *      the product after it.
- * rows or cols == 0 is a no-op. */
+ * Apart from dx no output may overlap an input.  The sigmoid is formed from
+ * the hardware's exponential and reciprocal: s is within a few 2^-24 + (1 - s)
+ * |g| 2^-22 of its value, relatively.  rows or cols == 0 is a no-op. */
 int amp_swiglu_backward(const void* dy, int dt, int64_t rows, int64_t cols, int64_t lddy,
                         const void* x, int64_t ldx, const amp_fp8_tiles* ckpt, void* dx,
                         int64_t lddx, const amp_fp8_tiles* dxq, const amp_fp8_tiles* dxqt,
@@ -505,8 +507,8 @@ int amp_swiglu_backward(const void* dy, int dt, int64_t rows, int64_t cols, int6
  * x: [rows, cols] in tiles; qt: [cols, rows] (tiles along the rows of x).
  * d_row: [rows] FP32, col: [cols] of ct in {F32, F16, BF16}; NULL means 1.
  * With d_row = rstd and col = gamma, v is the output of amp_rmsnorm
- * recomputed from the checkpoint of its input.  rows or cols == 0 is a
- * no-op. */
+ * recomputed from the checkpoint of its input.  qt may not overlap x.  rows
+ * or cols == 0 is a no-op. */
 int amp_requantize_blockwise(const amp_fp8_tiles* x, int64_t rows, int64_t cols,
                              const float* d_row, const void* col, int ct,
                              const amp_fp8_tiles* qt, void* stream);

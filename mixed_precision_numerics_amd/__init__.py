@@ -416,6 +416,8 @@ def amp_rmsnorm(x, xt, rows, cols, ldx, res, ldr, gamma, gt, eps, h=None, ldh=0,
     _room_mat(f, "gamma", gamma, 1, cols, cols, gt)
     _room_mat(f, "h", h, rows, cols, ldh, xt)
     _room_mat(f, "y", y, rows, cols, ldy, yt)
+    _room_mat(f, "d_scale", d_scale, 1, 1, 1, F32)
+    _room_mat(f, "d_amax", d_amax, 1, 1, 1, F32)
     _room_mat(f, "rstd", rstd, 1, rows, rows, F32)
     _room_tiles(f, "yq", yq, rows, cols)
     _room_tiles(f, "ckpt", ckpt, rows, cols)
@@ -449,6 +451,8 @@ def amp_swiglu(x, xt, rows, cols, ldx, y=None, yt=BF16, ldy=0, d_scale=None, d_a
     f = "amp_swiglu"
     _room_mat(f, "x", x, rows, 2 * cols, ldx, xt)
     _room_mat(f, "y", y, rows, cols, ldy, yt)
+    _room_mat(f, "d_scale", d_scale, 1, 1, 1, F32)
+    _room_mat(f, "d_amax", d_amax, 1, 1, 1, F32)
     _room_tiles(f, "yq", yq, rows, cols)
     _room_tiles(f, "ckpt", ckpt, rows, 2 * cols, 2 * -(-cols // 128))
     _here(f, x, y, d_scale, d_amax, yq, ckpt)

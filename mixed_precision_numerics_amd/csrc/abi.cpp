@@ -59,6 +59,10 @@ bool is_fp8(int t) { return t == AMP_E4M3 || t == AMP_E5M2; }
 // error, not a memory fault.  NULL passes (optional arguments).
 bool al(const void* p, uintptr_t a) { return p == nullptr || amp::aligned(p, a); }
 
+// Columns of a norm or gated activation: a launch counts its threads in 32
+// bits, of which a column takes up to 32 (the sum of its gamma gradient).
+constexpr int64_t kMostCols = 1 << 26;
+
 // An FP8 matrix [rows, cols] in 1x128 tiles (NULL: absent, valid).
 int tiles_status(const amp_fp8_tiles* t, int64_t rows, int64_t cols) {
   if (!t) return AMP_OK;
@@ -410,7 +414,7 @@ int amp_rmsnorm(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx, 
                 const amp_fp8_tiles* ckpt, float* rstd, void* stream) {
   if (!al(d_scale, 4) || !al(d_amax, 4) || !al(rstd, 4)) return AMP_EINVAL;
   if (rows < 0 || cols < 0 || !(eps >= 0.0f && eps < 3.0e38f)) return AMP_EINVAL;
-  if (!is_cast_in(xt) || (gamma && !is_cast_in(gt)) || (y && !is_cast_out(yt))) return AMP_EUNSUPPORTED;
+  if (cols > kMostCols || !is_cast_in(xt) || (gamma && !is_cast_in(gt)) || (y && !is_cast_out(yt))) return AMP_EUNSUPPORTED;
   if (rows == 0 || cols == 0) return AMP_OK;
   if (!x || (!h && !y && !yq && !ckpt && !d_amax && !rstd)) return AMP_EINVAL;
   if (ldx < cols || (res && ldr < cols) || (h && ldh < cols) || (y && ldy < cols)) return AMP_EINVAL;
@@ -429,7 +433,7 @@ int amp_rmsnorm_backward(const void* dy, int dt, int64_t rows, int64_t cols, int
                          float* dgamma, float* d_work, void* stream) {
   if (!al(rstd, 4) || !al(dgamma, 4) || !al(d_work, 4)) return AMP_EINVAL;
   if (rows < 0 || cols < 0) return AMP_EINVAL;
-  if (!is_cast_in(dt) || (gamma && !is_cast_in(gt))) return AMP_EUNSUPPORTED;
+  if (cols > kMostCols || !is_cast_in(dt) || (gamma && !is_cast_in(gt))) return AMP_EUNSUPPORTED;
   if (cols == 0 || (rows == 0 && !dgamma)) return AMP_OK;
   if (rows > 0) {
     if (!dy || !rstd || (!dx && !dgamma) || (dgamma && !d_work)) return AMP_EINVAL;
@@ -449,7 +453,7 @@ int amp_swiglu(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx, v
                void* stream) {
   if (!al(d_scale, 4) || !al(d_amax, 4)) return AMP_EINVAL;
   if (rows < 0 || cols < 0) return AMP_EINVAL;
-  if (!is_cast_in(xt) || (y && !is_cast_out(yt))) return AMP_EUNSUPPORTED;
+  if (cols > kMostCols || !is_cast_in(xt) || (y && !is_cast_out(yt))) return AMP_EUNSUPPORTED;
   if (rows == 0 || cols == 0) return AMP_OK;
   if (!x || (!y && !yq && !ckpt && !d_amax)) return AMP_EINVAL;
   if (ldx < 2 * cols || (y && ldy < cols)) return AMP_EINVAL;
@@ -465,7 +469,7 @@ int amp_swiglu_backward(const void* dy, int dt, int64_t rows, int64_t cols, int6
                         const amp_fp8_tiles* dxq, const amp_fp8_tiles* dxqt, const amp_fp8_tiles* yqt,
                         void* stream) {
   if (rows < 0 || cols < 0) return AMP_EINVAL;
-  if (!is_cast_in(dt) || (dxq && cols % 128 != 0)) return AMP_EUNSUPPORTED;
+  if (cols > kMostCols || !is_cast_in(dt) || (dxq && cols % 128 != 0)) return AMP_EUNSUPPORTED;
   if (rows == 0 || cols == 0) return AMP_OK;
   if (!dy || (x != nullptr) == (ckpt != nullptr) || (!dx && !dxq && !dxqt && !yqt)) return AMP_EINVAL;
   if (lddy < cols || (x && ldx < 2 * cols) || (dx && lddx < 2 * cols)) return AMP_EINVAL;
@@ -484,7 +488,7 @@ int amp_requantize_blockwise(const amp_fp8_tiles* x, int64_t rows, int64_t cols,
                              const void* col, int ct, const amp_fp8_tiles* qt, void* stream) {
   if (!al(d_row, 4)) return AMP_EINVAL;
   if (rows < 0 || cols < 0) return AMP_EINVAL;
-  if (col && !is_cast_in(ct)) return AMP_EUNSUPPORTED;
+  if (cols > kMostCols || (col && !is_cast_in(ct))) return AMP_EUNSUPPORTED;
   if (rows == 0 || cols == 0) return AMP_OK;
   if (!x || !qt) return AMP_EINVAL;
   if (int e = tiles_status(x, rows, cols)) return e;

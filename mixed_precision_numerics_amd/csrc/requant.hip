@@ -54,9 +54,9 @@ __global__ __launch_bounds__(kRegThreads) void requant_region(const RequantArgs 
 
 hipError_t launch_requantize(const amp_fp8_tiles& x, int64_t rows, int64_t cols, const float* row, const void* col, int ct,
                              const amp_fp8_tiles& qt, hipStream_t s) {
-  constexpr int64_t kMost = 65535 * static_cast<int64_t>(kTileK);   // rows a launch: the grid's y bound
-  for (int64_t r0 = 0; r0 < rows; r0 += kMost) {
-    RequantArgs a{x, qt, rows - r0 < kMost ? rows - r0 : kMost, cols, row ? row + r0 : nullptr, col, ct};
+  const int64_t most = grid_rows((cols + kTileK - 1) / kTileK) * kTileK;   // rows a launch
+  for (int64_t r0 = 0; r0 < rows; r0 += most) {
+    RequantArgs a{x, qt, rows - r0 < most ? rows - r0 : most, cols, row ? row + r0 : nullptr, col, ct};
     a.x.q += r0 * x.ldq;
     a.x.s += r0;
     a.qt.q += r0;

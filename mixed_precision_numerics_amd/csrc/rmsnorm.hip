@@ -412,7 +412,7 @@ __global__ __launch_bounds__(S > 1 ? 512 : 1024) void rmsnorm_back_rows(const No
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float dy[E], h[E], d[E];
-          widen<XT>(w.dy[v], dy);
+        widen<XT>(w.dy[v], dy);
         w.h[v].values(a, h);
         dx_of<E>(dy, h, gm[v], w.r, m, d);
         if (a.dres) {

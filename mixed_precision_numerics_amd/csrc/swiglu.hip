@@ -338,13 +338,11 @@ hipError_t in_slices(int64_t rows, int64_t most, F f) {
   return hipSuccess;
 }
 
-constexpr int kGridY = 65535;
-
 template <int XT, int W, int R>
 hipError_t run_swiglu(const GateArgs& whole, hipStream_t s) {
   constexpr int E = kVec<XT>, per = 256 / W * R;
   const bool full = whole.cols % (W * E) == 0;
-  return in_slices(whole.rows, static_cast<int64_t>(kGridY) * per, [&](int64_t r0, int64_t rows) {
+  return in_slices(whole.rows, grid_rows((whole.cols + W * E - 1) / (W * E)) * per, [&](int64_t r0, int64_t rows) {
     GateArgs a = whole;
     a.rows = rows;
     a.x = elem<XT>(a.x, r0 * a.ldx);
@@ -370,7 +368,7 @@ template <int XT, bool CK, int W, int R>
 hipError_t run_swiglu_back(const GateArgs& whole, hipStream_t s) {
   constexpr int E = kVec<XT>, per = 256 / W * R;
   const bool full = whole.cols % (W * E) == 0;
-  return in_slices(whole.rows, static_cast<int64_t>(kGridY) * per, [&](int64_t r0, int64_t rows) {
+  return in_slices(whole.rows, grid_rows((whole.cols + W * E - 1) / (W * E)) * per, [&](int64_t r0, int64_t rows) {
     GateArgs a = whole;
     a.rows = rows;
     a.dy = elem<XT>(a.dy, r0 * a.lddy);
@@ -386,7 +384,7 @@ hipError_t run_swiglu_back(const GateArgs& whole, hipStream_t s) {
 template <int XT, bool CK>
 hipError_t dispatch_swiglu_back(const GateArgs& whole, hipStream_t s) {
   if (whole.dxq.q || whole.dxqt.q || whole.yqt.q) {
-    return in_slices(whole.rows, static_cast<int64_t>(kGridY) * kTileK, [&](int64_t r0, int64_t rows) {
+    return in_slices(whole.rows, grid_rows((whole.cols + kTileK - 1) / kTileK) * kTileK, [&](int64_t r0, int64_t rows) {
       GateArgs a = whole;
       a.rows = rows;
       a.dy = elem<XT>(a.dy, r0 * a.lddy);

@@ -4,7 +4,8 @@
 //
 // Rows need no alignment: gfx950 loads and stores dwords and wider at any
 // byte address, so a row of odd length costs extra cache lines, not another
-// code path.  Only a row's last, partial vector goes element by element.
+// code path.  A row's last, partial vector is loaded as the whole vector that
+// ends with the row and stored element by element.
 //
 // The operators are HBM-bound only as long as the vector ALUs keep up (about
 // 50 operations per element at one 16-bit stream's rate), so addresses are a
@@ -35,6 +36,14 @@ __host__ __device__ __forceinline__ void* elem(void* p, int64_t i) { return stat
 // p advanced by i elements of the run-time type t.
 __device__ __forceinline__ const void* elem_of(int t, const void* p, int64_t i) {
   return static_cast<const uint8_t*>(p) + i * (t == AMP_F32 ? 4 : 2);
+}
+
+// Row blocks of a grid with x blocks along the columns: within the bound of
+// the y dimension and with the grid's threads (512 a block at most) countable
+// in 32 bits.
+inline int64_t grid_rows(int64_t x) {
+  const int64_t y = (1 << 22) / x;
+  return y < 1 ? 1 : y > 65535 ? 65535 : y;
 }
 
 // The number of columns left, as the 32-bit bound that the helpers take (they

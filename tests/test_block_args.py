@@ -138,3 +138,18 @@ def test_binding_refuses_tensors_that_are_not_on_the_current_gpu():
                      (amp.amp_requantize_blockwise, (t, 4, 300, None, None, 0, tt), {})):
         with pytest.raises(ValueError, match="on cpu"):
             fn(*a, **k)
+
+
+@pytest.mark.parametrize("call", [norm, norm_back, gate, gate_back, requant])
+def test_columns_beyond_a_launch_are_refused(call):
+    assert call(cols=(1 << 26) + 1) == EUNSUP
+
+
+def test_binding_refuses_scalars_without_room():
+    x, none = torch.zeros(2, 256, dtype=torch.bfloat16), torch.zeros(0)
+    y = torch.zeros(2, 256, dtype=torch.bfloat16)
+    for k in ("d_scale", "d_amax"):
+        with pytest.raises(ValueError, match=k):
+            amp.amp_rmsnorm(x, amp.BF16, 2, 256, 256, None, 0, None, 0, 1e-5, y=y, ldy=256, **{k: none})
+        with pytest.raises(ValueError, match=k):
+            amp.amp_swiglu(x, amp.BF16, 2, 128, 256, y=y, ldy=256, **{k: none})

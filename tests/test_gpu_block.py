@@ -281,6 +281,25 @@ def test_norm_backward(dt, saved, rows, cols):
     check_values(dy.values(), FMT[dt], w0, dx_err(dy.v, hh, gamma.v[0], r, None, w0), "dx in place of dy")
 
 
+@pytest.mark.parametrize("cols", [264, 9000, 20483, 40003])
+@pytest.mark.parametrize("saved", ["stored", "checkpoint"])
+def test_norm_backward_in_place_with_gamma_gradient(saved, cols):
+    """dx replaces dy, which the gamma gradient reads too, in one call."""
+    rows, dt = 301, amp.BF16
+    hv = rand(1, rows, cols)
+    h = Mat(rows, cols, dt, 0, hv) if saved == "stored" else None
+    ck = Tiles(rows, cols, amp.E4M3, 0, v=F.f32(hv)) if saved == "checkpoint" else None
+    hh = h.v if h else ck.v
+    dy, ones = Mat(rows, cols, dt, 0, rand(2, rows, cols)), np.ones(cols)
+    r = F.f32(B.rmsnorm(hh, ones, EPS)[1])
+    dgamma, work = Mat(1, cols, amp.F32), Mat(amp.RMSNORM_PARTIALS, cols, amp.F32)
+    amp.amp_rmsnorm_backward(dy.d, dt, rows, cols, dy.ld, h.d if h else None, h.ld if h else 0, ck.arg if ck else None, None, dt,
+                             dev(r.astype(np.float32)), None, 0, dy.d, dy.ld, dgamma.d, work.d)
+    wx, wg = B.rmsnorm_backward(dy.v, hh, ones, r)
+    check_values(dy.values(), F.BF16, wx, dx_err(dy.v, hh, ones, r, None, wx), "dx in place of dy")
+    check_values(dgamma.values()[0], F.F32, wg, (rows + 8) * U * np.abs(dy.v * hh * r[:, None]).sum(0), "dgamma")
+
+
 def test_norm_backward_over_many_rows_and_shared_gamma():
     """More rows than partial sums: every block walks several."""
     rows, cols, dt = 5003, 264, amp.BF16
@@ -610,3 +629,56 @@ def test_ffn_block_captured_and_replayed_on_another_stream():
         torch.cuda.synchronize()
         for (b, _, _), w in zip(made, want):
             assert all(torch.equal(b[k], w[k]) for k in RESULTS)
+
+
+def test_more_rows_than_one_launch_takes():
+    """The last rows of a call that is launched in slices, bit for bit those of
+    a call on them alone."""
+    bf = torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(3)
+
+    def randn(n):
+        return torch.randn(n, generator=gen, device="cuda").to(bf)
+
+    def tail(rows, first, run):
+        whole, part = run(0, rows), run(first, rows)
+        for w, p in zip(whole, part):
+            assert torch.equal(w[..., first:] if w.shape[-1] != p.shape[-1] else w[first:], p)
+
+    rows = (1 << 21) + 70                              # one column: rows of one element
+    x = randn(rows)
+
+    def norm(a, b):
+        n = b - a
+        y, q, s = torch.empty(n, dtype=bf, device="cuda"), torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty(n, device="cuda")
+        amp.amp_rmsnorm(x[a:], amp.BF16, n, 1, 1, None, 0, None, 0, 1e-5, y=y, ldy=1, yq=amp.Fp8Tiles(q, s, 1, n))
+        return y, q, s
+    tail(rows, rows - 5, norm)
+
+    x2, dy = randn(2 * rows), randn(rows)
+
+    def gate(a, b):
+        n = b - a
+        y, dx = torch.empty(n, dtype=bf, device="cuda"), torch.empty(n, 2, dtype=bf, device="cuda")
+        amp.amp_swiglu(x2[2 * a:], amp.BF16, n, 1, 2, y=y, ldy=1)
+        amp.amp_swiglu_backward(dy[a:], amp.BF16, n, 1, 1, x2[2 * a:], 2, None, dx, 2)
+        return y, dx
+    tail(rows, rows - 5, gate)
+
+    rows = 65535 * 128 + 300
+    codes = torch.randint(0, 120, (rows,), generator=gen, device="cuda", dtype=torch.uint8)
+    scale, x2, dy = torch.rand(rows, generator=gen, device="cuda") + 0.5, randn(2 * rows), randn(rows)
+
+    def transposed(a, b):
+        n = b - a
+        kb = -(-n // 128)
+        q, s = torch.empty(3, n, dtype=torch.uint8, device="cuda"), torch.empty(kb, 3, device="cuda")
+        amp.amp_requantize_blockwise(amp.Fp8Tiles(codes[a:], scale[a:], 1, n), n, 1, None, None, 0,
+                                     amp.Fp8Tiles(q, s, n, 3))
+        amp.amp_swiglu_backward(dy[a:], amp.BF16, n, 1, 1, x2[2 * a:], 2, None, None, 0, None,
+                                amp.Fp8Tiles(q[1:], s[0, 1:], n, 3))
+        return (q,) + tuple(s[-3:, k].clone() for k in range(3))
+    first = 65535 * 128                                # a tile's first row
+    whole, part = transposed(0, rows), transposed(first, rows)
+    assert torch.equal(whole[0][:, first:], part[0])
+    assert all(torch.equal(w, p) for w, p in zip(whole[1:], part[1:]))
