@@ -24,12 +24,13 @@ struct GateArgs {
 // s = 1 / (1 + e), e = exp(-g), from the hardware's exponential and
 // reciprocal (each within an ulp; the scaled argument adds |g| 2^-24, so s is
 // good to a few 2^-23 over the range where it is not negligible).  g = -inf
-// gives s = 0 and, as in the formula, 0 * inf = NaN for g s.
+// gives s = 0 and, as in the formula, 0 * inf = NaN for g s.  Where e overflows
+// s is 0 and e s a NaN, of which the minimum makes 1 (a NaN g leaves one in s).
 struct Gate { float s, om; };   // s and 1 - s
 __device__ __forceinline__ Gate gate(float g) {
   const float e = __builtin_amdgcn_exp2f(g * -1.4426950408889634f);
   const float s = __builtin_amdgcn_rcpf(1.0f + e);
-  return {s, e > 1.7e38f ? 1.0f : e * s};
+  return {s, __builtin_fminf(e * s, 1.0f)};
 }
 
 // Index along K of the tile that holds column c of half `half`: the tiles
@@ -62,7 +63,8 @@ __device__ __forceinline__ void store_row_tiles(const amp_fp8_tiles& o, int64_t 
 
 // W threads cover W vectors of a row, 256 / W rows side by side and R of
 // those groups one after the other; blockIdx.x runs along the row.  FULL: the
-// row is whole spans of W vectors.
+// row is whole spans of W vectors.  HBM-bound: 8192 x 14336 BF16 with tiles and
+// checkpoint 138 us = 6.0 TB/s; one row of 14336 3.1 us, the launch.
 template <int XT, int W, int R, bool FULL>
 __global__ __launch_bounds__(256) void swiglu_rows(const GateArgs a) {
   constexpr int E = kVec<XT>, S = 256 / W;
@@ -119,7 +121,8 @@ __global__ __launch_bounds__(256) void swiglu_rows(const GateArgs a) {
 }
 
 // Backward with dx in the gradient's own type only: element-wise, laid out
-// as above.
+// as above; HBM-bound (777 x 2049 FP16 stored: 6.6 us, 2.8 at the copy rate;
+// rows of odd length begin at any alignment).
 template <int XT, bool CK, int W, int R, bool FULL>
 __global__ __launch_bounds__(256) void swiglu_back_rows(const GateArgs a) {
   constexpr int E = kVec<XT>, S = 256 / W;
@@ -167,7 +170,7 @@ __global__ __launch_bounds__(256) void swiglu_back_rows(const GateArgs a) {
       const Gate p = gate(g[k]);
       const float t = dy[k] * p.s;
       du[k] = t * g[k];
-      dg[k] = t * u[k] * (1.0f + g[k] * p.om);
+      dg[k] = t * u[k] * __builtin_fmaf(g[k], p.om, 1.0f);
     }
     void* p = elem<XT>(a.y, row * a.ldy + c0);
     store_vec<XT, FULL>(p, c, n, narrow<XT>(dg));
@@ -176,21 +179,27 @@ __global__ __launch_bounds__(256) void swiglu_back_rows(const GateArgs a) {
 }
 
 // Backward with FP8 operands: one 128x128 region of dy, g and u per block,
-// read once.  dg and du are formed in registers and leave from there in every
-// form asked for: dx in dy's type, dx in row tiles (dgrad), dx^T in tiles
-// along the rows (wgrad); then y is recomputed from g and u for y^T, so that
-// no more than two of the three are held at a time and two blocks share a CU
-// (stored inputs take twice the registers: one block there; held to two they
-// spilled, 4096 x 14336 BF16 330 us instead of 184).
+// read once.  DX: some form of dx is asked for, not y^T alone.  dg and du are
+// formed in registers and leave from there in every form asked for: dx in dy's
+// type, dx in row tiles (dgrad), dx^T in tiles along the rows (wgrad).  Then y
+// leaves as y^T.  From a checkpoint dg, du and two blocks a CU take every
+// register, so y is formed again from g and u, except for the kKeep rows a
+// thread that the LDS has room for; stored inputs take twice the registers and
+// one block a CU (held to two they spilled, 4096 x 14336 BF16 330 us), whose
+// LDS holds all of y.
 //
-// Bound by the vector ALUs (79 % busy at 8192 x 14336 from a checkpoint, 60
-// operations per element of y, 254 us = 4.3 TB/s): the sigmoid's two
-// quarter-rate instructions, formed twice, are a quarter of it.
-template <int XT, bool CK>
+// Bound by the vector ALUs and the two blocks' turns on them (8192 x 14336
+// from a checkpoint: 236 us = 4.6 TB/s, about 57 operations per element of y,
+// the sigmoid's two quarter-rate instructions a fifth of it; 257 with no row
+// kept, 237 with two).  Stored, 4096 x 14336 BF16: 178 us with all of y kept,
+// 184 with none.
+template <int XT, bool CK, bool DX>
 __global__ __launch_bounds__(kRegThreads, CK ? 4 : 2) void swiglu_back_region(const GateArgs a) {
   __shared__ RegLds<2> l;
   __shared__ uint32_t rmax[2][kTileK];
   __shared__ float rscale[2][kTileK], gscale[2][kTileK];
+  constexpr int kKeep = CK ? 1 : kRegRows, kFirst = kRegRows - kKeep;   // y is kept of rows kFirst on
+  __shared__ u32x4 kept[kKeep][kRegCols / 4][kRegThreads];
   constexpr int GB = CK ? 1 : kBytes<XT>;
   const Region g(a.rows, a.cols, true);
   const int t = threadIdx.x;
@@ -223,7 +232,7 @@ __global__ __launch_bounds__(kRegThreads, CK ? 4 : 2) void swiglu_back_region(co
       reg_values<XT>(xu.w[i], vu);
     }
   };
-  if (a.y || a.dxq.q || a.dxqt.q) {
+  if constexpr (DX) {
     float v[2][kRegRows][kRegCols];   // dg, du
 #pragma unroll
     for (int i = 0; i < kRegRows; ++i) {
@@ -234,8 +243,14 @@ __global__ __launch_bounds__(kRegThreads, CK ? 4 : 2) void swiglu_back_region(co
       for (int k = 0; k < kRegCols; ++k) {
         const Gate p = gate(vg[k]);
         const float d = dy[k] * p.s;
-        v[0][i][k] = d * vu[k] * (1.0f + vg[k] * p.om);
+        v[0][i][k] = d * vu[k] * __builtin_fmaf(vg[k], p.om, 1.0f);
         v[1][i][k] = d * vg[k];
+        vu[k] = vg[k] * p.s * vu[k];
+      }
+      if (i >= kFirst) {
+#pragma unroll
+        for (int q = 0; q < kRegCols / 4; ++q)
+          kept[i - kFirst][q][t] = u32x4{fbits(vu[4 * q]), fbits(vu[4 * q + 1]), fbits(vu[4 * q + 2]), fbits(vu[4 * q + 3])};
       }
     }
     if (a.y) {
@@ -302,10 +317,15 @@ __global__ __launch_bounds__(kRegThreads, CK ? 4 : 2) void swiglu_back_region(co
     float v[1][kRegRows][kRegCols];
 #pragma unroll
     for (int i = 0; i < kRegRows; ++i) {
-      float vg[kRegCols], vu[kRegCols];
-      gu(i, vg, vu);
+      if (DX && i >= kFirst) {
 #pragma unroll
-      for (int k = 0; k < kRegCols; ++k) v[0][i][k] = vg[k] * gate(vg[k]).s * vu[k];
+        for (int k = 0; k < kRegCols; ++k) v[0][i][k] = bitsf(kept[i - kFirst][k / 4][t][k % 4]);
+      } else {
+        float vg[kRegCols], vu[kRegCols];
+        gu(i, vg, vu);
+#pragma unroll
+        for (int k = 0; k < kRegCols; ++k) v[0][i][k] = vg[k] * gate(vg[k]).s * vu[k];
+      }
     }
     const amp_fp8_tiles o[1] = {a.yqt};
     const int64_t first[1] = {g.c0};
@@ -395,7 +415,8 @@ hipError_t dispatch_swiglu_back(const GateArgs& whole, hipStream_t s) {
       if (a.dxqt.q) { a.dxqt.q += r0; a.dxqt.s += r0 / kTileK * a.dxqt.lds; }
       if (a.yqt.q) { a.yqt.q += r0; a.yqt.s += r0 / kTileK * a.yqt.lds; }
       const dim3 grid(static_cast<unsigned>((a.cols + kTileK - 1) / kTileK), static_cast<unsigned>((rows + kTileK - 1) / kTileK));
-      swiglu_back_region<XT, CK><<<grid, kRegThreads, 0, s>>>(a);
+      if (a.y || a.dxq.q || a.dxqt.q) swiglu_back_region<XT, CK, true><<<grid, kRegThreads, 0, s>>>(a);
+      else swiglu_back_region<XT, CK, false><<<grid, kRegThreads, 0, s>>>(a);
     });
   }
   switch (row_width(whole.cols, kVec<XT>)) {
