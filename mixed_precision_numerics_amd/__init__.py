@@ -369,123 +369,115 @@ def amp_gemm_blockwise(M, N, K, A, at, lda, sA, ldsA, a_block, B, bt, ldb, sB, l
         ldsB, int(b_block), _ptr(C), ct, ldc, _stream(stream)))
 
 
-def _room_mat(fn: str, what: str, t, rows, cols, ld, dt) -> None:
-    """_room of a matrix; a tensor whose own elements suffice costs one comparison."""
+def _where() -> list:
+    """[current device], None before torch uses a GPU; _mem adds what is elsewhere."""
+    if _current is None:
+        import torch
+        if not torch.cuda.is_initialized():
+            return [None]
+    return [_now()[1]]
+
+
+def _mem(fn: str, what: str, t, nbytes: int, at: list) -> int | None:
+    """Device pointer of an operand; raises where a tensor holds fewer than
+    ``nbytes``.  Written for the call of one token, where each attribute read
+    counts."""
     if t is None:
-        return
-    need = _mat(rows, cols, ld, dt)
-    if getattr(t, "nbytes", 0) < need or not t.is_contiguous():
-        _room(fn, what, t, need)
+        return None
+    try:
+        where = t.get_device()
+    except AttributeError:
+        return _ptr(t)
+    if t.nbytes < nbytes or not t.is_contiguous():   # else its own elements suffice
+        _room(fn, what, t, nbytes)
+    if where != at[0]:
+        at.append(f"{what} is on {t.device}")
+    return t.data_ptr()
 
 
-def _here(fn: str, *operands) -> None:
-    """Raise where a torch operand is not on the current device (a host tensor
-    or another GPU's would fault in the kernel)."""
-    dev = None
-    for t in operands:
-        where = getattr(t, "get_device", None)
-        if where is None:
-            if isinstance(t, Fp8Tiles):
-                _here(fn, *t.tensors)
-            continue
-        where = where()
-        if dev is None:
-            dev = _now()[1] if where >= 0 else None
-        if where != dev:
-            raise ValueError(f"{fn}: an operand is on {t.device}, not on the current GPU")
+def _ready(fn: str, stream, at: list) -> int | None:
+    """The stream, last of a call's arguments; raises where an operand is not on
+    the current GPU (a host tensor or another GPU's would fault in the kernel)."""
+    if len(at) > 1:
+        raise ValueError(f"{fn}: {at[1]}, not on the current GPU")
+    return _stream(stream)
 
 
-def _room_tiles(fn: str, what: str, t, rows, cols, nb=None) -> None:
+def _tiles(fn: str, what: str, t, rows, cols, at, nb=None) -> int | None:
     """The same for an FP8 matrix [rows, cols] (``nb``: its tiles along K)."""
-    if t is None or rows <= 0 or cols <= 0:
-        return
+    if t is None:
+        return None
+    some = rows > 0 and cols > 0
     q, s = t.tensors
-    need = (rows - 1) * t.ldq + cols
-    if getattr(q, "nbytes", 0) < need or not q.is_contiguous():
-        _room(fn, what + ".q", q, need)
-    need = 4 * ((nb if nb else -(-cols // 128)) - 1) * t.lds + 4 * rows
-    if getattr(s, "nbytes", 0) < need or not s.is_contiguous():
-        _room(fn, what + ".s", s, need)
+    _mem(fn, what + ".q", q, (rows - 1) * t.ldq + cols if some else 0, at)
+    _mem(fn, what + ".s", s, 4 * ((nb or -(-cols // 128)) - 1) * t.lds + 4 * rows if some else 0, at)
+    return ctypes.addressof(t)
 
 
 def amp_rmsnorm(x, xt, rows, cols, ldx, res, ldr, gamma, gt, eps, h=None, ldh=0, y=None, yt=BF16,
                 ldy=0, d_scale=None, d_amax=None, yq=None, ckpt=None, rstd=None, stream=None):
     f = "amp_rmsnorm"
-    _room_mat(f, "x", x, rows, cols, ldx, xt)
-    _room_mat(f, "res", res, rows, cols, ldr, xt)
-    _room_mat(f, "gamma", gamma, 1, cols, cols, gt)
-    _room_mat(f, "h", h, rows, cols, ldh, xt)
-    _room_mat(f, "y", y, rows, cols, ldy, yt)
-    _room_mat(f, "d_scale", d_scale, 1, 1, 1, F32)
-    _room_mat(f, "d_amax", d_amax, 1, 1, 1, F32)
-    _room_mat(f, "rstd", rstd, 1, rows, rows, F32)
-    _room_tiles(f, "yq", yq, rows, cols)
-    _room_tiles(f, "ckpt", ckpt, rows, cols)
-    _here(f, x, res, gamma, h, y, d_scale, d_amax, yq, ckpt, rstd)
+    at = _where()
     _check(f, load().amp_rmsnorm(
-        _ptr(x), xt, rows, cols, ldx, _ptr(res), ldr, _ptr(gamma), gt, eps, _ptr(h), ldh, _ptr(y),
-        yt, ldy, _ptr(d_scale), _ptr(d_amax), _ptr(yq), _ptr(ckpt), _ptr(rstd), _stream(stream)))
+        _mem(f, "x", x, _mat(rows, cols, ldx, xt), at), xt, rows, cols, ldx,
+        _mem(f, "res", res, _mat(rows, cols, ldr, xt), at), ldr,
+        _mem(f, "gamma", gamma, _vec(cols, gt), at), gt, eps,
+        _mem(f, "h", h, _mat(rows, cols, ldh, xt), at), ldh,
+        _mem(f, "y", y, _mat(rows, cols, ldy, yt), at), yt, ldy,
+        _mem(f, "d_scale", d_scale, 4, at), _mem(f, "d_amax", d_amax, 4, at),
+        _tiles(f, "yq", yq, rows, cols, at), _tiles(f, "ckpt", ckpt, rows, cols, at),
+        _mem(f, "rstd", rstd, _vec(rows, F32), at), _ready(f, stream, at)))
 
 
 def amp_rmsnorm_backward(dy, dt, rows, cols, lddy, h, ldh, ckpt, gamma, gt, rstd, dres=None, lddr=0,
                          dx=None, lddx=0, dgamma=None, d_work=None, stream=None):
     f = "amp_rmsnorm_backward"
-    _room_mat(f, "dy", dy, rows, cols, lddy, dt)
-    _room_mat(f, "h", h, rows, cols, ldh, dt)
-    _room_tiles(f, "ckpt", ckpt, rows, cols)
-    _room_mat(f, "gamma", gamma, 1, cols, cols, gt)
-    _room_mat(f, "rstd", rstd, 1, rows, rows, F32)
-    _room_mat(f, "dres", dres, rows, cols, lddr, dt)
-    _room_mat(f, "dx", dx, rows, cols, lddx, dt)
-    if dgamma is not None:
-        _room_mat(f, "dgamma", dgamma, 1, cols, cols, F32)
-        _room(f, "d_work", d_work, _vec(min(rows, RMSNORM_PARTIALS) * cols, F32))
-    _here(f, dy, h, ckpt, gamma, rstd, dres, dx, dgamma, d_work)
+    at = _where()
+    work = _vec(min(rows, RMSNORM_PARTIALS) * cols, F32) if dgamma is not None else 0
     _check(f, load().amp_rmsnorm_backward(
-        _ptr(dy), dt, rows, cols, lddy, _ptr(h), ldh, _ptr(ckpt), _ptr(gamma), gt, _ptr(rstd),
-        _ptr(dres), lddr, _ptr(dx), lddx, _ptr(dgamma), _ptr(d_work), _stream(stream)))
+        _mem(f, "dy", dy, _mat(rows, cols, lddy, dt), at), dt, rows, cols, lddy,
+        _mem(f, "h", h, _mat(rows, cols, ldh, dt), at), ldh,
+        _tiles(f, "ckpt", ckpt, rows, cols, at),
+        _mem(f, "gamma", gamma, _vec(cols, gt), at), gt,
+        _mem(f, "rstd", rstd, _vec(rows, F32), at),
+        _mem(f, "dres", dres, _mat(rows, cols, lddr, dt), at), lddr,
+        _mem(f, "dx", dx, _mat(rows, cols, lddx, dt), at), lddx,
+        _mem(f, "dgamma", dgamma, _vec(cols, F32), at), _mem(f, "d_work", d_work, work, at),
+        _ready(f, stream, at)))
 
 
 def amp_swiglu(x, xt, rows, cols, ldx, y=None, yt=BF16, ldy=0, d_scale=None, d_amax=None, yq=None,
                ckpt=None, stream=None):
     f = "amp_swiglu"
-    _room_mat(f, "x", x, rows, 2 * cols, ldx, xt)
-    _room_mat(f, "y", y, rows, cols, ldy, yt)
-    _room_mat(f, "d_scale", d_scale, 1, 1, 1, F32)
-    _room_mat(f, "d_amax", d_amax, 1, 1, 1, F32)
-    _room_tiles(f, "yq", yq, rows, cols)
-    _room_tiles(f, "ckpt", ckpt, rows, 2 * cols, 2 * -(-cols // 128))
-    _here(f, x, y, d_scale, d_amax, yq, ckpt)
+    at = _where()
     _check(f, load().amp_swiglu(
-        _ptr(x), xt, rows, cols, ldx, _ptr(y), yt, ldy, _ptr(d_scale), _ptr(d_amax), _ptr(yq),
-        _ptr(ckpt), _stream(stream)))
+        _mem(f, "x", x, _mat(rows, 2 * cols, ldx, xt), at), xt, rows, cols, ldx,
+        _mem(f, "y", y, _mat(rows, cols, ldy, yt), at), yt, ldy,
+        _mem(f, "d_scale", d_scale, 4, at), _mem(f, "d_amax", d_amax, 4, at),
+        _tiles(f, "yq", yq, rows, cols, at),
+        _tiles(f, "ckpt", ckpt, rows, 2 * cols, at, 2 * -(-cols // 128)), _ready(f, stream, at)))
 
 
 def amp_swiglu_backward(dy, dt, rows, cols, lddy, x, ldx, ckpt, dx=None, lddx=0, dxq=None,
                         dxqt=None, yqt=None, stream=None):
     f = "amp_swiglu_backward"
-    _room_mat(f, "dy", dy, rows, cols, lddy, dt)
-    _room_mat(f, "x", x, rows, 2 * cols, ldx, dt)
-    _room_tiles(f, "ckpt", ckpt, rows, 2 * cols, 2 * -(-cols // 128))
-    _room_mat(f, "dx", dx, rows, 2 * cols, lddx, dt)
-    _room_tiles(f, "dxq", dxq, rows, 2 * cols)
-    _room_tiles(f, "dxqt", dxqt, 2 * cols, rows)
-    _room_tiles(f, "yqt", yqt, cols, rows)
-    _here(f, dy, x, ckpt, dx, dxq, dxqt, yqt)
+    at = _where()
     _check(f, load().amp_swiglu_backward(
-        _ptr(dy), dt, rows, cols, lddy, _ptr(x), ldx, _ptr(ckpt), _ptr(dx), lddx, _ptr(dxq),
-        _ptr(dxqt), _ptr(yqt), _stream(stream)))
+        _mem(f, "dy", dy, _mat(rows, cols, lddy, dt), at), dt, rows, cols, lddy,
+        _mem(f, "x", x, _mat(rows, 2 * cols, ldx, dt), at), ldx,
+        _tiles(f, "ckpt", ckpt, rows, 2 * cols, at, 2 * -(-cols // 128)),
+        _mem(f, "dx", dx, _mat(rows, 2 * cols, lddx, dt), at), lddx,
+        _tiles(f, "dxq", dxq, rows, 2 * cols, at), _tiles(f, "dxqt", dxqt, 2 * cols, rows, at),
+        _tiles(f, "yqt", yqt, cols, rows, at), _ready(f, stream, at)))
 
 
 def amp_requantize_blockwise(x, rows, cols, d_row, col, ct, qt, stream=None):
     f = "amp_requantize_blockwise"
-    _room_tiles(f, "x", x, rows, cols)
-    _room_mat(f, "d_row", d_row, 1, rows, rows, F32)
-    _room_mat(f, "col", col, 1, cols, cols, ct)
-    _room_tiles(f, "qt", qt, cols, rows)
-    _here(f, x, d_row, col, qt)
-    _check(f, load().amp_requantize_blockwise(_ptr(x), rows, cols, _ptr(d_row), _ptr(col), ct,
-                                              _ptr(qt), _stream(stream)))
+    at = _where()
+    _check(f, load().amp_requantize_blockwise(
+        _tiles(f, "x", x, rows, cols, at), rows, cols, _mem(f, "d_row", d_row, _vec(rows, F32), at),
+        _mem(f, "col", col, _vec(cols, ct), at), ct, _tiles(f, "qt", qt, cols, rows, at),
+        _ready(f, stream, at)))
 
 
 def amp_mx_quantize(x, xt, rows, cols, ldx, transpose, yt, q, scales, stream=None):
