@@ -187,7 +187,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_rows(const NormArgs
 }
 
 // Rows too long for the registers: a block walks its row twice (the second
-// reads come from the caches).  In place, h is what the second walk reads.
+// reads come from the caches; 1024 x 65536 with residual and tiles BF16 91 us =
+// 5.2 TB/s, FP32 with a checkpoint 150).  In place, h is what the second walk
+// reads.
 template <int XT>
 __global__ __launch_bounds__(1024) void rmsnorm_long(const NormArgs a) {
   constexpr int E = kVec<XT>, T = 1024;
@@ -306,6 +308,14 @@ struct NormBackArgs {
   float* part;
   int64_t rows, cols;
 };
+
+// The compiler no longer knows what was formed from w: those values are formed
+// again at its next use instead of staying in registers.
+template <int N>
+__device__ __forceinline__ void forget(uint32_t (&w)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) asm("" : "+v"(w[k]));
+}
 
 // One vector of h from the stored tensor (type XT) or the checkpoint.
 template <int XT, bool CK>
@@ -459,7 +469,10 @@ __global__ __launch_bounds__(S > 1 ? 512 : 1024) void rmsnorm_back_rows(const No
 // Rows of more than two vectors in each of 1024 threads, whose sums and next
 // row have no registers: dx by one block a row, and the sums of dy n in a pass
 // of their own, which reads dy and h again.  (Kept together with the sums in
-// the LDS, 2000 x 28672 BF16 took 238 us, and in the work area 440.)
+// the LDS, 2000 x 28672 BF16 took 238 us, and in the work area 440.)  HBM-bound
+// with both passes' reads: 2000 x 20480 BF16 stored 97 us = 4.2 TB/s, from a
+// checkpoint with dres 107 (143 while the values of dy and h stayed in
+// registers over the row's sum, which spilled).
 template <int XT, bool CK, int V>
 __global__ __launch_bounds__(1024) void rmsnorm_dx_rows(const NormBackArgs a) {
   constexpr int E = kVec<XT>, T = 1024;
@@ -494,6 +507,12 @@ __global__ __launch_bounds__(1024) void rmsnorm_dx_rows(const NormBackArgs a) {
   for (int v = 0; v < V; ++v) {
     const int c = (v * T + threadIdx.x) * E;
     float dy[E], h[E], gm[E], d[E];
+    if constexpr (CK) {
+      uint32_t w[4] = {wd[v].x, wd[v].y, wd[v].z, wd[v].w};
+      forget(w);
+      wd[v] = u32x4{w[0], w[1], w[2], w[3]};
+      forget(hr[v].q);
+    }
     widen<XT>(wd[v], dy);
     hr[v].values(a, h);
     load_cols<E>(a.gamma, a.gt, c, n, gm);
@@ -507,9 +526,11 @@ __global__ __launch_bounds__(1024) void rmsnorm_dx_rows(const NormBackArgs a) {
   }
 }
 
-// Longer rows still: the block walks its row twice.
+// Longer rows still: the block walks its row twice, two blocks a CU (2000 x
+// 32768 BF16 from a checkpoint with dres 163 us, with one 187; 1024 x 65536 stored
+// 173 us = 3.9 TB/s of both passes' reads).
 template <int XT, bool CK>
-__global__ __launch_bounds__(1024) void rmsnorm_dx_long(const NormBackArgs a) {
+__global__ __launch_bounds__(1024, 8) void rmsnorm_dx_long(const NormBackArgs a) {
   constexpr int E = kVec<XT>, T = 1024;
   __shared__ float red[32];
   const int64_t row = blockIdx.x;
@@ -650,7 +671,7 @@ hipError_t dispatch_back(const NormBackArgs& a, float* dgamma, hipStream_t s) {
         dgamma_part<XT, CK><<<dim3(static_cast<unsigned>(x), static_cast<unsigned>(blocks)), 256, 0, s>>>(a);
       }
       // four vectors of 16-bit gradients and of codes with their scales do not
-      // fit the registers (2000 x 32768: 305 us)
+      // fit the registers (2000 x 32768: 198 us, walked twice 163)
       constexpr bool kFour = !CK || XT == AMP_F32;
       constexpr int64_t kMost = 1 << 21;   // rows a launch: a grid's threads are counted in 32 bits
       for (int64_t r0 = 0; a.dx && r0 < a.rows; r0 += kMost) {

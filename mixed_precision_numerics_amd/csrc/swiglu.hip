@@ -189,9 +189,8 @@ __global__ __launch_bounds__(256) void swiglu_back_rows(const GateArgs a) {
 // LDS holds all of y.
 //
 // Bound by the vector ALUs and the two blocks' turns on them (8192 x 14336
-// from a checkpoint: 236 us = 4.6 TB/s, about 57 operations per element of y,
-// the sigmoid's two quarter-rate instructions a fifth of it; 257 with no row
-// kept, 237 with two).  Stored, 4096 x 14336 BF16: 178 us with all of y kept,
+// from a checkpoint: 236 us = 4.6 TB/s, 51 operations per element of y, the
+// ALUs 74 % busy; 257 us with no row kept, 237 with two).  Stored, 4096 x 14336 BF16: 178 us with all of y kept,
 // 184 with none.
 template <int XT, bool CK, bool DX>
 __global__ __launch_bounds__(kRegThreads, CK ? 4 : 2) void swiglu_back_region(const GateArgs a) {
