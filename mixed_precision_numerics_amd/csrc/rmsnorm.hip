@@ -311,10 +311,14 @@ struct NormBackArgs {
 
 // The compiler no longer knows what was formed from w: those values are formed
 // again at its next use instead of staying in registers.
-template <int N>
-__device__ __forceinline__ void forget(uint32_t (&w)[N]) {
+__device__ __forceinline__ void forget(uint32_t& w) { asm("" : "+v"(w)); }
+__device__ __forceinline__ void forget(u32x4& w) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) asm("" : "+v"(w[k]));
+  for (int k = 0; k < 4; ++k) {
+    uint32_t t = w[k];
+    forget(t);
+    w[k] = t;
+  }
 }
 
 // One vector of h from the stored tensor (type XT) or the checkpoint.
@@ -339,6 +343,14 @@ struct HRaw {
   __device__ __forceinline__ void trim(int c, int n) {
     if constexpr (CK) trim_codes<E, FULL>(q, c, n);
     else w = trim_vec<XT, FULL>(w, c, n);
+  }
+  __device__ __forceinline__ void forget_values() {
+    if constexpr (CK) {
+#pragma unroll
+      for (int k = 0; k < E / 4; ++k) forget(q[k]);
+    } else {
+      forget(w);
+    }
   }
   __device__ __forceinline__ void values(const NormBackArgs& a, float (&v)[E]) const {
     if constexpr (CK) decode<E>(a.ck.type, q, s, v);
@@ -422,6 +434,10 @@ __global__ __launch_bounds__(S > 1 ? 512 : 1024) void rmsnorm_back_rows(const No
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float dy[E], h[E], d[E];
+        if constexpr (V > 1) {   // 2000 x 12000 BF16 stored: 41 us, 66 without
+          forget(w.dy[v]);
+          w.h[v].forget_values();
+        }
         widen<XT>(w.dy[v], dy);
         w.h[v].values(a, h);
         dx_of<E>(dy, h, gm[v], w.r, m, d);
@@ -508,10 +524,8 @@ __global__ __launch_bounds__(1024) void rmsnorm_dx_rows(const NormBackArgs a) {
     const int c = (v * T + threadIdx.x) * E;
     float dy[E], h[E], gm[E], d[E];
     if constexpr (CK) {
-      uint32_t w[4] = {wd[v].x, wd[v].y, wd[v].z, wd[v].w};
-      forget(w);
-      wd[v] = u32x4{w[0], w[1], w[2], w[3]};
-      forget(hr[v].q);
+      forget(wd[v]);
+      hr[v].forget_values();
     }
     widen<XT>(wd[v], dy);
     hr[v].values(a, h);
