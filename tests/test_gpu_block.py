@@ -300,6 +300,31 @@ def test_norm_backward_in_place_with_gamma_gradient(saved, cols):
     check_values(dgamma.values()[0], F.F32, wg, (rows + 8) * U * np.abs(dy.v * hh * r[:, None]).sum(0), "dgamma")
 
 
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("saved", ["stored", "checkpoint"])
+@pytest.mark.parametrize("rows,cols", [(512, 96), (513, 96), (513, 257), (512, 700), (600, 700), (530, 1500), (512, 2048), (513, 2048), (520, 4095)])
+def test_norm_backward_on_both_sides_of_few_rows(dt, saved, rows, cols):
+    hv = loud(rows + cols, rows, cols)
+    h = Mat(rows, cols, dt, 5, hv) if saved == "stored" else None
+    ck = Tiles(rows, cols, amp.E4M3, 5, v=F.f32(hv)) if saved == "checkpoint" else None
+    hh = h.v if h else ck.v
+    dy, dres = Mat(rows, cols, dt, 1, rand(2, rows, cols)), Mat(rows, cols, dt, 2, rand(3, rows, cols))
+    gamma = Mat(1, cols, dt, 0, 1 + rand(7, 1, cols, scale=0.1))
+    r = F.f32(B.rmsnorm(hh, gamma.v[0], EPS)[1])
+    rstd, dx, dgamma = Mat(1, rows, amp.F32, 0, r[None]), Mat(rows, cols, dt, 3), Mat(1, cols, amp.F32)
+    work = Mat(min(rows, amp.RMSNORM_PARTIALS), cols, amp.F32)
+    args = (dy.d, dt, rows, cols, dy.ld, h.d if h else None, h.ld if h else 0, ck.arg if ck else None, gamma.d, dt, rstd.d)
+    amp.amp_rmsnorm_backward(*args, dres.d, dres.ld, dx.d, dx.ld, dgamma.d, work.d)
+    wx, wg = B.rmsnorm_backward(dy.v, hh, gamma.v[0], r, dres.v)
+    check_values(dx.values(), FMT[dt], wx, dx_err(dy.v, hh, gamma.v[0], r, dres.v, wx), "dx")
+    check_values(dgamma.values()[0], F.F32, wg, (rows + 8) * U * np.abs(dy.v * hh * r[:, None]).sum(0), "dgamma")
+    work.codes()
+    sums = dgamma.codes().copy()
+    amp.amp_rmsnorm_backward(*args, dres.d, dres.ld, dres.d, dres.ld, dgamma.d, work.d)
+    check_values(dres.values(), FMT[dt], wx, dx_err(dy.v, hh, gamma.v[0], r, dres.v, wx), "dx in place of dres")
+    assert np.array_equal(dgamma.codes(), sums)
+
+
 def test_norm_backward_over_many_rows_and_shared_gamma():
     """More rows than partial sums: every block walks several."""
     rows, cols, dt = 5003, 264, amp.BF16
