@@ -4,7 +4,9 @@ A thin ctypes binding of ``libamp.so`` (built from ``csrc/`` by
 ``mixed_precision_numerics_amd.build``).  Every function has the name and
 argument order of the C entry point declared in ``include/amp.h``; this module
 only marshals arguments (device pointers from torch tensors or ints, host
-structs, the stream handle) and turns a negative status into ``AmpError``.
+structs, the stream handle) and turns a negative status into ``AmpError``; the
+norm, gated-activation and requantization calls do so in C (``_quick``) where
+every operand is a contiguous tensor on the current GPU.
 All arithmetic runs in the HIP kernels.  There is no CPU fallback: when the
 library is missing or no gfx950 device is current, the calls raise.
 """
@@ -166,7 +168,24 @@ def load():
             fn.argtypes = args
             fn.restype = res
         _lib = lib
+        _bind()
     return _lib
+
+
+_plain = None                              # the module for plain operands (pyext/quick.cpp), once a GPU is in use
+
+
+def _bind() -> None:
+    """Give the built ``_quick`` module the library's entry points."""
+    global _plain
+    if _lib is None or _current is None or not os.path.exists(
+            os.path.join(os.path.dirname(os.path.abspath(__file__)), "_quick.so")):
+        return
+    import torch
+    from . import _quick as q
+    q.bind(torch.Tensor, Fp8Tiles, *(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
+        "amp_rmsnorm", "amp_rmsnorm_backward", "amp_swiglu", "amp_swiglu_backward", "amp_requantize_blockwise")))
+    _plain = q
 
 
 def _ptr(x) -> int | None:
@@ -201,6 +220,7 @@ def _now():
             def f():
                 return torch.cuda.current_stream().cuda_stream, torch.cuda.current_device()
         _current = f
+        _bind()
     return _current()
 
 
@@ -417,6 +437,11 @@ def _tiles(fn: str, what: str, t, rows, cols, at, nb=None) -> int | None:
 def amp_rmsnorm(x, xt, rows, cols, ldx, res, ldr, gamma, gt, eps, h=None, ldh=0, y=None, yt=BF16,
                 ldy=0, d_scale=None, d_amax=None, yq=None, ckpt=None, rstd=None, stream=None):
     f = "amp_rmsnorm"
+    if stream is None and _plain is not None:
+        st = _plain.rmsnorm(x, xt, rows, cols, ldx, res, ldr, gamma, gt, eps, h, ldh, y, yt, ldy,
+                            d_scale, d_amax, yq, ckpt, rstd, *_now())
+        if st is not None:
+            return _check(f, st)
     at = _where()
     _check(f, load().amp_rmsnorm(
         _mem(f, "x", x, _mat(rows, cols, ldx, xt), at), xt, rows, cols, ldx,
@@ -432,6 +457,11 @@ def amp_rmsnorm(x, xt, rows, cols, ldx, res, ldr, gamma, gt, eps, h=None, ldh=0,
 def amp_rmsnorm_backward(dy, dt, rows, cols, lddy, h, ldh, ckpt, gamma, gt, rstd, dres=None, lddr=0,
                          dx=None, lddx=0, dgamma=None, d_work=None, stream=None):
     f = "amp_rmsnorm_backward"
+    if stream is None and _plain is not None:
+        st = _plain.rmsnorm_backward(dy, dt, rows, cols, lddy, h, ldh, ckpt, gamma, gt, rstd, dres,
+                                     lddr, dx, lddx, dgamma, d_work, *_now())
+        if st is not None:
+            return _check(f, st)
     at = _where()
     work = _vec(min(rows, RMSNORM_PARTIALS) * cols, F32) if dgamma is not None else 0
     _check(f, load().amp_rmsnorm_backward(
@@ -449,6 +479,10 @@ def amp_rmsnorm_backward(dy, dt, rows, cols, lddy, h, ldh, ckpt, gamma, gt, rstd
 def amp_swiglu(x, xt, rows, cols, ldx, y=None, yt=BF16, ldy=0, d_scale=None, d_amax=None, yq=None,
                ckpt=None, stream=None):
     f = "amp_swiglu"
+    if stream is None and _plain is not None:
+        st = _plain.swiglu(x, xt, rows, cols, ldx, y, yt, ldy, d_scale, d_amax, yq, ckpt, *_now())
+        if st is not None:
+            return _check(f, st)
     at = _where()
     _check(f, load().amp_swiglu(
         _mem(f, "x", x, _mat(rows, 2 * cols, ldx, xt), at), xt, rows, cols, ldx,
@@ -461,6 +495,11 @@ def amp_swiglu(x, xt, rows, cols, ldx, y=None, yt=BF16, ldy=0, d_scale=None, d_a
 def amp_swiglu_backward(dy, dt, rows, cols, lddy, x, ldx, ckpt, dx=None, lddx=0, dxq=None,
                         dxqt=None, yqt=None, stream=None):
     f = "amp_swiglu_backward"
+    if stream is None and _plain is not None:
+        st = _plain.swiglu_backward(dy, dt, rows, cols, lddy, x, ldx, ckpt, dx, lddx, dxq, dxqt, yqt,
+                                    *_now())
+        if st is not None:
+            return _check(f, st)
     at = _where()
     _check(f, load().amp_swiglu_backward(
         _mem(f, "dy", dy, _mat(rows, cols, lddy, dt), at), dt, rows, cols, lddy,
@@ -473,6 +512,10 @@ def amp_swiglu_backward(dy, dt, rows, cols, lddy, x, ldx, ckpt, dx=None, lddx=0,
 
 def amp_requantize_blockwise(x, rows, cols, d_row, col, ct, qt, stream=None):
     f = "amp_requantize_blockwise"
+    if stream is None and _plain is not None:
+        st = _plain.requantize(x, rows, cols, d_row, col, ct, qt, *_now())
+        if st is not None:
+            return _check(f, st)
     at = _where()
     _check(f, load().amp_requantize_blockwise(
         _tiles(f, "x", x, rows, cols, at), rows, cols, _mem(f, "d_row", d_row, _vec(rows, F32), at),

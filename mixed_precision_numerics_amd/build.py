@@ -1,7 +1,8 @@
 """Build the HIP library ``libamp.so`` for gfx950 in-tree.
 
 Every ``csrc/*.hip`` and ``csrc/*.cpp`` is compiled by hipcc into ``_build/``
-(in parallel) and linked into ``mixed_precision_numerics_amd/libamp.so``.
+(in parallel) and linked into ``mixed_precision_numerics_amd/libamp.so``; the
+host compiler builds the binding's ``_quick`` module from ``pyext/``.
 """
 from __future__ import annotations
 
@@ -11,12 +12,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libamp.so")
+QUICK = os.path.join(PKG, "_quick.so")
 ARCH = "gfx950"
 
 COMMON = [
@@ -65,6 +68,17 @@ def _compile(src: str, incremental: bool = False) -> str:
     return obj
 
 
+def _build_quick() -> None:
+    tmp = QUICK + ".tmp"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-o", tmp,
+           os.path.join(PKG, "pyext", "quick.cpp"), "-I" + os.path.join(ROOT, "include"),
+           "-I" + sysconfig.get_paths()["include"]]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on quick.cpp:\n" + r.stderr)
+    os.replace(tmp, QUICK)
+
+
 def build(verbose: bool = False, jobs: int | None = None, incremental: bool = False) -> str:
     """Compile every source (``incremental``: reuse objects newer than their
     source, the headers and this script) and link the library."""
@@ -81,6 +95,7 @@ def build(verbose: bool = False, jobs: int | None = None, incremental: bool = Fa
     os.replace(tmp, LIB)
     if verbose:
         print("built", LIB, file=sys.stderr)
+    _build_quick()
     return LIB
 
 

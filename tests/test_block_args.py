@@ -153,3 +153,29 @@ def test_binding_refuses_scalars_without_room():
             amp.amp_rmsnorm(x, amp.BF16, 2, 256, 256, None, 0, None, 0, 1e-5, y=y, ldy=256, **{k: none})
         with pytest.raises(ValueError, match=k):
             amp.amp_swiglu(x, amp.BF16, 2, 128, 256, y=y, ldy=256, **{k: none})
+
+
+def test_the_quick_module_takes_plain_operands_only():
+    """Anything else gives None (the binding's own path decides), a plain call
+    the entry point's status; every call here is refused before device work."""
+    from mixed_precision_numerics_amd import _quick
+    lib = amp.load()
+    names = ("amp_rmsnorm", "amp_rmsnorm_backward", "amp_swiglu", "amp_swiglu_backward", "amp_requantize_blockwise")
+    _quick.bind(torch.Tensor, amp.Fp8Tiles, *(amp.ctypes.cast(getattr(lib, n), amp.ctypes.c_void_p).value for n in names))
+    x, g = torch.zeros(4, 300, dtype=torch.bfloat16), torch.zeros(300)
+    q, s = torch.zeros(4, 300, dtype=torch.uint8), torch.zeros(3, 4)
+    good = [x, amp.BF16, 4, 300, 300, None, 0, g, 9, 1e-5, None, 0, None, amp.BF16, 0, None, None, amp.Fp8Tiles(q, s, 300, 4), None, None, 0, -1]
+    assert _quick.rmsnorm(*good) == EUNSUP              # gamma's type; all operands are plain
+
+    def but(i, v):
+        return _quick.rmsnorm(*good[:i], v, *good[i + 1:])
+    for i, v in ((0, P), (0, x[:, :200]), (0, torch.zeros(4, 299, dtype=torch.bfloat16)), (2, 5), (2, "4"), (2, 1 << 70), (4, 400), (9, 1),
+                 (16, torch.zeros(0)), (17, P), (17, q), (17, amp.Fp8Tiles(q, s[:2], 300, 4)), (17, amp.Fp8Tiles(q, s, 301, 4)),
+                 (17, amp.Fp8Tiles(P, P, 300, 4)), (21, 0)):
+        assert but(i, v) is None, (i, v)
+    assert but(2, -1) == EINVAL and but(1, 7) == EUNSUP
+    with pytest.raises(TypeError):
+        _quick.rmsnorm(*good[:-1])
+    dead = amp.Fp8Tiles(q, s, 300, 4)
+    dead.tensors = (q.clone(), s)                       # not what the structure points to
+    assert but(17, dead) is None

@@ -707,3 +707,41 @@ def test_more_rows_than_one_launch_takes():
     whole, part = transposed(0, rows), transposed(first, rows)
     assert torch.equal(whole[0][:, first:], part[0])
     assert all(torch.equal(w, p) for w, p in zip(whole[1:], part[1:]))
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 4096), (600, 256)])
+def test_pointers_views_and_streams_give_what_tensors_give(rows, cols):
+    """The binding's ways to an operand: a contiguous tensor, its address, a
+    view with padded rows, a stream handed over."""
+    bf = torch.bfloat16
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    wide = torch.randn(rows, 2 * cols + 8, generator=gen, device="cuda").to(bf)
+    x, dy = wide[:, :2 * cols].contiguous(), torch.randn(rows, cols, generator=gen, device="cuda").to(bf)
+    gamma = torch.ones(cols, device="cuda")
+    side = torch.cuda.Stream()
+    seen = []
+    for how in ("tensors", "addresses", "views", "stream"):
+        a = (lambda t: t.data_ptr()) if how == "addresses" else (lambda t: t)
+        src, ld = (wide[:, :2 * cols], 2 * cols + 8) if how == "views" else (x, 2 * cols)
+        k = dict(stream=side) if how == "stream" else {}
+
+        def out(*shape, dtype=bf):
+            return torch.zeros(*shape, dtype=dtype, device="cuda")
+        o = dict(y=out(rows, cols), rstd=out(rows, dtype=torch.float32), z=out(rows, 2 * cols), dx=out(rows, 2 * cols), dg=out(cols, dtype=torch.float32),
+                 q=out(rows, 2 * cols, dtype=torch.uint8), s=out(2 * cols // 128, rows, dtype=torch.float32),
+                 qt=out(2 * cols, rows, dtype=torch.uint8), st=out(-(-rows // 128), 2 * cols, dtype=torch.float32))
+        work, n = out(min(rows, amp.RMSNORM_PARTIALS), cols, dtype=torch.float32), out(rows, cols)
+        torch.cuda.synchronize()
+        ck, qt = amp.Fp8Tiles(a(o["q"]), a(o["s"]), 2 * cols, rows), amp.Fp8Tiles(a(o["qt"]), a(o["st"]), rows, 2 * cols)
+        amp.amp_swiglu(a(src), amp.BF16, rows, cols, ld, a(o["y"]), amp.BF16, cols, ckpt=ck, **k)
+        amp.amp_swiglu_backward(a(dy), amp.BF16, rows, cols, cols, a(src), ld, None, a(o["dx"]), 2 * cols, **k)
+        amp.amp_requantize_blockwise(ck, rows, 2 * cols, None, None, 0, qt, **k)
+        amp.amp_rmsnorm(a(src), amp.BF16, rows, cols, ld, None, 0, a(gamma), amp.F32, EPS, y=a(n), ldy=cols, rstd=a(o["rstd"]), **k)
+        amp.amp_rmsnorm_backward(a(dy), amp.BF16, rows, cols, cols, a(src), ld, None, a(gamma), amp.F32, a(o["rstd"]), None, 0,
+                                 a(o["z"]), cols, a(o["dg"]), a(work), **k)
+        torch.cuda.synchronize()
+        seen.append(dict(o, n=n))
+    assert amp._plain is not None                       # the first of them went through the compiled module
+    for o in seen[1:]:
+        for name in o:
+            assert torch.equal(o[name], seen[0][name]), name
