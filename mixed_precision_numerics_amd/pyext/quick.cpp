@@ -153,7 +153,7 @@ PyObject* swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
   AMP_OPEN(12);
   const int xt = a.type(1), yt = a.type(6);
   const int64_t rows = a.num(2), cols = a.num(3), ldx = a.num(4), ldy = a.num(7);
-  if (cols > INT64_MAX / 4) Py_RETURN_NONE;
+  if (cols < 0 || cols > INT64_MAX / 4) Py_RETURN_NONE;
   amp_fp8_tiles q, c;
   const void* x = a.mem(0, span(rows, 2 * cols, ldx, xt));
   void* y = a.mem(5, span(rows, cols, ldy, yt));
@@ -167,7 +167,7 @@ PyObject* swiglu_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
   AMP_OPEN(13);
   const int dt = a.type(1);
   const int64_t rows = a.num(2), cols = a.num(3), lddy = a.num(4), ldx = a.num(6), lddx = a.num(9);
-  if (cols > INT64_MAX / 4) Py_RETURN_NONE;
+  if (cols < 0 || cols > INT64_MAX / 4) Py_RETURN_NONE;
   amp_fp8_tiles c, q, qt, yt;
   const void *dy = a.mem(0, span(rows, cols, lddy, dt)), *x = a.mem(5, span(rows, 2 * cols, ldx, dt));
   const amp_fp8_tiles* ck = a.tiles(7, rows, 2 * cols, 2 * blocks(cols), c);
