@@ -427,7 +427,8 @@ typedef struct {
  *   y = (h * r) * gamma
  * x, res: [rows, cols] of xt in {F32, F16, BF16}, strides ldx, ldr >= cols.
  * gamma: [cols] of gt in {F32, F16, BF16}; NULL means 1.  eps >= 0 and finite
- *    (with eps == 0 an all-zero row has r = inf and y = NaN).
+ *    (with eps == 0 a row whose FP32 squares sum to 0 has r = inf, y of inf and
+ *    NaN, and makes *d_amax NaN or inf).
  * Outputs, at least one (each may be NULL):
  *   h: [rows, cols] of xt, stride ldh; may be x or res themselves, with the
  *      same stride.  y is formed from the rounded h.

@@ -183,7 +183,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_rows(const NormArgs
     for (int k = 0; k < N; ++k) load_cols<E, FULL>(a.gamma, a.gt, c + (p * N + k) * step, n, gm[k]);
     am = __builtin_elementwise_maximum(am, norm_outputs<XT, N, FULL>(a, h[p], gm, row, 0, c + p * N * step, step, n, live, r, scale));
   }
-  if (a.amax) block_amax(am, seen, redm, a.amax);
+  // a wave past the last row holds zeros, whose y is NaN where eps is 0
+  if (a.amax) block_amax(live ? am : 0.0f, seen, redm, a.amax);
 }
 
 // Rows too long for the registers: a block walks its row twice (the second

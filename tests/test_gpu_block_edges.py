@@ -1,0 +1,32 @@
+"""Calls of the norm, gated-activation and requantization entry points at the
+edges of what they allow, against oracle/block.py in float64."""
+import numpy as np
+import pytest
+import torch
+
+import mixed_precision_numerics_amd as amp
+from oracle import block as B
+from block_util import U, check_scaled, check_values, norm_err
+from gpu_util import dev
+from test_gpu_block import FMT, TYPES, Mat, Tiles, rand
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("xt", TYPES)
+@pytest.mark.parametrize("cols", [40, 512, 1536])
+@pytest.mark.parametrize("rows", [1, 2, 3, 5, 1030])
+def test_norm_without_eps_records_the_rows_maximum_alone(xt, rows, cols):
+    """eps == 0 with no zero row: what the threads of a block hold past the last
+    row (zeros, whose norm is 0 * inf) reaches no output, the amax among them."""
+    x = Mat(rows, cols, xt, 3, rand(rows + cols, rows, cols))
+    y, yq, rstd = Mat(rows, cols, amp.E4M3, 1), Tiles(rows, cols), Mat(1, rows, amp.F32)
+    am, sc = torch.full((1,), 1e-3, device="cuda"), np.float32([16.0])
+    amp.amp_rmsnorm(x.d, xt, rows, cols, x.ld, None, 0, None, 0, 0.0, None, 0, y.d, amp.E4M3, y.ld, dev(sc), am, yq.arg, None, rstd.d)
+    wy, wr = B.rmsnorm(x.v, np.ones(cols), 0.0)
+    e = norm_err(cols)
+    err = np.abs(wy) * (e + 3 * U)
+    check_values(am.cpu().numpy(), FMT[amp.F32], np.array([np.abs(wy).max()]), err.max(), "amax")
+    check_values(rstd.values()[0], FMT[amp.F32], wr, e * wr, "rstd")
+    check_scaled(y.codes(), FMT[amp.E4M3], wy, err, 16.0, 16.0, "y")
+    yq.check(wy, err, "yq")
