@@ -89,7 +89,8 @@ class Fp8Tiles(ctypes.Structure):
 
     ``q``: codes [R, K], row stride ``ldq``; ``s``: scale_inv of tile kb of row
     r at ``s[kb * lds + r]``.  Tensors given for them are kept alive and, in
-    every call, checked against what the call spans."""
+    every call, checked against what the call spans; they must stay where they
+    were (a call with one that was resized or given other storage is refused)."""
     _fields_ = [("q", ctypes.c_void_p), ("s", ctypes.c_void_p), ("ldq", ctypes.c_int64),
                 ("lds", ctypes.c_int64), ("type", ctypes.c_int32), ("pad_", ctypes.c_int32)]
 
@@ -424,13 +425,19 @@ def _ready(fn: str, stream, at: list) -> int | None:
 
 
 def _tiles(fn: str, what: str, t, rows, cols, at, nb=None) -> int | None:
-    """The same for an FP8 matrix [rows, cols] (``nb``: its tiles along K)."""
+    """The same for an FP8 matrix [rows, cols] (``nb``: its tiles along K).  The
+    kernel follows the structure's addresses: tensors that have other storage
+    by now (``resize_``, ``set_``, ``data``) are refused."""
     if t is None:
         return None
     some = rows > 0 and cols > 0
     q, s = t.tensors
-    _mem(fn, what + ".q", q, (rows - 1) * t.ldq + cols if some else 0, at)
-    _mem(fn, what + ".s", s, 4 * ((nb or -(-cols // 128)) - 1) * t.lds + 4 * rows if some else 0, at)
+    for name, o, now, n in (
+            (".q", q, t.q, (rows - 1) * t.ldq + cols),
+            (".s", s, t.s, 4 * ((nb or -(-cols // 128)) - 1) * t.lds + 4 * rows)):
+        p = _mem(fn, what + name, o, n if some else 0, at)
+        if p != now and hasattr(o, "data_ptr") and (p or now):   # (a field of 0 reads as None)
+            raise ValueError(f"{fn}: {what}{name} has moved since the Fp8Tiles was made from it")
     return ctypes.addressof(t)
 
 

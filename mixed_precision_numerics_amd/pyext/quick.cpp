@@ -6,8 +6,9 @@
 // Each function takes its Python counterpart's arguments in order, then the
 // stream's handle and the current device's index, and returns the entry
 // point's status; None where an operand is anything else (an integer pointer,
-// a view, a tensor that is too small or elsewhere): the caller then takes its
-// own path, which names the operand or makes the call.
+// a view, a tensor that is too small, elsewhere, or no longer where an
+// Fp8Tiles points): the caller then takes its own path, which names and refuses
+// the operand or makes the call.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

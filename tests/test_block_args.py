@@ -179,3 +179,44 @@ def test_the_quick_module_takes_plain_operands_only():
     dead = amp.Fp8Tiles(q, s, 300, 4)
     dead.tensors = (q.clone(), s)                       # not what the structure points to
     assert but(17, dead) is None
+
+
+@pytest.mark.parametrize("part", [0, 1])
+@pytest.mark.parametrize("how", ["resize_", "set_", "data", "field"])
+def test_binding_refuses_tiles_that_no_longer_point_to_their_tensors(how, part):
+    """The room is checked at the tensors, the kernel follows the structure."""
+    def made(rows, nb):
+        q, s = torch.zeros(rows, 512, dtype=torch.uint8), torch.zeros(nb, rows)
+        t = amp.Fp8Tiles(q, s, 512, rows)
+        v = t.tensors[part]
+        if how == "resize_":
+            v.resize_(64 * v.shape[0], v.shape[1])
+        elif how == "set_":
+            v.set_(torch.zeros_like(v))
+        elif how == "data":
+            v.data = torch.zeros_like(v)
+        else:
+            setattr(t, "qs"[part], getattr(t, "qs"[part]) + 16)
+        return t
+
+    x, r = torch.zeros(4, 600, dtype=torch.bfloat16), torch.zeros(4)
+    good, tall = amp.Fp8Tiles(torch.zeros(4, 600, dtype=torch.uint8), torch.zeros(6, 4), 600, 4), made(300, 1)
+    for what, fn, a, k in (("yq", amp.amp_rmsnorm, (x, amp.BF16, 4, 300, 600, None, 0, None, 0, 1e-5), dict(yq=made(4, 3))),
+                           ("ckpt", amp.amp_rmsnorm, (x, amp.BF16, 4, 300, 600, None, 0, None, 0, 1e-5), dict(ckpt=made(4, 3))),
+                           ("ckpt", amp.amp_rmsnorm_backward, (x, amp.BF16, 4, 300, 600, None, 0, made(4, 3), None, 0, r), dict(dx=x, lddx=600)),
+                           ("yq", amp.amp_swiglu, (x, amp.BF16, 4, 300, 600), dict(yq=made(4, 3))),
+                           ("ckpt", amp.amp_swiglu_backward, (x, amp.BF16, 4, 150, 600, None, 0, made(4, 4)), dict(dx=x, lddx=600)),
+                           ("yqt", amp.amp_swiglu_backward, (x, amp.BF16, 4, 300, 600, x, 600, None), dict(yqt=tall)),
+                           ("x", amp.amp_requantize_blockwise, (made(4, 3), 4, 300, None, None, 0, good), {}),
+                           ("qt", amp.amp_requantize_blockwise, (good, 4, 300, None, None, 0, tall), {})):
+        with pytest.raises(ValueError, match=what + r"\." + "qs"[part] + " has moved"):
+            fn(*a, **k)
+
+
+def test_tiles_of_addresses_follow_their_fields():
+    """Without a tensor to compare with, the structure's fields are what a call takes."""
+    t = amp.Fp8Tiles(P, P, 300, 4)
+    t.q = 2 * P
+    assert amp._tiles("f", "yq", t, 4, 300, [None]) == amp.ctypes.addressof(t)
+    empty = amp.Fp8Tiles(torch.zeros(0, dtype=torch.uint8), torch.zeros(0), 300, 4)
+    assert amp._tiles("f", "yq", empty, 0, 300, [-1]) == amp.ctypes.addressof(empty)
