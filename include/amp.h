@@ -455,12 +455,13 @@ int amp_rmsnorm(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx,
  * dres: [rows, cols] of dt, stride lddr: the gradient that reaches h past the
  *    norm (the residual branch); NULL for none.
  * dx: [rows, cols] of dt, stride lddx, the gradient of h and so of x and of
- *    res; may be dy or dres themselves, with the same stride; NULL for none.
+ *    res; may be dy, dres or h themselves, with the same stride; NULL for none.
  * dgamma: [cols] FP32, overwritten (zeros for rows == 0); NULL for none.
  * d_work: FP32 [min(rows, AMP_RMSNORM_PARTIALS), cols], the partial sums of
  *    dgamma (needed with dgamma); calls that may overlap need one each.  The
  *    sums are added in a fixed order: the result is reproducible.
- * Apart from dx no output may overlap an input.  cols == 0 is a no-op. */
+ * Apart from dx in the place of one of those three no output may overlap an
+ * input.  cols == 0 is a no-op. */
 #define AMP_RMSNORM_PARTIALS 256
 int amp_rmsnorm_backward(const void* dy, int dt, int64_t rows, int64_t cols, int64_t lddy,
                          const void* h, int64_t ldh, const amp_fp8_tiles* ckpt,

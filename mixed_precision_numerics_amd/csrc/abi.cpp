@@ -440,7 +440,7 @@ int amp_rmsnorm_backward(const void* dy, int dt, int64_t rows, int64_t cols, int
     if ((h != nullptr) == (ckpt != nullptr)) return AMP_EINVAL;
     if (lddy < cols || (h && ldh < cols) || (dres && lddr < cols) || (dx && lddx < cols)) return AMP_EINVAL;
     if (int e = tiles_status(ckpt, rows, cols)) return e;
-    if ((dx == dy && lddx != lddy) || (dx && dx == dres && lddx != lddr)) return AMP_EINVAL;
+    if (dx && ((dx == dy && lddx != lddy) || (dx == dres && lddx != lddr) || (dx == h && lddx != ldh))) return AMP_EINVAL;
   }
   if (int e = check_device()) return e;
   return hip_status(amp::launch_rmsnorm_backward(dy, dt, rows, cols, lddy, h, ldh, or_none(ckpt), gamma, gt, rstd,

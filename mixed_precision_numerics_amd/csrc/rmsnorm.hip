@@ -753,8 +753,9 @@ hipError_t dispatch_back(const NormBackArgs& a, float* dgamma, hipStream_t s) {
     else                                                                                               \
       rmsnorm_back_rows<XT, CK, V, S, false><<<static_cast<unsigned>(blocks), B, 0, s>>>(a);           \
   } while (0)
-  // (not where dx takes the place of dy, which the columns' blocks still read)
-  if (a.rows > 0 && a.rows <= kFewRows && nv <= 512 && !(dgamma && a.dx == a.dy)) {
+  // (not where dx takes the place of dy or h, which the columns' blocks still read)
+  const bool over = a.dx && (a.dx == a.dy || a.dx == a.h);
+  if (a.rows > 0 && a.rows <= kFewRows && nv <= 512 && !(dgamma && over)) {
     const int sums = dgamma ? static_cast<int>((a.cols + 31) / 32) : 0;
     const int S = nv <= 64 ? 8 : nv <= 128 ? 4 : nv <= 256 ? 2 : 1;
     const unsigned grid = static_cast<unsigned>(sums + (a.dx ? (a.rows + S - 1) / S : 0));
@@ -772,7 +773,7 @@ hipError_t dispatch_back(const NormBackArgs& a, float* dgamma, hipStream_t s) {
     else if (nv <= 1024) AMP_BACK(1, 1, 1024);
     else if (nv <= 2 * 1024) AMP_BACK(2, 1, 1024);
     else {
-      if (dgamma) {   // before dx, which may take the place of dy
+      if (dgamma) {   // before dx, which may take the place of dy or h
         // about eight blocks a CU, each with at least four rows
         const int64_t x = (nv + 255) / 256;
         blocks = (a.rows + 3) / 4 < 2048 / x + 1 ? (a.rows + 3) / 4 : 2048 / x + 1;

@@ -220,3 +220,7 @@ def test_tiles_of_addresses_follow_their_fields():
     assert amp._tiles("f", "yq", t, 4, 300, [None]) == amp.ctypes.addressof(t)
     empty = amp.Fp8Tiles(torch.zeros(0, dtype=torch.uint8), torch.zeros(0), 300, 4)
     assert amp._tiles("f", "yq", empty, 0, 300, [-1]) == amp.ctypes.addressof(empty)
+
+
+def test_norm_gradient_over_the_stored_input_needs_its_stride():
+    assert norm_back(h=2 * P, ldh=301) == EINVAL and norm_back(h=2 * P, ldh=301, dgamma=None) == EINVAL

@@ -6,7 +6,8 @@ import torch
 
 import mixed_precision_numerics_amd as amp
 from oracle import block as B
-from block_util import U, check_scaled, check_values, norm_err
+from oracle import formats as F
+from block_util import U, check_scaled, check_values, dx_err, norm_err
 from gpu_util import dev
 from test_gpu_block import FMT, TYPES, Mat, Tiles, rand
 
@@ -30,3 +31,23 @@ def test_norm_without_eps_records_the_rows_maximum_alone(xt, rows, cols):
     check_values(rstd.values()[0], FMT[amp.F32], wr, e * wr, "rstd")
     check_scaled(y.codes(), FMT[amp.E4M3], wy, err, 16.0, 16.0, "y")
     yq.check(wy, err, "yq")
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("rows,cols", [(1, 40), (5, 4096), (64, 1000), (301, 96), (512, 512), (512, 2047), (513, 96), (700, 520), (600, 2048),
+                                       (7, 5120), (40, 9000), (30, 20483), (5, 40003)])
+def test_norm_backward_in_place_of_the_stored_input(dt, rows, cols):
+    """dx replaces h, which the gamma gradient reads too, on every path by rows and by vectors."""
+    hv, ones = rand(1, rows, cols), np.ones(cols)
+    dy, dres = Mat(rows, cols, dt, 1, rand(2, rows, cols)), Mat(rows, cols, dt, 2, rand(3, rows, cols))
+    for gradient in (True, False):
+        h = Mat(rows, cols, dt, 5, hv)
+        r = F.f32(B.rmsnorm(h.v, ones, 1e-5)[1])
+        dgamma, work = Mat(1, cols, amp.F32), Mat(min(rows, amp.RMSNORM_PARTIALS), cols, amp.F32)
+        amp.amp_rmsnorm_backward(dy.d, dt, rows, cols, dy.ld, h.d, h.ld, None, None, 0, dev(r.astype(np.float32)), dres.d, dres.ld,
+                                 h.d, h.ld, dgamma.d if gradient else None, work.d)
+        wx, wg = B.rmsnorm_backward(dy.v, h.v, ones, r, dres.v)
+        check_values(h.values(), FMT[dt], wx, dx_err(dy.v, h.v, ones, r, dres.v, wx), "dx in place of h")
+        work.codes()
+        if gradient:
+            check_values(dgamma.values()[0], FMT[amp.F32], wg, (rows + 8) * U * np.abs(dy.v * h.v * r[:, None]).sum(0), "dgamma")
