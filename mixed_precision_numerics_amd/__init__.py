@@ -13,7 +13,9 @@ library is missing or no gfx950 device is current, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
+import warnings
 
 import numpy as np
 
@@ -177,13 +179,17 @@ _plain = None                              # the module for plain operands (pyex
 
 
 def _bind() -> None:
-    """Give the built ``_quick`` module the library's entry points."""
+    """Give the ``_quick`` module the library's entry points, where it was built
+    and loads."""
     global _plain
-    if _lib is None or _current is None or not os.path.exists(
-            os.path.join(os.path.dirname(os.path.abspath(__file__)), "_quick.so")):
+    if _lib is None or _current is None or importlib.util.find_spec(__name__ + "._quick") is None:
+        return
+    try:
+        from . import _quick as q
+    except ImportError as e:
+        warnings.warn(f"the binding's _quick module does not load, its calls take the Python path: {e}", RuntimeWarning)
         return
     import torch
-    from . import _quick as q
     q.bind(torch.Tensor, Fp8Tiles, *(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
         "amp_rmsnorm", "amp_rmsnorm_backward", "amp_swiglu", "amp_swiglu_backward", "amp_requantize_blockwise")))
     _plain = q

@@ -13,13 +13,14 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libamp.so")
-QUICK = os.path.join(PKG, "_quick.so")
+QUICK = os.path.join(PKG, "_quick" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = "gfx950"
 
 COMMON = [
@@ -69,13 +70,25 @@ def _compile(src: str, incremental: bool = False) -> str:
 
 
 def _build_quick() -> None:
+    """Build the binding's module, which the package does without where a
+    compiler or Python's headers are missing.  One of an earlier build does not
+    stay: it may not fit the library's calls, and a name without the
+    interpreter's tag is loaded by every interpreter."""
+    for old in {QUICK, os.path.join(os.path.dirname(QUICK), "_quick.so")}:
+        if os.path.exists(old):
+            os.remove(old)
     tmp = QUICK + ".tmp"
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-o", tmp,
            os.path.join(PKG, "pyext", "quick.cpp"), "-I" + os.path.join(ROOT, "include"),
            "-I" + sysconfig.get_paths()["include"]]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("g++ failed on quick.cpp:\n" + r.stderr)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        failed = r.stderr if r.returncode else None
+    except OSError as e:
+        failed = str(e)
+    if failed is not None:
+        warnings.warn("the binding's _quick module was not built, its calls take the Python path:\n" + failed, RuntimeWarning)
+        return
     os.replace(tmp, QUICK)
 
 
