@@ -413,7 +413,7 @@ int amp_rmsnorm(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx, 
                 int yt, int64_t ldy, const float* d_scale, float* d_amax, const amp_fp8_tiles* yq,
                 const amp_fp8_tiles* ckpt, float* rstd, void* stream) {
   if (!al(d_scale, 4) || !al(d_amax, 4) || !al(rstd, 4)) return AMP_EINVAL;
-  if (rows < 0 || cols < 0 || !(eps >= 0.0f && eps < 3.0e38f)) return AMP_EINVAL;
+  if (rows < 0 || cols < 0 || !(eps >= 0.0f && __builtin_isfinite(eps))) return AMP_EINVAL;
   if (cols > kMostCols || !is_cast_in(xt) || (gamma && !is_cast_in(gt)) || (y && !is_cast_out(yt))) return AMP_EUNSUPPORTED;
   if (rows == 0 || cols == 0) return AMP_OK;
   if (!x || (!h && !y && !yq && !ckpt && !d_amax && !rstd)) return AMP_EINVAL;

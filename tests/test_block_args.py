@@ -224,3 +224,9 @@ def test_tiles_of_addresses_follow_their_fields():
 
 def test_norm_gradient_over_the_stored_input_needs_its_stride():
     assert norm_back(h=2 * P, ldh=301) == EINVAL and norm_back(h=2 * P, ldh=301, dgamma=None) == EINVAL
+
+
+def test_every_finite_eps_is_accepted():
+    top = float(torch.finfo(torch.float32).max)
+    assert norm(eps=top, rows=0) == 0 and norm(eps=3.1e38, rows=0) == 0 and norm(eps=0.0, rows=0) == 0
+    assert norm(eps=float("inf"), rows=0) == EINVAL and norm(eps=-0.5, rows=0) == EINVAL
