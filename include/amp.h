@@ -472,11 +472,15 @@ int amp_rmsnorm_backward(const void* dy, int dt, int64_t rows, int64_t cols, int
 /* amp_swiglu -- gated activation y = g * sigmoid(g) * u of x = [g | u].
  * x: [rows, 2*cols] of xt in {F32, F16, BF16} (g the first cols columns, u the
  *    others), stride ldx >= 2*cols.
- * Outputs, at least one of y, yq, ckpt:
+ * Outputs, at least one of y, d_amax, yq, ckpt:
  *   y, d_scale, d_amax, yq: as amp_rmsnorm, [rows, cols];
  *   ckpt: x in FP8, q [rows, 2*cols], the tiles starting again at u: tile kb of
  *      half i is at s[(i*ceil(cols/128) + kb)*lds + r] (for cols % 128 == 0
  *      the layout of any [rows, 2*cols] matrix in tiles).
+ * The sigmoid s is formed from the hardware's exponential and reciprocal: for
+ * g >= -87 it is within 6 2^-24 + (1 - s) |g| 2^-22 of its value, relatively;
+ * below, where it leaves FP32's normal range, within 2^-125 (it may be 0,
+ * which a u of 2^100 makes visible).  Products are FP32, from the left.
  * No output may overlap x.  rows or cols == 0 is a no-op. */
 int amp_swiglu(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx, void* y, int yt,
                int64_t ldy, const float* d_scale, float* d_amax, const amp_fp8_tiles* yq,
@@ -496,9 +500,9 @@ int amp_swiglu(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx, v
  *      operand of the product before the activation;
  *   yqt: y^T [cols, rows] in 1x128 tiles, y recomputed: the wgrad operand of
  *      the product after it.
- * Apart from dx no output may overlap an input.  The sigmoid is formed from
- * the hardware's exponential and reciprocal: s is within a few 2^-24 + (1 - s)
- * |g| 2^-22 of its value, relatively.  rows or cols == 0 is a no-op. */
+ * s as in amp_swiglu; 1 - s is formed as exp(-g) s.  dy s is formed first.
+ * Apart from dx in the place of x no output may overlap an input.  rows or
+ * cols == 0 is a no-op. */
 int amp_swiglu_backward(const void* dy, int dt, int64_t rows, int64_t cols, int64_t lddy,
                         const void* x, int64_t ldx, const amp_fp8_tiles* ckpt, void* dx,
                         int64_t lddx, const amp_fp8_tiles* dxq, const amp_fp8_tiles* dxqt,

@@ -51,3 +51,23 @@ def test_norm_backward_in_place_of_the_stored_input(dt, rows, cols):
         work.codes()
         if gradient:
             check_values(dgamma.values()[0], FMT[amp.F32], wg, (rows + 8) * U * np.abs(dy.v * h.v * r[:, None]).sum(0), "dgamma")
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 100])
+def test_sigmoid_over_its_whole_range(scale):
+    """s as the header bounds it, through du = dy s g with dy a power of two
+    (FP32) and through y = g s u with u one (BF16, whose range is FP32's)."""
+    rows, cols, dt = 5, 4096, amp.F32
+    gv = np.linspace(-135.0, 100.0, rows * cols).reshape(rows, cols)
+    x = Mat(rows, 2 * cols, dt, 1, np.concatenate([gv, np.full((rows, cols), scale)], 1))
+    dy, dx, y = Mat(rows, cols, dt, 2, np.full((rows, cols), scale)), Mat(rows, 2 * cols, dt), Mat(rows, cols, amp.BF16)
+    g = x.v[:, :cols]
+    s, om = B.sigmoid(g), B.sigmoid(-g)
+    # the header's bounds of s, and a rounding of the product with g (that with a power of two has none: where s is
+    # normal dy s and g s u are, and below 2^-126 the absolute bound holds)
+    es = np.where(g >= -87, s * (6 * U + om * np.abs(g) * 4 * U), 2.0 ** -125)
+    err = np.abs(g) * scale * (es + U * s)
+    amp.amp_swiglu_backward(dy.d, dt, rows, cols, dy.ld, x.d, x.ld, None, dx.d, dx.ld)
+    amp.amp_swiglu(x.d, dt, rows, cols, x.ld, y.d, amp.BF16, y.ld)
+    check_values(dx.values()[:, cols:], FMT[dt], g * s * scale, err, "du")
+    check_values(y.values(), FMT[amp.BF16], g * s * scale, err, "y")
