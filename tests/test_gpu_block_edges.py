@@ -8,8 +8,9 @@ import mixed_precision_numerics_amd as amp
 from oracle import block as B
 from oracle import formats as F
 from block_util import U, check_scaled, check_values, dx_err, norm_err
-from gpu_util import dev
-from test_gpu_block import FMT, TYPES, Mat, Tiles, rand
+from gpu_util import dev, host
+import test_gpu_block as plain
+from test_gpu_block import FMT, NPT, TYPES, Mat, Tiles, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +72,58 @@ def test_sigmoid_over_its_whole_range(scale):
     amp.amp_swiglu(x.d, dt, rows, cols, x.ld, y.d, amp.BF16, y.ld)
     check_values(dx.values()[:, cols:], FMT[dt], g * s * scale, err, "du")
     check_values(y.values(), FMT[amp.BF16], g * s * scale, err, "y")
+
+
+# ------------------------------------------- what lies behind an input's rows ---
+
+class Hollow(Mat):
+    """A Mat that, as an input, has NaN (all bits set in every type) behind its rows and its end."""
+
+    def __init__(self, rows, cols, t, pad=0, v=None):
+        super().__init__(rows, cols, t, pad, v)
+        if v is not None:
+            a = host(self.d, NPT[t]).copy()
+            keep = self.codes().copy()
+            a.view(np.uint8)[:] = self.fill = 0xFF
+            a[:rows * self.ld].reshape(rows, self.ld)[:, :cols] = keep
+            self.d = dev(a)
+
+
+@pytest.fixture
+def hollow(monkeypatch):
+    monkeypatch.setattr(plain, "Mat", Hollow)
+
+
+@pytest.mark.parametrize("xt", TYPES)
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 5), (2, 129), (9, 511), (33, 2047), (1027, 1401), (2, 7001), (2, 20483), (3, 70003)])
+def test_norm_reads_its_rows_alone(hollow, xt, rows, cols):
+    plain.test_norm_every_output(xt, rows, cols)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("saved", ["stored", "checkpoint"])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 5), (2, 129), (33, 2047), (700, 41), (601, 515), (530, 1501), (4, 7001), (9, 25001), (2, 40003)])
+def test_norm_backward_reads_its_rows_alone(hollow, dt, saved, rows, cols):
+    plain.test_norm_backward(dt, saved, rows, cols)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 5), (2, 129), (37, 201), (9, 2047), (3, 4101)])
+def test_swiglu_and_its_backward_read_their_rows_alone(hollow, dt, rows, cols):
+    plain.test_swiglu_every_output(dt, rows, cols)
+    for saved in ("stored", "checkpoint"):
+        plain.test_swiglu_backward_in_the_gradients_type(dt, saved, rows, cols)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("saved", ["stored", "checkpoint"])
+@pytest.mark.parametrize("rows,cols", [(1, 128), (129, 256)])
+def test_swiglu_backward_reads_its_rows_alone_for_every_fp8_operand(hollow, dt, saved, rows, cols):
+    plain.test_swiglu_backward_every_fp8_operand(dt, saved, rows, cols)
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 3), (5, 7), (129, 201), (260, 333)])
+def test_transposed_operands_read_their_rows_alone(hollow, rows, cols):
+    plain.test_swiglu_backward_transposed_operands_at_odd_widths(rows, cols)
+    plain.test_requantize(rows, cols, amp.E4M3, amp.E5M2, amp.BF16)
+    plain.test_requantize(rows, cols, amp.E5M2, amp.E4M3, None)
