@@ -7,7 +7,7 @@ import torch
 import mixed_precision_numerics_amd as amp
 from oracle import block as B
 from oracle import formats as F
-from block_util import U, check_scaled, check_values, dx_err, norm_err
+from block_util import U, check_scaled, check_values, dx_err, norm_err, swiglu_back_err, swiglu_err
 from gpu_util import dev, host
 import test_gpu_block as plain
 from test_gpu_block import FMT, NPT, TYPES, Mat, Tiles, rand
@@ -127,3 +127,37 @@ def test_transposed_operands_read_their_rows_alone(hollow, rows, cols):
     plain.test_swiglu_backward_transposed_operands_at_odd_widths(rows, cols)
     plain.test_requantize(rows, cols, amp.E4M3, amp.E5M2, amp.BF16)
     plain.test_requantize(rows, cols, amp.E5M2, amp.E4M3, None)
+
+
+# --------------------------------------- forms that the other tests do not combine ---
+
+@pytest.mark.parametrize("xt", TYPES)
+@pytest.mark.parametrize("gt", TYPES)
+@pytest.mark.parametrize("rows,cols", [(3, 512), (5, 1003), (600, 520)])
+def test_norm_with_gamma_of_another_type(xt, gt, rows, cols):
+    x, dy = Mat(rows, cols, xt, 1, rand(1, rows, cols)), Mat(rows, cols, xt, 2, rand(2, rows, cols))
+    gamma = Mat(1, cols, gt, 0, 1 + rand(3, 1, cols, scale=0.1))
+    yq, rstd, dx, dgamma = Tiles(rows, cols), Mat(1, rows, amp.F32), Mat(rows, cols, xt), Mat(1, cols, amp.F32)
+    work = Mat(min(rows, amp.RMSNORM_PARTIALS), cols, amp.F32)
+    amp.amp_rmsnorm(x.d, xt, rows, cols, x.ld, None, 0, gamma.d, gt, 1e-5, yq=yq.arg, rstd=rstd.d)
+    wy, _ = B.rmsnorm(x.v, gamma.v[0], 1e-5)
+    yq.check(wy, np.abs(wy) * (norm_err(cols) + 3 * U), "yq")
+    r = rstd.values()[0]
+    amp.amp_rmsnorm_backward(dy.d, xt, rows, cols, dy.ld, x.d, x.ld, None, gamma.d, gt, rstd.d, None, 0, dx.d, dx.ld, dgamma.d, work.d)
+    wx, wg = B.rmsnorm_backward(dy.v, x.v, gamma.v[0], r)
+    check_values(dx.values(), FMT[xt], wx, dx_err(dy.v, x.v, gamma.v[0], r, None, wx), "dx")
+    check_values(dgamma.values()[0], FMT[amp.F32], wg, (rows + 8) * U * np.abs(dy.v * x.v * r[:, None]).sum(0), "dgamma")
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("rows,cols", [(3, 5), (130, 201), (129, 256)])
+def test_swiglu_backward_in_place_with_fp8_operands(dt, rows, cols):
+    """dx replaces x while the same call writes the transposed operands."""
+    x, dy = Mat(rows, 2 * cols, dt, 3, rand(1, rows, 2 * cols)), Mat(rows, cols, dt, 1, rand(2, rows, cols))
+    g, u = x.v[:, :cols], x.v[:, cols:]
+    dxqt, yqt = Tiles(2 * cols, rows, amp.E5M2, 3), Tiles(cols, rows, amp.E4M3, 5)
+    amp.amp_swiglu_backward(dy.d, dt, rows, cols, dy.ld, x.d, x.ld, None, x.d, x.ld, None, dxqt.arg, yqt.arg)
+    w, e = np.concatenate(B.swiglu_backward(dy.v, g, u), 1), np.concatenate(swiglu_back_err(dy.v, g, u), 1)
+    check_values(x.values(), FMT[dt], w, e, "dx in place of x")
+    dxqt.check(w.T, e.T, "dxqt")
+    yqt.check(B.swiglu(g, u).T, swiglu_err(g, u).T, "yqt")
