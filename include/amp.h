@@ -458,8 +458,10 @@ int amp_rmsnorm(const void* x, int xt, int64_t rows, int64_t cols, int64_t ldx,
  *    res; may be dy, dres or h themselves, with the same stride; NULL for none.
  * dgamma: [cols] FP32, overwritten (zeros for rows == 0); NULL for none.
  * d_work: FP32 [min(rows, AMP_RMSNORM_PARTIALS), cols], the partial sums of
- *    dgamma (needed with dgamma); calls that may overlap need one each.  The
- *    sums are added in a fixed order: the result is reproducible.
+ *    dgamma (needed with dgamma, though calls of few rows leave it untouched);
+ *    calls that may overlap need one each.  The sums are added in an order that
+ *    the sizes, the types and dx in the place of dy or h decide, and nothing
+ *    else: the result is reproducible.
  * Apart from dx in the place of one of those three no output may overlap an
  * input.  cols == 0 is a no-op. */
 #define AMP_RMSNORM_PARTIALS 256

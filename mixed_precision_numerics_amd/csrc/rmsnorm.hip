@@ -188,9 +188,10 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_rows(const NormArgs
 }
 
 // Rows too long for the registers: a block walks its row twice (the second
-// reads come from the caches; 1024 x 65536 with residual and tiles BF16 91 us =
-// 5.2 TB/s, FP32 with a checkpoint 150).  In place, h is what the second walk
-// reads.
+// reads come from the caches; 1024 x 73728 with residual and tiles BF16 133 us =
+// 4.0 TB/s, 1024 x 65536 FP32 with a checkpoint and a 16-bit y 149 = 3.2; 1024 x
+// 65536 BF16, the longest that the registers hold, 89 = 5.3).  In place, h is
+// what the second walk reads.
 template <int XT>
 __global__ __launch_bounds__(1024) void rmsnorm_long(const NormArgs a) {
   constexpr int E = kVec<XT>, T = 1024;
@@ -489,7 +490,9 @@ __global__ __launch_bounds__(S > 1 ? 512 : 1024) void rmsnorm_back_rows(const No
 // the second time from the caches.  Against rmsnorm_back_rows and dgamma_sum,
 // BF16: 1 x 4096 3.7 us (5.7), 64 x 1000 3.6 (6.7), 512 x 4096 8.7 (9.6), 512 x
 // 512 5.0 (6.4); beyond kFewRows the columns' blocks last longest (1000 x 2047
-// 13.1 against 11.0, 2000 x 512 17.8 against 7.9).
+// 13.1 against 11.0, 2000 x 512 17.8 against 7.9).  The bound of 512 vectors is
+// where one vector a thread ends; wider rows were not measured in this form (1 x
+// 5120 takes 3.4 and 2.7 us in two launches).
 template <int XT, bool CK, int S>
 __global__ __launch_bounds__(512) void rmsnorm_back_few(const NormBackArgs a, float* dgamma, int sums) {
   constexpr int E = kVec<XT>, kCols = 32, G = kCols / E, P = 512 / G, R = 4;
@@ -567,7 +570,8 @@ __global__ __launch_bounds__(512) void rmsnorm_back_few(const NormBackArgs a, fl
 // Rows of more than two vectors in each of 1024 threads, whose sums and next
 // row have no registers: dx by one block a row, and the sums of dy n in a pass
 // of their own, which reads dy and h again.  (Kept together with the sums in
-// the LDS, 2000 x 28672 BF16 took 238 us, and in the work area 440.)  HBM-bound
+// the LDS, 2000 x 28672 BF16 took 238 us, and in the work area 440, both measured
+// before the values were formed again after the row's sum.)  HBM-bound
 // with both passes' reads: 2000 x 20480 BF16 stored 97 us = 4.2 TB/s, from a
 // checkpoint with dres 107 (143 while the values of dy and h stayed in
 // registers over the row's sum, which spilled).

@@ -65,7 +65,8 @@ __device__ __forceinline__ void store_row_tiles(const amp_fp8_tiles& o, int64_t 
 // W threads cover W vectors of a row, 256 / W rows side by side and R of
 // those groups one after the other; blockIdx.x runs along the row.  FULL: the
 // row is whole spans of W vectors.  HBM-bound: 8192 x 14336 BF16 with tiles and
-// checkpoint 138 us = 6.0 TB/s; one row of 14336 3.1 us, the launch.
+// checkpoint 137 us = 6.1 TB/s, 4096 x 14336 FP32 102 = 6.4; one row of 14336 2.5
+// us in a captured graph, the launch.
 template <int XT, int W, int R, bool FULL>
 __global__ __launch_bounds__(256) void swiglu_rows(const GateArgs a) {
   constexpr int E = kVec<XT>, S = 256 / W;
@@ -122,8 +123,10 @@ __global__ __launch_bounds__(256) void swiglu_rows(const GateArgs a) {
 }
 
 // Backward with dx in the gradient's own type only: element-wise, laid out
-// as above; HBM-bound (777 x 2049 FP16 stored: 6.6 us, 2.8 at the copy rate;
-// rows of odd length begin at any alignment).
+// as above; HBM-bound (8192 x 14336 BF16 stored 182 us = 6.4 TB/s, from a
+// checkpoint 151 = 6.3; 777 x 2049 FP16 stored 6.0 in a captured graph, 776 x 2048
+// 3.9, 2.8 at the copy rate: rows of odd length begin at any byte, which reads
+// 1.26 times the bytes).
 template <int XT, bool CK, int W, int R, bool FULL>
 __global__ __launch_bounds__(256) void swiglu_back_rows(const GateArgs a) {
   constexpr int E = kVec<XT>, S = 256 / W;
