@@ -10,7 +10,8 @@
  *      gradient accumulation and global-norm clipping;
  *   4. what lies between the GEMMs of a transformer block in fine-grained FP8:
  *      RMS norm and gated activation with FP8 outputs and FP8 activation
- *      checkpoints, and their backward passes.
+ *      checkpoints, and their backward passes; and the gated feed-forward
+ *      block whose projections, activation and product are one kernel.
  *
  * Conventions for every call
  * --------------------------
@@ -521,6 +522,53 @@ int amp_requantize_blockwise(const amp_fp8_tiles* x, int64_t rows, int64_t cols,
                              const float* d_row, const void* col, int ct,
                              const amp_fp8_tiles* qt, void* stream);
 
+/* ---- Gated feed-forward block: both projections, the activation and the
+ * product in one kernel, and its backward pass -------------------------------
+ * x [M, K] (M tokens), w [2F, K]: the gate projection's F rows, then the up
+ * projection's (the layout whose product with x is amp_swiglu's input).
+ *   [g | u] = x w^T,  s = sigmoid(g) (as amp_swiglu forms it),  y = g s u
+ * Operands and results are of one type t, AMP_BF16 or AMP_F16; products are
+ * exact and summed in FP32, y is formed from the FP32 sums, each result is
+ * rounded once.  Any size, row stride and 2-byte alignment; rows that are 16-byte
+ * aligned (pointers, strides % 8 == 0 and, in the backward pass, F % 4 == 0 and
+ * K % 8 == 0) are the fast ones.  No output may overlap an input or another
+ * output, but for dgu and gu as said below.  K and F are at most 2^26 and a
+ * product may have at most 2^24 tiles of 128 x 128 (else AMP_EUNSUPPORTED). */
+
+/* amp_gemm_swiglu -- the forward pass.  Up to 64 tokens (one token included)
+ * the weights stream past them once.
+ * x: [M, K], stride ldx >= K.  w: [2F, K], stride ldw >= K.
+ * y: [M, F], stride ldy >= F; NULL for none.
+ * gu: [g | u] rounded, [M, 2F], stride ldgu >= 2F, for the backward pass; NULL
+ *    for none.  One of y and gu at least.
+ * K == 0 writes zeros; M or F == 0 is a no-op. */
+int amp_gemm_swiglu(int64_t M, int64_t F, int64_t K, const void* x, int t, int64_t ldx,
+                    const void* w, int64_t ldw, void* y, int64_t ldy, void* gu, int64_t ldgu,
+                    void* stream);
+
+/* amp_gemm_swiglu_backward -- its gradients.
+ *   dg = dy u s (1 + g (1 - s));  du = dy g s;  dgu = [dg | du]
+ *   dx = dgu w;  dw = dgu^T x       (of the dgu that is stored, rounded to t)
+ * dy: [M, F], stride lddy >= F.  x, w as in the forward call.
+ * gu: what the forward call kept, or NULL: g and u are formed again from x and w
+ *    (and enter unrounded).
+ * dgu: [M, 2F], stride lddgu >= 2F, required; may be gu itself, with its stride.
+ * y: [M, F], stride ldy, y formed again; only without gu (AMP_EINVAL with it: y
+ *    is what the forward call returned); NULL for none.
+ * dx: [M, K], stride lddx >= K; NULL for none.
+ * dw: [2F, K] of dwt in {t, AMP_F32}, stride lddw >= K, overwritten; NULL for none.
+ * d_work: AMP_GEMM_SWIGLU_WORK FP32, partial sums of products whose outputs are
+ *    too few for the machine; calls that may overlap need one each.  NULL: no
+ *    such parts (slower then).  How sums are split follows from sizes alone: the
+ *    results are reproducible.
+ * M == 0: dw = 0.  F == 0: dx = 0. */
+#define AMP_GEMM_SWIGLU_WORK (1 << 23)
+int amp_gemm_swiglu_backward(int64_t M, int64_t F, int64_t K, const void* dy, int t, int64_t lddy,
+                             const void* x, int64_t ldx, const void* w, int64_t ldw,
+                             const void* gu, int64_t ldgu, void* dgu, int64_t lddgu, void* y,
+                             int64_t ldy, void* dx, int64_t lddx, void* dw, int dwt, int64_t lddw,
+                             float* d_work, void* stream);
+
 /* ---- FP16 AMP training step of a two-layer MLP: the element-wise glue ----
  * Page "혼합 정밀도 학습" (itwiki), section "FP16 학습 루프": Linear(512, 2048)
  * -> GELU -> Linear(2048, 10) under FP16 autocast with cross-entropy in FP32
@@ -631,6 +679,46 @@ int amp_optimizer_step_ex(float* master, float* m, float* v, const void* grads, 
                           void* w16, int wt, int64_t n, const amp_adamw_hparams* hp,
                           amp_scaler_state* d_state, const float* d_grad_mult, int flags,
                           void* stream);
+
+/* ---- the same over a list of tensors ----------------------------------------
+ * A model's gradients are hundreds of tensors: these calls take all of them at
+ * once, in a host array that is read during the call only.  Typical step:
+ * amp_grad_norm_list, then either the optimizer step with d_out as its
+ * d_grad_mult, or amp_grad_clip_list. */
+typedef struct {
+  void* p;      /* device memory, aligned to an element */
+  int64_t n;    /* elements, one after another; 0 is valid (p is then ignored) */
+  int32_t type; /* AMP_F32, AMP_F16 or AMP_BF16 */
+  int32_t pad_;
+} amp_tensor;
+
+/* Tensors of one call (more: AMP_EUNSUPPORTED), and the most elements of one. */
+#define AMP_LIST_TENSORS 65536
+#define AMP_LIST_ELEMENTS ((int64_t)1 << 37)
+
+/* amp_grad_norm_list -- what amp_grad_norm_init (first != 0), one
+ * amp_grad_norm_accumulate per tensor and amp_clip_coefficient do, in one pass:
+ *   sumsq = (first ? 0 : sumsq) + sum_t sum_i (f32(g_t[i]) * (1/S))^2
+ * over the finite elements, in float64 and an order that the lengths and the
+ * tensors' order decide (reproducible); any other element sets
+ * d_state->found_inf = 1.  Then, with d_out: d_out = {coef, norm} as by
+ * amp_clip_coefficient with max_norm (d_out NULL: max_norm is ignored).
+ * Calls on one d_norm must not overlap.  count == 0 is an empty sum. */
+int amp_grad_norm_list(const amp_tensor* grads, int32_t count, int first,
+                       amp_scaler_state* d_state, amp_grad_norm_state* d_norm, float max_norm,
+                       float* d_out, void* stream);
+
+/* amp_grad_clip_list -- unscaled and clipped gradients:
+ *   out_t[i] = round( fl32( fl32(f32(g_t[i]) * (1/S)) * *d_coef ) )
+ * the products that amp_optimizer_step_ex forms of d_grad_mult.  S =
+ * d_state->scale (d_state NULL: 1); d_coef: device FP32 (NULL: 1).  inf and NaN
+ * propagate; values beyond FP16's range become inf.
+ * outs: count tensors of the same lengths, each of any of the three types; NULL
+ * or tensors that are the gradients themselves (same p and type): in place,
+ * where a factor of exactly 1 leaves the tensor as it is.  No other overlap of
+ * an output with any tensor of the call is allowed. */
+int amp_grad_clip_list(const amp_tensor* grads, const amp_tensor* outs, int32_t count,
+                       const amp_scaler_state* d_state, const float* d_coef, void* stream);
 
 /* amp_stream_copy -- a plain device copy dst[0..bytes) = src[0..bytes), the
  * reference for the HBM roofline of the element-wise kernels (not a step of

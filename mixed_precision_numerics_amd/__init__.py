@@ -33,7 +33,8 @@ __all__ = [
     "amp_quantize_blockwise", "amp_gemm_blockwise", "amp_cast_ex",
     "amp_found_inf_from_amax", "amp_stream_copy", "amp_grad_norm_accumulate_noalloc",
     "amp_fp8_mfma_probe", "Fp8Tiles", "RMSNORM_PARTIALS", "amp_rmsnorm", "amp_rmsnorm_backward",
-    "amp_swiglu", "amp_swiglu_backward", "amp_requantize_blockwise",
+    "amp_swiglu", "amp_swiglu_backward", "amp_requantize_blockwise", "GEMM_SWIGLU_WORK",
+    "amp_gemm_swiglu", "amp_gemm_swiglu_backward", "TensorList", "amp_grad_norm_list", "amp_grad_clip_list",
 ]
 
 F32, F16, BF16, E4M3, E5M2, E2M1X2 = 0, 1, 2, 3, 4, 5
@@ -46,6 +47,7 @@ OPT_SKIP_CHECK = 1
 GEMM_FP8_NATIVE = 1
 GEMM_MX = 2
 RMSNORM_PARTIALS = 256                     # rows of amp_rmsnorm_backward's work area
+GEMM_SWIGLU_WORK = 1 << 23                 # FP32 numbers of amp_gemm_swiglu_backward's work area
 
 # Device-resident state layouts (mirror the C structs; for reading back).
 SCALER_STATE_DTYPE = np.dtype([("scale", "<f4"), ("growth_tracker", "<i4"),
@@ -101,6 +103,40 @@ class Fp8Tiles(ctypes.Structure):
         self.tensors = (q, s)
 
 
+class _Tensor(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("n", ctypes.c_int64), ("type", ctypes.c_int32), ("pad_", ctypes.c_int32)]
+
+
+class TensorList:
+    """A list of ``(tensor or pointer, elements, type)`` (an array of ``amp_tensor``).
+
+    Made once, e.g. beside a model's parameters, and passed to every step.
+    Tensors are kept alive; each has to hold its elements one after another on
+    one GPU, checked here, and has to stay where it was: a call with a list of
+    which one was resized or given other storage is refused."""
+
+    def __init__(self, entries):
+        entries = list(entries)
+        self.array = (_Tensor * len(entries))()
+        self.tensors, self.where = [], None
+        for i, (t, n, dtype) in enumerate(entries):
+            if dtype not in (F32, F16, BF16):
+                raise ValueError(f"TensorList: tensor {i} is of type {dtype}")
+            _room("TensorList", f"tensor {i}", t, _vec(n, dtype))
+            a = self.array[i]
+            a.p, a.n, a.type = _ptr(t), n, dtype
+            if n > 0 and hasattr(t, "get_device"):
+                self.tensors.append(t)
+                if self.where is None:
+                    self.where = t.get_device()
+                elif self.where != t.get_device():
+                    raise ValueError(f"TensorList: tensor {i} is on {t.device}, others are not")
+        self.places = [t.data_ptr() for t in self.tensors]
+
+    def __len__(self):
+        return len(self.array)
+
+
 _P, _I, _I64, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64
 _SIGS = {
     "amp_abi_version": ([], _I),
@@ -144,6 +180,11 @@ _SIGS = {
     "amp_swiglu_backward": ([_P, _I, _I64, _I64, _I64, _P, _I64, _P, _P, _I64, _P, _P, _P, _P],
                             _I),
     "amp_requantize_blockwise": ([_P, _I64, _I64, _P, _P, _I, _P, _P], _I),
+    "amp_gemm_swiglu": ([_I64, _I64, _I64, _P, _I, _I64, _P, _I64, _P, _I64, _P, _I64, _P], _I),
+    "amp_gemm_swiglu_backward": ([_I64, _I64, _I64, _P, _I, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                                  _P, _I, _I64, _P, _P], _I),
+    "amp_grad_norm_list": ([_P, ctypes.c_int32, _I, _P, _P, ctypes.c_float, _P, _P], _I),
+    "amp_grad_clip_list": ([_P, _P, ctypes.c_int32, _P, _P, _P], _I),
     "amp_bias_gelu_f16": ([_P, _I64, _I64, _P, _P, _P, _P], _I),
     "amp_softmax_xent_f16": ([_P, _P, _I64, _I64, _P, _P, _P, _P], _I),
     "amp_gelu_backward_f16": ([_P, _P, _I64, _P, _P], _I),
@@ -533,6 +574,58 @@ def amp_requantize_blockwise(x, rows, cols, d_row, col, ct, qt, stream=None):
     _check(f, load().amp_requantize_blockwise(
         _tiles(f, "x", x, rows, cols, at), rows, cols, _mem(f, "d_row", d_row, _vec(rows, F32), at),
         _mem(f, "col", col, _vec(cols, ct), at), ct, _tiles(f, "qt", qt, cols, rows, at),
+        _ready(f, stream, at)))
+
+
+def amp_gemm_swiglu(M, F, K, x, t, ldx, w, ldw, y=None, ldy=0, gu=None, ldgu=0, stream=None):
+    f = "amp_gemm_swiglu"
+    at = _where()
+    _check(f, load().amp_gemm_swiglu(
+        M, F, K, _mem(f, "x", x, _mat(M, K, ldx, t), at), t, ldx, _mem(f, "w", w, _mat(2 * F, K, ldw, t), at), ldw,
+        _mem(f, "y", y, _mat(M, F, ldy, t), at), ldy, _mem(f, "gu", gu, _mat(M, 2 * F, ldgu, t), at), ldgu,
+        _ready(f, stream, at)))
+
+
+def amp_gemm_swiglu_backward(M, F, K, dy, t, lddy, x, ldx, w, ldw, gu, ldgu, dgu, lddgu, y=None, ldy=0, dx=None, lddx=0,
+                             dw=None, dwt=BF16, lddw=0, d_work=None, stream=None):
+    f = "amp_gemm_swiglu_backward"
+    at = _where()
+    _check(f, load().amp_gemm_swiglu_backward(
+        M, F, K, _mem(f, "dy", dy, _mat(M, F, lddy, t), at), t, lddy, _mem(f, "x", x, _mat(M, K, ldx, t), at), ldx,
+        _mem(f, "w", w, _mat(2 * F, K, ldw, t), at), ldw, _mem(f, "gu", gu, _mat(M, 2 * F, ldgu, t), at), ldgu,
+        _mem(f, "dgu", dgu, _mat(M, 2 * F, lddgu, t), at), lddgu, _mem(f, "y", y, _mat(M, F, ldy, t), at), ldy,
+        _mem(f, "dx", dx, _mat(M, K, lddx, t), at), lddx, _mem(f, "dw", dw, _mat(2 * F, K, lddw, dwt), at), dwt, lddw,
+        _mem(f, "d_work", d_work, _vec(GEMM_SWIGLU_WORK, F32), at), _ready(f, stream, at)))
+
+
+def _listed(fn: str, what: str, ts: TensorList | None, at: list) -> int | None:
+    """Address of a list's array; a tensor that has moved is refused."""
+    if ts is None:
+        return None
+    if [t.data_ptr() for t in ts.tensors] != ts.places:
+        raise ValueError(f"{fn}: a tensor of {what} has moved since the TensorList was made from it")
+    if ts.tensors and ts.where != at[0]:
+        at.append(f"{what} is on {ts.tensors[0].device}")
+    return ctypes.addressof(ts.array)
+
+
+def amp_grad_norm_list(grads: TensorList, first, d_state, d_norm, max_norm=1.0, d_out=None, stream=None):
+    f = "amp_grad_norm_list"
+    at = _where()
+    _check(f, load().amp_grad_norm_list(
+        _listed(f, "grads", grads, at), len(grads), int(bool(first)),
+        _mem(f, "d_state", d_state, SCALER_STATE_DTYPE.itemsize, at), _mem(f, "d_norm", d_norm, NORM_STATE_BYTES, at),
+        float(max_norm), _mem(f, "d_out", d_out, 8, at), _ready(f, stream, at)))
+
+
+def amp_grad_clip_list(grads: TensorList, outs: TensorList | None = None, d_state=None, d_coef=None, stream=None):
+    f = "amp_grad_clip_list"
+    if outs is not None and len(outs) != len(grads):
+        raise ValueError(f"{f}: {len(grads)} gradients, {len(outs)} outputs")
+    at = _where()
+    _check(f, load().amp_grad_clip_list(
+        _listed(f, "grads", grads, at), _listed(f, "outs", outs, at), len(grads),
+        _mem(f, "d_state", d_state, SCALER_STATE_DTYPE.itemsize, at), _mem(f, "d_coef", d_coef, 4, at),
         _ready(f, stream, at)))
 
 

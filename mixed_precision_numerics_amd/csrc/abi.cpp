@@ -71,6 +71,30 @@ int tiles_status(const amp_fp8_tiles* t, int64_t rows, int64_t cols) {
   return AMP_OK;
 }
 
+// Sizes of a gated feed-forward block: columns as above, and tiles whose
+// threads a launch can count.
+bool block_sizes(int64_t M, int64_t F, int64_t K) {
+  if (K > kMostCols || F > kMostCols || M > (int64_t(1) << 31)) return false;
+  const int64_t m = (M + 127) / 128, f = (2 * F + 127) / 128, k = (K + 127) / 128, most = int64_t(1) << 24;
+  return m * (f > k ? f : k) <= most && f * k <= most;
+}
+
+// Tensors of a list (outs: of the same lengths).
+int list_status(const amp_tensor* a, const amp_tensor* outs, int32_t count) {
+  if (count < 0) return AMP_EINVAL;
+  if (count > AMP_LIST_TENSORS) return AMP_EUNSUPPORTED;
+  if (count > 0 && !a) return AMP_EINVAL;
+  for (int32_t i = 0; i < count; ++i) {
+    if (a[i].n < 0 || (outs && outs[i].n != a[i].n)) return AMP_EINVAL;
+    if (!is_grad(a[i].type) || (outs && !is_grad(outs[i].type)) || a[i].n > AMP_LIST_ELEMENTS) return AMP_EUNSUPPORTED;
+    if (a[i].n == 0) continue;
+    for (const amp_tensor* t : {a + i, outs ? outs + i : a + i})
+      if (!t->p || !al(t->p, t->type == AMP_F32 ? 4 : 2)) return AMP_EINVAL;
+    if (outs && outs[i].p == a[i].p && outs[i].type != a[i].type) return AMP_EINVAL;
+  }
+  return AMP_OK;
+}
+
 amp_fp8_tiles or_none(const amp_fp8_tiles* t) { return t ? *t : amp_fp8_tiles{}; }
 
 }  // namespace
@@ -495,6 +519,58 @@ int amp_requantize_blockwise(const amp_fp8_tiles* x, int64_t rows, int64_t cols,
   if (int e = tiles_status(qt, cols, rows)) return e;
   if (int e = check_device()) return e;
   return hip_status(amp::launch_requantize(*x, rows, cols, d_row, col, ct, *qt, static_cast<hipStream_t>(stream)));
+}
+
+int amp_gemm_swiglu(int64_t M, int64_t F, int64_t K, const void* x, int t, int64_t ldx, const void* w, int64_t ldw, void* y,
+                    int64_t ldy, void* gu, int64_t ldgu, void* stream) {
+  if (M < 0 || F < 0 || K < 0) return AMP_EINVAL;
+  if ((t != AMP_BF16 && t != AMP_F16) || !block_sizes(M, F, K)) return AMP_EUNSUPPORTED;
+  if (M == 0 || F == 0) return AMP_OK;
+  if ((K > 0 && (!x || !w)) || (!y && !gu) || !al(x, 2) || !al(w, 2) || !al(y, 2) || !al(gu, 2)) return AMP_EINVAL;
+  if (ldx < K || ldw < K || (y && ldy < F) || (gu && ldgu < 2 * F)) return AMP_EINVAL;
+  if (int e = check_device()) return e;
+  return hip_status(amp::launch_gemm_swiglu(M, F, K, x, t, ldx, w, ldw, y, ldy, gu, ldgu, static_cast<hipStream_t>(stream)));
+}
+
+int amp_gemm_swiglu_backward(int64_t M, int64_t F, int64_t K, const void* dy, int t, int64_t lddy, const void* x, int64_t ldx,
+                             const void* w, int64_t ldw, const void* gu, int64_t ldgu, void* dgu, int64_t lddgu, void* y,
+                             int64_t ldy, void* dx, int64_t lddx, void* dw, int dwt, int64_t lddw, float* d_work, void* stream) {
+  if (M < 0 || F < 0 || K < 0) return AMP_EINVAL;
+  if ((t != AMP_BF16 && t != AMP_F16) || (dw && dwt != t && dwt != AMP_F32) || !block_sizes(M, F, K)) return AMP_EUNSUPPORTED;
+  if (gu && y) return AMP_EINVAL;
+  if (!al(dy, 2) || !al(x, 2) || !al(w, 2) || !al(gu, 2) || !al(dgu, 2) || !al(y, 2) || !al(dx, 2) ||
+      !al(dw, dwt == AMP_F32 ? 4 : 2) || !al(d_work, 4))
+    return AMP_EINVAL;
+  if (M > 0 && F > 0) {
+    if (!dy || !dgu || lddy < F || lddgu < 2 * F || (gu && ldgu < 2 * F) || (y && ldy < F)) return AMP_EINVAL;
+    if (gu == dgu && ldgu != lddgu) return AMP_EINVAL;
+    if (K > 0 && (((!gu || dw) && !x) || ((!gu || dx) && !w))) return AMP_EINVAL;
+    if (((!gu || dw) && ldx < K) || ((!gu || dx) && ldw < K)) return AMP_EINVAL;
+  }
+  if ((dx && lddx < K) || (dw && lddw < K)) return AMP_EINVAL;
+  if ((M == 0 || F == 0) && (!dx || M == 0) && (!dw || F == 0)) return AMP_OK;
+  if (int e = check_device()) return e;
+  return hip_status(amp::launch_gemm_swiglu_backward(M, F, K, dy, t, lddy, x, ldx, w, ldw, gu, ldgu, dgu, lddgu, y, ldy, dx, lddx,
+                                                     dw, dwt, lddw, d_work, static_cast<hipStream_t>(stream)));
+}
+
+int amp_grad_norm_list(const amp_tensor* grads, int32_t count, int first, amp_scaler_state* d_state, amp_grad_norm_state* d_norm,
+                       float max_norm, float* d_out, void* stream) {
+  if (!al(d_state, 8) || !al(d_norm, 8) || !al(d_out, 4) || !d_state || !d_norm) return AMP_EINVAL;
+  if (d_out && (!(max_norm > 0.0f) || !(max_norm < 3.0e38f))) return AMP_EINVAL;
+  if (int e = list_status(grads, nullptr, count)) return e;
+  if (int e = check_device()) return e;
+  return hip_status(amp::launch_grad_norm_list(grads, count, first ? 1 : 0, d_state, d_norm, max_norm, d_out,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int amp_grad_clip_list(const amp_tensor* grads, const amp_tensor* outs, int32_t count, const amp_scaler_state* d_state,
+                       const float* d_coef, void* stream) {
+  if (!al(d_state, 8) || !al(d_coef, 4)) return AMP_EINVAL;
+  if (int e = list_status(grads, outs, count)) return e;
+  if (count == 0) return AMP_OK;
+  if (int e = check_device()) return e;
+  return hip_status(amp::launch_grad_clip_list(grads, outs ? outs : grads, count, d_state, d_coef, static_cast<hipStream_t>(stream)));
 }
 
 int amp_bias_gelu_f16(const float* acc, int64_t rows, int64_t cols, const void* b16, void* z16,

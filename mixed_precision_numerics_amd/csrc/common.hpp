@@ -144,6 +144,19 @@ hipError_t launch_swiglu_backward(const void* dy, int dt, int64_t rows, int64_t 
                                   const amp_fp8_tiles& yqt, hipStream_t s);
 hipError_t launch_requantize(const amp_fp8_tiles& x, int64_t rows, int64_t cols, const float* row,
                              const void* col, int ct, const amp_fp8_tiles& qt, hipStream_t s);
+hipError_t launch_gemm_swiglu(int64_t M, int64_t F, int64_t K, const void* x, int t, int64_t ldx,
+                              const void* w, int64_t ldw, void* y, int64_t ldy, void* gu,
+                              int64_t ldgu, hipStream_t s);
+hipError_t launch_gemm_swiglu_backward(int64_t M, int64_t F, int64_t K, const void* dy, int t,
+                                       int64_t lddy, const void* x, int64_t ldx, const void* w,
+                                       int64_t ldw, const void* gu, int64_t ldgu, void* dgu,
+                                       int64_t lddgu, void* y, int64_t ldy, void* dx, int64_t lddx,
+                                       void* dw, int dwt, int64_t lddw, float* work, hipStream_t s);
+hipError_t launch_grad_norm_list(const amp_tensor* grads, int32_t count, int first,
+                                 amp_scaler_state* st, amp_grad_norm_state* ns, float max_norm,
+                                 float* out, hipStream_t s);
+hipError_t launch_grad_clip_list(const amp_tensor* grads, const amp_tensor* outs, int32_t count,
+                                 const amp_scaler_state* st, const float* coef, hipStream_t s);
 hipError_t launch_bias_gelu(const float* acc, int64_t rows, int64_t cols, const void* b16,
                             void* z16, void* a16, hipStream_t s);
 hipError_t launch_softmax_xent(const void* logits16, const int32_t* labels, int64_t rows,

@@ -1,0 +1,520 @@
+// Products of a gated feed-forward block on the matrix cores (gfx950): one
+// tile kernel for the fused forward pass, its recomputing backward form and
+// the two gradient products.
+//
+//   forward      [g | u] = x [Wg; Wu]^T,  y = g sigmoid(g) u   (kOutGate)
+//   backward     dg, du of dy from g, u formed again           (kOutGrad)
+//   gradients    dx = [dg | du] W,  dW = [dg | du]^T x         (kOutC)
+//
+// A block of four waves (2 x 2) owns an output tile of 64 MB x 64 NB (columns
+// of both projections together: a wave's first NB/2 blocks of 32 columns are
+// gate columns, the others the up columns of the same features, so that a
+// lane's accumulators pair up with no exchange).  The summed dimension advances
+// 32 elements at a time through three LDS stages, filled by direct loads two
+// steps ahead, while this step's fragments feed the 32x32x16 instruction.  Two
+// blocks share a CU: one's prologue and epilogue run under the other's products.
+// Operands are contiguous along the summed dimension (KC) or along their rows
+// of outputs (then read with transposing LDS reads).
+//
+// Edges.  Output rows and columns past the end are read from the last valid
+// one (their results are not stored), so no load leaves the operand.  What
+// does not fill a step of the summed dimension is put into LDS through
+// registers, masked with zeros on both sides (a NaN behind a row's end must
+// not meet a zero), as the first step of a tile.  Operands without 16-byte
+// rows go that way in every step (FAST == false).
+#pragma once
+#include <type_traits>
+
+#include "common.hpp"
+#include "formats.hpp"
+#include "gate.hpp"
+#include "mfma.hpp"
+
+namespace amp {
+namespace {
+
+enum Out : int { kOutC = 0, kOutGate = 1, kOutGrad = 2 };
+
+struct ProductArgs {
+  const void* A;           // [M, K], or [K, M] where M is contiguous
+  const void* B;           // [N, K] ([2N, K] with a gate), or [K, N]
+  int64_t M, N, K;         // N: columns of the output (features with a gate)
+  int64_t lda, ldb;
+  void* C; int64_t ldc;    // the product; with a gate y (may be NULL)
+  void* gu; int64_t ldgu;  // kOutGate: [g | u] (may be NULL); kOutGrad: [dg | du]
+  const void* dy; int64_t lddy;
+  int splits;              // parts of the summed dimension; > 1: C is FP32 [splits][M][N]
+};
+
+// 16 bytes at any 2-byte address: one load or store instruction either way.
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ u32x4 ld16u(const uint16_t* p) { return *reinterpret_cast<const u32x4_u*>(p); }
+
+template <int ET>
+__device__ __forceinline__ float from16(uint32_t c) {
+  return ET == AMP_BF16 ? bf16_to_f32(c) : f16_to_f32(c);
+}
+template <int ET>
+__device__ __forceinline__ uint32_t to16(float x) { return ET == AMP_BF16 ? f32_to_bf16(x) : f32_to_f16(x); }
+
+template <int ET>
+__device__ __forceinline__ f32x16 mfma16(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (ET == AMP_F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// Eight elements from p on of which the first n exist, zeros behind them.
+__device__ __forceinline__ u32x4 ld16_part(const uint16_t* p, int n) {
+  if (n >= 8) return ld16u(p);
+  u32x4 v = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) v[j >> 1] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
+  return v;
+}
+
+// LDS writes of one wave before its own reads of them (and reads before the
+// next writes): a wave's LDS operations complete in order, the compiler has to
+// keep that order.
+__device__ __forceinline__ void wave_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// Epilogue of one wave: a band of 32 rows x 32 NBW columns leaves through this
+// wave's LDS region as whole 16-byte pieces of rows (the pitch, a row's bytes +
+// 32, puts the half-waves' writes on disjoint banks).  value(nb, r): the element
+// of column block nb in accumulator register r.
+template <int CT, int NBW, typename V>
+__device__ __forceinline__ void band_out(V&& value, void* C, int64_t ldc, int64_t row0, int64_t col0, int64_t M,
+                                         int64_t N, uint8_t* buf) {
+  constexpr int kES = CT == AMP_F32 ? 4 : 2, kRow = NBW * 32 * kES, kPitch = kRow + 32;
+  constexpr int kLPR = kRow / 16, kRPP = 64 / kLPR, kEPL = 16 / kES;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  wave_lds();
+#pragma unroll
+  for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      uint8_t* p = buf + (8 * (r >> 2) + 4 * h + (r & 3)) * kPitch + (nb * 32 + l32) * kES;
+      const float x = value(nb, r);
+      if constexpr (CT == AMP_F32) *reinterpret_cast<float*>(p) = x;
+      else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(to16<CT>(x));
+    }
+  wave_lds();
+  const int64_t col = col0 + (lane % kLPR) * kEPL;
+#pragma unroll
+  for (int ps = 0; ps < 32 / kRPP; ++ps) {
+    const int rl = ps * kRPP + lane / kLPR;
+    const int64_t row = row0 + rl;
+    const uint8_t* q = buf + rl * kPitch + (lane % kLPR) * 16;
+    if (row >= M || col >= N) continue;
+    uint8_t* out = static_cast<uint8_t*>(C) + (row * ldc + col) * kES;
+    if (col + kEPL <= N) {
+      *reinterpret_cast<u32x4_u*>(out) = *reinterpret_cast<const u32x4*>(q);
+    } else {
+      for (int j = 0; j < N - col; ++j) {
+        if constexpr (CT == AMP_F32) reinterpret_cast<float*>(out)[j] = reinterpret_cast<const float*>(q)[j];
+        else reinterpret_cast<uint16_t*>(out)[j] = reinterpret_cast<const uint16_t*>(q)[j];
+      }
+    }
+  }
+}
+
+// The reverse way: a band of a 16-bit matrix into v[nb][r], zeros outside.
+template <int ET, int NBW>
+__device__ __forceinline__ void band_in(float (&v)[NBW][16], const void* X, int64_t ldx, int64_t row0, int64_t col0,
+                                        int64_t M, int64_t N, uint8_t* buf) {
+  constexpr int kRow = NBW * 64, kPitch = kRow + 32, kLPR = kRow / 16, kRPP = 64 / kLPR;
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int64_t col = col0 + (lane % kLPR) * 8;
+  const int left = col < N ? static_cast<int>(N - col < 8 ? N - col : 8) : 0;
+  u32x4 w[32 / kRPP];
+#pragma unroll
+  for (int ps = 0; ps < 32 / kRPP; ++ps) {
+    const int64_t row = row0 + ps * kRPP + lane / kLPR;
+    w[ps] = row < M ? ld16_part(static_cast<const uint16_t*>(X) + row * ldx + col, left) : u32x4{0u, 0u, 0u, 0u};
+  }
+  wave_lds();
+#pragma unroll
+  for (int ps = 0; ps < 32 / kRPP; ++ps)
+    *reinterpret_cast<u32x4*>(buf + (ps * kRPP + lane / kLPR) * kPitch + (lane % kLPR) * 16) = w[ps];
+  wave_lds();
+#pragma unroll
+  for (int nb = 0; nb < NBW; ++nb)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      v[nb][r] = from16<ET>(*reinterpret_cast<const uint16_t*>(buf + (8 * (r >> 2) + 4 * h + (r & 3)) * kPitch +
+                                                               (nb * 32 + l32) * 2));
+}
+
+// A direct-to-LDS load of 16 bytes a lane (64 lanes fill 1 KB from dst on) that
+// the compiler does not track: the kernel waits for it by count.
+__device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t dst, uint32_t voff, uint32_t soff) {
+  asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc), "s"(soff), "{m0}"(dst));
+}
+
+constexpr int kStepK = 64, kStepBytes = 2 * kStepK;      // elements and bytes of a row of a step
+static_assert(kStepBytes == kRowBytes, "the slots' layout");
+constexpr int kSlots = 5;
+
+// The same in an output-contiguous stage, rows of `pitch` bytes along K.
+__device__ __forceinline__ int mn_at(int k, int c, int pitch) { return k * pitch + ((c ^ (4 * (k & 3))) << 4); }
+
+template <int ET, bool A_KC, bool B_KC, int OUT, int CT, int MB, int NB, bool FAST>
+__global__ __launch_bounds__(256, MB * NB > 8 ? 1 : 2) void product_tiles(ProductArgs g) {
+  constexpr bool kGate = OUT != kOutC;
+  static_assert(!kGate || (A_KC && B_KC), "the projections' operands are K-contiguous");
+  constexpr int BM = 64 * MB, BN = 64 * NB, BNO = kGate ? BN / 2 : BN, NBH = NB / 2;
+  constexpr int kSlot = (MB > NB ? BM : BN) * kStepBytes;      // one operand of a step
+  constexpr int kLA = 2 * MB, kLB = 2 * NB;                    // direct loads of a wave and operand
+  __shared__ __align__(16) uint8_t smem[kSlots * kSlot];
+
+  // Blocks of one XCD (every eighth) take one contiguous run of tiles, eight
+  // tile rows at a time, so that its L2 holds the operands' shared parts.
+  const uint32_t nbm = static_cast<uint32_t>((g.M + BM - 1) / BM), nbn = static_cast<uint32_t>((g.N + BNO - 1) / BNO);
+  const uint32_t total = nbm * nbn, xcd = blockIdx.x % 8, most = total % 8;
+  const uint32_t tile = xcd * (total / 8) + (xcd < most ? xcd : most) + blockIdx.x / 8;
+  constexpr uint32_t kGroup = 8;
+  const uint32_t first_m = tile / (kGroup * nbn) * kGroup;
+  const uint32_t gsz = nbm - first_m < kGroup ? nbm - first_m : kGroup;
+  const uint32_t in_group = tile % (kGroup * nbn);
+  const int64_t m0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(first_m + in_group % gsz)) * BM;
+  const int64_t n0 = static_cast<int64_t>(__builtin_amdgcn_readfirstlane(in_group / gsz)) * BNO;
+
+  const int t = threadIdx.x, lane = t & 63, wave = wave_id();
+  const int wm = wave >> 1, wn = wave & 1, l32 = lane & 31, h = lane >> 5;
+  const int rows_a = static_cast<int>(g.M - m0 < BM ? g.M - m0 : BM);       // what the tile holds of each operand
+  const int rows_b = static_cast<int>(g.N - n0 < BNO ? g.N - n0 : BNO);
+  const uint16_t* A = static_cast<const uint16_t*>(g.A) + (A_KC ? m0 * g.lda : m0);
+  const uint16_t* B = static_cast<const uint16_t*>(g.B) + (B_KC ? n0 * g.ldb : n0);
+  const uint32_t lda_b = static_cast<uint32_t>(g.lda * 2), ldb_b = static_cast<uint32_t>(g.ldb * 2);
+
+  // The steps of this block: whole ones, what is left over being the first.
+  const int whole = static_cast<int>(g.K / kStepK), tail = g.K % kStepK != 0, steps = whole + tail;
+  const int s0 = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<int64_t>(steps) * blockIdx.y / g.splits));
+  const int s1 = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<int64_t>(steps) * (blockIdx.y + 1) / g.splits));
+  auto first_k = [&](int s) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane((tail ? (s == 0 ? whole : s - 1) : s) * kStepK); };
+
+  // LDS row r of the B stage: with a gate, the feature and the projection that
+  // it holds; rows past the end repeat the last.
+  auto row_b = [&](int r) __attribute__((always_inline)) -> int64_t {
+    if constexpr (!kGate) return r < rows_b ? r : rows_b - 1;
+    const int f = r / (32 * NB) * (16 * NB) + r % (16 * NB);
+    return (f < rows_b ? f : rows_b - 1) + (r / (16 * NB) % 2 ? g.N : 0);
+  };
+
+  // ---- direct loads of a whole step, 1 KB of LDS each.  KC: eight rows; lane l
+  // fetches the chunk that belongs at byte 16 l.  Else: K-rows, likewise.
+  uint32_t va[A_KC ? kLA : 2], vb[B_KC ? kLB : 2];
+  constexpr int kChA = BM / 8, kChB = BN / 8, kRowsA = 64 / kChA, kRowsB = 64 / kChB;   // chunks of a K-row, K-rows of a load
+  const int part = kGate ? wave & 1 : 0;
+  const uint16_t* Bw = B + (part ? g.N * g.ldb : 0);      // the wave's projection
+  if constexpr (FAST) {
+#pragma unroll
+    for (int i = 0; i < (A_KC ? kLA : 2); ++i) {
+      if constexpr (A_KC) {
+        const int r = wave * 8 * kLA + 8 * i + lane / 8;
+        va[i] = static_cast<uint32_t>(r < rows_a ? r : rows_a - 1) * lda_b + (((lane & 7) ^ (lane >> 3) ^ ((wave * kLA + i) & 7)) << 4);
+      } else {
+        const int k = i * kRowsA + lane / kChA, c = (lane % kChA) ^ (4 * (k & 3));
+        va[i] = static_cast<uint32_t>(lane / kChA) * lda_b + static_cast<uint32_t>(c < rows_a / 8 ? c : rows_a / 8 - 1) * 16;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < (B_KC ? kLB : 2); ++i) {
+      if constexpr (B_KC) {
+        const int f = (kGate ? wave >> 1 : wave) * 8 * kLB + 8 * i + lane / 8;
+        vb[i] = static_cast<uint32_t>(f < rows_b ? f : rows_b - 1) * ldb_b + (((lane & 7) ^ (lane >> 3) ^ ((wave * kLB + i) & 7)) << 4);
+      } else {
+        const int k = i * kRowsB + lane / kChB, c = (lane % kChB) ^ (4 * (k & 3));
+        vb[i] = static_cast<uint32_t>(lane / kChB) * ldb_b + static_cast<uint32_t>(c < rows_b / 8 ? c : rows_b / 8 - 1) * 16;
+      }
+    }
+  }
+  // bytes from the operand's first to its last element in the tile (KC) or the step
+  const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint16_t*>(A), 0, static_cast<int>(A_KC ? (rows_a - 1) * lda_b + g.K * 2 : 0), 0x00020000);
+  const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint16_t*>(Bw), 0, static_cast<int>(B_KC ? (rows_b - 1) * ldb_b + g.K * 2 : 0), 0x00020000);
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_void*)smem));
+  // Load i of a wave's share; past the end the last step is loaded once more,
+  // into a slot that nobody reads.
+  auto direct_a = [&](int s, int slot, int i) __attribute__((always_inline)) {
+    const int k0 = ((s < s1 ? s : s1 - 1) - tail) * kStepK;
+    const uint32_t dst = lds0 + slot * kSlot + (wave * kLA + i) * 1024;
+    if constexpr (A_KC) {
+      to_lds(ra, dst, va[i], static_cast<uint32_t>(k0 * 2));
+    } else {
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint16_t*>(A + k0 * g.lda), 0, static_cast<int>((kStepK - 1) * lda_b + rows_a * 2), 0x00020000);
+      to_lds(r, dst, va[kRowsA == 2 ? i & 1 : 0], static_cast<uint32_t>(wave * (kStepK / 4) + kRowsA * i) * lda_b);
+    }
+  };
+  auto direct_b = [&](int s, int slot, int i) __attribute__((always_inline)) {
+    const int k0 = ((s < s1 ? s : s1 - 1) - tail) * kStepK;
+    const uint32_t dst = lds0 + slot * kSlot + (wave * kLB + i) * 1024;
+    if constexpr (B_KC) {
+      to_lds(rb, dst, vb[i], static_cast<uint32_t>(k0 * 2));
+    } else {
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint16_t*>(B + k0 * g.ldb), 0, static_cast<int>((kStepK - 1) * ldb_b + rows_b * 2), 0x00020000);
+      to_lds(r, dst, vb[kRowsB == 2 ? i & 1 : 0], static_cast<uint32_t>(wave * (kStepK / 4) + kRowsB * i) * ldb_b);
+    }
+  };
+
+  // ---- the same through registers, masked
+  u32x4 ha[kLA], hb[kLB];
+  auto fetch_a = [&](int s) __attribute__((always_inline)) {
+    const int k0 = first_k(s), n = static_cast<int>(g.K - k0 < kStepK ? g.K - k0 : kStepK);
+#pragma unroll
+    for (int i = 0; i < kLA; ++i) {
+      const int e = t + 256 * i;
+      if constexpr (A_KC) {
+        const int r = e >> 3, c = e & 7;
+        ha[i] = ld16_part(A + (r < rows_a ? r : rows_a - 1) * g.lda + k0 + 8 * c, n - 8 * c);
+      } else {
+        const int k = e / kChA, c = e % kChA;
+        ha[i] = ld16_part(A + static_cast<int64_t>(k0 + k) * g.lda + 8 * c, k < n ? rows_a - 8 * c : 0);
+      }
+    }
+  };
+  auto fetch_b = [&](int s) __attribute__((always_inline)) {
+    const int k0 = first_k(s), n = static_cast<int>(g.K - k0 < kStepK ? g.K - k0 : kStepK);
+#pragma unroll
+    for (int i = 0; i < kLB; ++i) {
+      const int e = t + 256 * i;
+      if constexpr (B_KC) {
+        hb[i] = ld16_part(B + row_b(e >> 3) * g.ldb + k0 + 8 * (e & 7), n - 8 * (e & 7));
+      } else {
+        const int k = e / kChB, c = e % kChB;
+        hb[i] = ld16_part(B + static_cast<int64_t>(k0 + k) * g.ldb + 8 * c, k < n ? rows_b - 8 * c : 0);
+      }
+    }
+  };
+  auto put_a = [&](int slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kLA; ++i) {
+      const int e = t + 256 * i;
+      *reinterpret_cast<u32x4*>(smem + slot * kSlot + (A_KC ? swz(e >> 3, e & 7) : mn_at(e / kChA, e % kChA, BM * 2))) = ha[i];
+    }
+  };
+  auto put_b = [&](int slot) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kLB; ++i) {
+      const int e = t + 256 * i;
+      *reinterpret_cast<u32x4*>(smem + slot * kSlot + (B_KC ? swz(e >> 3, e & 7) : mn_at(e / kChB, e % kChB, BN * 2))) = hb[i];
+    }
+  };
+
+  // ---- fragments of 16 along K: KC, chunk 2 ks + h of the lane's row; else two
+  // transposing reads
+  const uint32_t sw = static_cast<uint32_t>((h ^ l32 ^ (l32 >> 3)) & 7) << 4;      // rows 32 apart: ^ 4 chunks
+  const uint32_t arow = static_cast<uint32_t>(wm * 32 * MB + l32) * kStepBytes + sw;
+  const uint32_t brow = static_cast<uint32_t>(wn * 32 * NB + l32) * kStepBytes + sw;
+  const int tq = lane >> 4, ts = lane & 15, tk = 8 * (tq >> 1) + (ts >> 2);
+  auto tr_at = [&](int c0, int b, int pitch) __attribute__((always_inline)) {
+    return static_cast<uint32_t>(mn_at(tk, (c0 >> 3) + 4 * b + 2 * (tq & 1) + ((ts & 3) >> 1), pitch) + 8 * (ts & 1));
+  };
+  u32x4 fa[2][MB], fb[2][NB];
+  auto frag_a = [&](int slot, int ks, int i, u32x4& v) __attribute__((always_inline)) {
+    const uint8_t* st = smem + slot * kSlot;
+    if constexpr (A_KC) v = *reinterpret_cast<const u32x4*>(st + (arow ^ static_cast<uint32_t>((2 * ks ^ 4 * (i & 1)) << 4)) + i * 32 * kStepBytes);
+    else v = frag_tr<BM * 2>(st, tr_at(wm * 32 * MB, i, BM * 2), ks);
+  };
+  auto frag_b = [&](int slot, int ks, int i, u32x4& v) __attribute__((always_inline)) {
+    const uint8_t* st = smem + slot * kSlot;
+    if constexpr (B_KC) v = *reinterpret_cast<const u32x4*>(st + (brow ^ static_cast<uint32_t>((2 * ks ^ 4 * (i & 1)) << 4)) + i * 32 * kStepBytes);
+    else v = frag_tr<BN * 2>(st, tr_at(wn * 32 * NB, i, BN * 2), ks);
+  };
+  // Part p of n of a slice's fragments, the columns' first: the next slice's
+  // first products need all of them and one of the rows'.
+  auto frag_part = [&](int sa, int sb, int ks, int p, int n) __attribute__((always_inline)) {
+    constexpr int kAll = MB + NB;
+#pragma unroll
+    for (int j = 0; j < kAll; ++j)
+      if (j >= kAll * p / n && j < kAll * (p + 1) / n) {
+        if (j < NB) frag_b(sb, ks, j, fb[ks & 1][j]);
+        else frag_a(sa, ks, j - NB, fa[ks & 1][j - NB]);
+      }
+  };
+
+  // Operand slots form a ring, A and B of a step side by side: A of step s + 2 and
+  // B of step s + 1 are on their way while step s is multiplied, one load for each
+  // row of products (the first of B as soon as the step before has met).
+  constexpr int kMeet = 3 * MB, kAhead = MB - 1;
+  static_assert(4 * MB == kLA + kLB, "a load for each row of products");
+  auto after = [](int slot, int n) __attribute__((always_inline)) { return slot + n >= kSlots ? slot + n - kSlots : slot + n; };
+  const bool more = s0 + 1 < s1;
+  if (s0 < s1) {
+    if (!FAST || (tail && s0 == 0)) {
+      fetch_a(s0);
+      put_a(0);
+      fetch_b(s0);
+      put_b(1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLA; ++i) direct_a(s0, 0, i);
+#pragma unroll
+      for (int i = 0; i < kLB; ++i) direct_b(s0, 1, i);
+    }
+    if (FAST && more) {
+#pragma unroll
+      for (int i = 0; i < kLA; ++i) direct_a(s0 + 1, 2, i);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) direct_b(s0 + 1, 3, i);
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLA + kAhead) : "memory");
+    } else {
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    }
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    frag_part(0, 1, 0, 0, 1);
+  }
+  f32x16 acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  // One step, slots sa and sa + 1: four slices of 16, a slice's products row by
+  // row, between them the next slice's fragments and the loads.  The block meets once, after the last slice's first row: the next step
+  // has landed, and every wave has its last fragments of this one.  The compiler
+  // keeps to this order.
+  auto step = [&](int s, int sa, auto next) __attribute__((always_inline)) {
+    constexpr bool MORE = decltype(next)::value;
+    const int sb = after(sa, 1), na = after(sa, 2), nb = after(sa, 3), aa = after(sa, 4);
+    if constexpr (MORE && !FAST) {
+      fetch_a(s + 1);
+      fetch_b(s + 1);
+    }
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      const int cur = ks & 1;
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        const int region = ks * MB + i, l = region + kAhead;
+        if constexpr (MORE && FAST) {
+          if (region > kMeet) direct_b(s + 2, sa, region - kMeet - 1);
+          else if (l < kLB) direct_b(s + 1, nb, l);
+          else direct_a(s + 2, aa, l - kLB);
+        }
+        if (ks < 3) frag_part(sa, sb, ks + 1, i, MB - 1);
+        else if (MORE && i > 0) frag_part(na, nb, 0, i - 1, MB - 1);
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[i][j] = mfma16<ET>(fa[cur][i], fb[cur][j], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (MORE && region == kMeet) {
+          if constexpr (FAST) {
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLA) : "memory");
+          } else {
+            put_a(na);
+            put_b(nb);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          }
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+        }
+      }
+    }
+  };
+  if (s0 < s1) {
+    int s = s0, sa = 0;
+    for (; s + 1 < s1; ++s) {
+      step(s, sa, std::true_type{});
+      sa = after(sa, 2);
+    }
+    step(s, sa, std::false_type{});
+  }
+
+  // ---- epilogue: a quarter of the slots for each wave's bands
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  constexpr int kBandCols = kGate ? 16 * NB : 32 * NB, kRegion = kSlots * kSlot / 4;
+  static_assert(32 * (kBandCols * (CT == AMP_F32 ? 4 : 2) + 32) <= kRegion, "a wave's band exceeds its part of the slots");
+  uint8_t* buf = smem + wave * kRegion;
+  const int64_t row0 = m0 + wm * 32 * MB, col0 = n0 + wn * kBandCols;
+  if constexpr (OUT == kOutC) {
+    void* C = g.splits > 1 ? static_cast<void*>(static_cast<float*>(g.C) + blockIdx.y * g.M * g.N) : g.C;
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+      band_out<CT, NB>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][nb][r]; }, C, g.ldc, row0 + 32 * i, col0, g.M, g.N, buf);
+  } else {
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const int64_t row = row0 + 32 * i;
+      if constexpr (OUT == kOutGate) {
+        if (g.gu) {
+          band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][nb][r]; }, g.gu, g.ldgu, row, col0, g.M, g.N, buf);
+          band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][NBH + nb][r]; },
+                            static_cast<uint16_t*>(g.gu) + g.N, g.ldgu, row, col0, g.M, g.N, buf);
+        }
+      } else {
+        float dy[NBH][16];
+        band_in<ET, NBH>(dy, g.dy, g.lddy, row, col0, g.M, g.N, buf);
+        if (g.C)
+          band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) {
+            const float x = acc[i][nb][r];
+            return x * gate(x).s * acc[i][NBH + nb][r];
+          }, g.C, g.ldc, row, col0, g.M, g.N, buf);
+        // dg = dy u s (1 + g (1 - s)), du = dy s g
+#pragma unroll
+        for (int nb = 0; nb < NBH; ++nb)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float x = acc[i][nb][r], u = acc[i][NBH + nb][r];
+            const Gate q = gate(x);
+            const float ds = dy[nb][r] * q.s;
+            acc[i][nb][r] = ds * u * (1.0f + x * q.om);
+            acc[i][NBH + nb][r] = ds * x;
+          }
+        band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][nb][r]; }, g.gu, g.ldgu, row, col0, g.M, g.N, buf);
+        band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][NBH + nb][r]; },
+                          static_cast<uint16_t*>(g.gu) + g.N, g.ldgu, row, col0, g.M, g.N, buf);
+      }
+      if constexpr (OUT == kOutGate) {
+        if (g.C)
+          band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) {
+            const float x = acc[i][nb][r];
+            return x * gate(x).s * acc[i][NBH + nb][r];
+          }, g.C, g.ldc, row, col0, g.M, g.N, buf);
+      }
+    }
+  }
+}
+
+// ---- which tile ------------------------------------------------------------
+
+// Operands that the direct loads take: 16-byte rows, windows below 2 GiB and,
+// where outputs are contiguous, a whole number of 16-byte pieces of them.
+inline bool direct_operand(const void* p, int64_t ld, bool kc, int64_t outs) {
+  return aligned(p, 16) && ld % 8 == 0 && ld < (int64_t(1) << 30) / (kc ? 256 : 64) && (kc || outs % 8 == 0);
+}
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tiles of 256 x 128, two to a CU, or of 128 x 128, three to a CU, which need about
+// a tenth more time for the same products; the fewer turns of the machine win.
+inline bool large_tiles(int64_t M, int64_t cols) {
+  const int64_t big = ceil_div(ceil_div(M, 256) * ceil_div(cols, 256), 256) * 40;
+  const int64_t small = ceil_div(ceil_div(M, 128) * ceil_div(cols, 128), 768) * 33;
+  return big <= small;
+}
+
+template <int ET, bool A_KC, bool B_KC, int OUT, int CT>
+hipError_t launch_product(const ProductArgs& g, hipStream_t s) {
+  constexpr int64_t kBoth = OUT == kOutC ? 1 : 2;
+  const bool fast = direct_operand(g.A, g.lda, A_KC, g.M) && direct_operand(g.B, g.ldb, B_KC, g.N);
+  const bool large = fast && g.splits == 1 && large_tiles(g.M, g.N * kBoth);
+  const int64_t edge = large ? 256 : 128;
+  const dim3 grid(static_cast<unsigned>(ceil_div(g.M, edge) * ceil_div(g.N * kBoth, edge)), static_cast<unsigned>(g.splits));
+  if (large) product_tiles<ET, A_KC, B_KC, OUT, CT, 4, 4, true><<<grid, 256, 0, s>>>(g);
+  else if (fast) product_tiles<ET, A_KC, B_KC, OUT, CT, 2, 2, true><<<grid, 256, 0, s>>>(g);
+  else product_tiles<ET, A_KC, B_KC, OUT, CT, 2, 2, false><<<grid, 256, 0, s>>>(g);
+  return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace amp
