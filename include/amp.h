@@ -533,7 +533,7 @@ int amp_requantize_blockwise(const amp_fp8_tiles* x, int64_t rows, int64_t cols,
  * aligned (pointers, strides % 8 == 0 and, in the backward pass, F % 4 == 0 and
  * K % 8 == 0) are the fast ones.  No output may overlap an input or another
  * output, but for dgu and gu as said below.  K and F are at most 2^26 and a
- * product may have at most 2^24 tiles of 128 x 128 (else AMP_EUNSUPPORTED). */
+ * product may have at most 2^22 tiles of 128 x 128 (else AMP_EUNSUPPORTED). */
 
 /* amp_gemm_swiglu -- the forward pass.  Up to 64 tokens (one token included)
  * the weights stream past them once.

@@ -72,10 +72,10 @@ int tiles_status(const amp_fp8_tiles* t, int64_t rows, int64_t cols) {
 }
 
 // Sizes of a gated feed-forward block: columns as above, and tiles whose
-// threads a launch can count.
+// threads one launch can count (both gradients' together).
 bool block_sizes(int64_t M, int64_t F, int64_t K) {
   if (K > kMostCols || F > kMostCols || M > (int64_t(1) << 31)) return false;
-  const int64_t m = (M + 127) / 128, f = (2 * F + 127) / 128, k = (K + 127) / 128, most = int64_t(1) << 24;
+  const int64_t m = (M + 127) / 128, f = (2 * F + 127) / 128, k = (K + 127) / 128, most = int64_t(1) << 22;
   return m * (f > k ? f : k) <= most && f * k <= most;
 }
 

@@ -43,6 +43,7 @@ struct ProductArgs {
   void* C; int64_t ldc;    // the product; with a gate y (may be NULL)
   void* gu; int64_t ldgu;  // kOutGate: [g | u] (may be NULL); kOutGrad: [dg | du]
   const void* dy; int64_t lddy;
+  int out32;               // kOutC: C is FP32
   int splits;              // parts of the summed dimension; > 1: C is FP32 [splits][M][N]
 };
 
@@ -55,7 +56,12 @@ __device__ __forceinline__ float from16(uint32_t c) {
   return ET == AMP_BF16 ? bf16_to_f32(c) : f16_to_f32(c);
 }
 template <int ET>
-__device__ __forceinline__ uint32_t to16(float x) { return ET == AMP_BF16 ? f32_to_bf16(x) : f32_to_f16(x); }
+__device__ __forceinline__ uint32_t to16(float x) {
+  if constexpr (ET == AMP_BF16) return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+  else return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+}
+template <int ET>
+__device__ __forceinline__ uint32_t to16x2(float x, float y) { return to16<ET>(x) | to16<ET>(y) << 16; }
 
 template <int ET>
 __device__ __forceinline__ f32x16 mfma16(u32x4 a, u32x4 b, f32x16 c) {
@@ -80,25 +86,28 @@ __device__ __forceinline__ u32x4 ld16_part(const uint16_t* p, int n) {
 // keep that order.
 __device__ __forceinline__ void wave_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// Epilogue of one wave: a band of 32 rows x 32 NBW columns leaves through this
-// wave's LDS region as whole 16-byte pieces of rows (the pitch, a row's bytes +
-// 32, puts the half-waves' writes on disjoint banks).  value(nb, r): the element
-// of column block nb in accumulator register r.
+// Epilogue of one wave.  The products are formed as B A^T, which leaves a lane
+// four neighbouring columns of one row in each four accumulator registers: lane l
+// holds row l % 32 and columns 8 q + 4 (l / 32) + e in register 4 q + e.  A band of
+// 32 rows x 32 NBW columns leaves through this wave's LDS region as whole 16-byte
+// pieces of rows; the pitch, a row's bytes + 16, spreads 16 rows over all banks.
+// value(nb, r): the element of column block nb in register r.
 template <int CT, int NBW, typename V>
 __device__ __forceinline__ void band_out(V&& value, void* C, int64_t ldc, int64_t row0, int64_t col0, int64_t M,
                                          int64_t N, uint8_t* buf) {
-  constexpr int kES = CT == AMP_F32 ? 4 : 2, kRow = NBW * 32 * kES, kPitch = kRow + 32;
+  constexpr int kES = CT == AMP_F32 ? 4 : 2, kRow = NBW * 32 * kES, kPitch = kRow + 16;
   constexpr int kLPR = kRow / 16, kRPP = 64 / kLPR, kEPL = 16 / kES;
-  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int lane = threadIdx.x & 63;
+  uint8_t* mine = buf + (lane & 31) * kPitch + (lane >> 5) * 4 * kES;
   wave_lds();
 #pragma unroll
   for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      uint8_t* p = buf + (8 * (r >> 2) + 4 * h + (r & 3)) * kPitch + (nb * 32 + l32) * kES;
-      const float x = value(nb, r);
-      if constexpr (CT == AMP_F32) *reinterpret_cast<float*>(p) = x;
-      else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(to16<CT>(x));
+    for (int q = 0; q < 4; ++q) {
+      const float x[4] = {value(nb, 4 * q), value(nb, 4 * q + 1), value(nb, 4 * q + 2), value(nb, 4 * q + 3)};
+      uint8_t* p = mine + (nb * 32 + 8 * q) * kES;
+      if constexpr (CT == AMP_F32) *reinterpret_cast<u32x4*>(p) = u32x4{fbits(x[0]), fbits(x[1]), fbits(x[2]), fbits(x[3])};
+      else *reinterpret_cast<u32x2*>(p) = u32x2{to16x2<CT>(x[0], x[1]), to16x2<CT>(x[2], x[3])};
     }
   wave_lds();
   const int64_t col = col0 + (lane % kLPR) * kEPL;
@@ -120,37 +129,43 @@ __device__ __forceinline__ void band_out(V&& value, void* C, int64_t ldc, int64_
   }
 }
 
-// The reverse way: a band of a 16-bit matrix into v[nb][r], zeros outside.
-template <int ET, int NBW>
-__device__ __forceinline__ void band_in(float (&v)[NBW][16], const void* X, int64_t ldx, int64_t row0, int64_t col0,
-                                        int64_t M, int64_t N, uint8_t* buf) {
-  constexpr int kRow = NBW * 64, kPitch = kRow + 32, kLPR = kRow / 16, kRPP = 64 / kLPR;
-  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-  const int64_t col = col0 + (lane % kLPR) * 8;
-  const int left = col < N ? static_cast<int>(N - col < 8 ? N - col : 8) : 0;
+// The reverse way for a band of a 16-bit matrix: its pieces on their way into
+// registers (zeros outside), then through LDS into the lanes' elements, four of
+// one row in v[nb][q].
+template <int NBW>
+struct Band {
+  static constexpr int kRow = NBW * 64, kPitch = kRow + 16, kLPR = kRow / 16, kRPP = 64 / kLPR;
   u32x4 w[32 / kRPP];
+  __device__ __forceinline__ void load(const void* X, int64_t ldx, int64_t row0, int64_t col0, int64_t M, int64_t N) {
+    const int lane = threadIdx.x & 63;
+    const int64_t col = col0 + (lane % kLPR) * 8;
+    const int left = col < N ? static_cast<int>(N - col < 8 ? N - col : 8) : 0;
 #pragma unroll
-  for (int ps = 0; ps < 32 / kRPP; ++ps) {
-    const int64_t row = row0 + ps * kRPP + lane / kLPR;
-    w[ps] = row < M ? ld16_part(static_cast<const uint16_t*>(X) + row * ldx + col, left) : u32x4{0u, 0u, 0u, 0u};
+    for (int ps = 0; ps < 32 / kRPP; ++ps) {
+      const int64_t row = row0 + ps * kRPP + lane / kLPR;
+      w[ps] = row < M ? ld16_part(static_cast<const uint16_t*>(X) + row * ldx + col, left) : u32x4{0u, 0u, 0u, 0u};
+    }
   }
-  wave_lds();
+  __device__ __forceinline__ void spread(u32x2 (&v)[NBW][4], uint8_t* buf) const {
+    const int lane = threadIdx.x & 63;
+    wave_lds();
 #pragma unroll
-  for (int ps = 0; ps < 32 / kRPP; ++ps)
-    *reinterpret_cast<u32x4*>(buf + (ps * kRPP + lane / kLPR) * kPitch + (lane % kLPR) * 16) = w[ps];
-  wave_lds();
+    for (int ps = 0; ps < 32 / kRPP; ++ps)
+      *reinterpret_cast<u32x4*>(buf + (ps * kRPP + lane / kLPR) * kPitch + (lane % kLPR) * 16) = w[ps];
+    wave_lds();
 #pragma unroll
-  for (int nb = 0; nb < NBW; ++nb)
+    for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-      v[nb][r] = from16<ET>(*reinterpret_cast<const uint16_t*>(buf + (8 * (r >> 2) + 4 * h + (r & 3)) * kPitch +
-                                                               (nb * 32 + l32) * 2));
-}
+      for (int q = 0; q < 4; ++q)
+        v[nb][q] = *reinterpret_cast<const u32x2*>(buf + (lane & 31) * kPitch + (nb * 32 + 8 * q + 4 * (lane >> 5)) * 2);
+  }
+};
 
 // A direct-to-LDS load of 16 bytes a lane (64 lanes fill 1 KB from dst on) that
 // the compiler does not track: the kernel waits for it by count.
 __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t dst, uint32_t voff, uint32_t soff) {
-  asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc), "s"(soff), "{m0}"(dst));
+  asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soff)),
+               "{m0}"(__builtin_amdgcn_readfirstlane(dst)));
 }
 
 constexpr int kStepK = 64, kStepBytes = 2 * kStepK;      // elements and bytes of a row of a step
@@ -160,20 +175,22 @@ constexpr int kSlots = 5;
 // The same in an output-contiguous stage, rows of `pitch` bytes along K.
 __device__ __forceinline__ int mn_at(int k, int c, int pitch) { return k * pitch + ((c ^ (4 * (k & 3))) << 4); }
 
-template <int ET, bool A_KC, bool B_KC, int OUT, int CT, int MB, int NB, bool FAST>
-__global__ __launch_bounds__(256, MB * NB > 8 ? 1 : 2) void product_tiles(ProductArgs g) {
+constexpr int lds_bytes(int MB, int NB) { return kSlots * 64 * (MB > NB ? MB : NB) * kStepBytes; }
+
+// Block `block` of the product's tiles, part z of the summed dimension.
+template <int ET, bool A_KC, bool B_KC, int OUT, int MB, int NB, bool FAST>
+__device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, uint32_t z, uint8_t* smem) {
   constexpr bool kGate = OUT != kOutC;
   static_assert(!kGate || (A_KC && B_KC), "the projections' operands are K-contiguous");
   constexpr int BM = 64 * MB, BN = 64 * NB, BNO = kGate ? BN / 2 : BN, NBH = NB / 2;
-  constexpr int kSlot = (MB > NB ? BM : BN) * kStepBytes;      // one operand of a step
+  constexpr int kSlot = lds_bytes(MB, NB) / kSlots;            // one operand of a step
   constexpr int kLA = 2 * MB, kLB = 2 * NB;                    // direct loads of a wave and operand
-  __shared__ __align__(16) uint8_t smem[kSlots * kSlot];
 
   // Blocks of one XCD (every eighth) take one contiguous run of tiles, eight
   // tile rows at a time, so that its L2 holds the operands' shared parts.
   const uint32_t nbm = static_cast<uint32_t>((g.M + BM - 1) / BM), nbn = static_cast<uint32_t>((g.N + BNO - 1) / BNO);
-  const uint32_t total = nbm * nbn, xcd = blockIdx.x % 8, most = total % 8;
-  const uint32_t tile = xcd * (total / 8) + (xcd < most ? xcd : most) + blockIdx.x / 8;
+  const uint32_t total = nbm * nbn, xcd = block % 8, most = total % 8;
+  const uint32_t tile = xcd * (total / 8) + (xcd < most ? xcd : most) + block / 8;
   constexpr uint32_t kGroup = 8;
   const uint32_t first_m = tile / (kGroup * nbn) * kGroup;
   const uint32_t gsz = nbm - first_m < kGroup ? nbm - first_m : kGroup;
@@ -190,9 +207,9 @@ __global__ __launch_bounds__(256, MB * NB > 8 ? 1 : 2) void product_tiles(Produc
   const uint32_t lda_b = static_cast<uint32_t>(g.lda * 2), ldb_b = static_cast<uint32_t>(g.ldb * 2);
 
   // The steps of this block: whole ones, what is left over being the first.
-  const int whole = static_cast<int>(g.K / kStepK), tail = g.K % kStepK != 0, steps = whole + tail;
-  const int s0 = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<int64_t>(steps) * blockIdx.y / g.splits));
-  const int s1 = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<int64_t>(steps) * (blockIdx.y + 1) / g.splits));
+  const int whole = __builtin_amdgcn_readfirstlane(static_cast<int>(g.K / kStepK)), tail = __builtin_amdgcn_readfirstlane(g.K % kStepK != 0), steps = whole + tail;
+  const int s0 = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<int64_t>(steps) * z / g.splits));
+  const int s1 = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<int64_t>(steps) * (z + 1) / g.splits));
   auto first_k = [&](int s) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane((tail ? (s == 0 ? whole : s - 1) : s) * kStepK); };
 
   // LDS row r of the B stage: with a gate, the feature and the projection that
@@ -366,6 +383,10 @@ __global__ __launch_bounds__(256, MB * NB > 8 ? 1 : 2) void product_tiles(Produc
     } else {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     }
+    if (!FAST && more) {
+      fetch_a(s0 + 1);
+      fetch_b(s0 + 1);
+    }
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     frag_part(0, 1, 0, 0, 1);
@@ -386,8 +407,12 @@ __global__ __launch_bounds__(256, MB * NB > 8 ? 1 : 2) void product_tiles(Produc
     constexpr bool MORE = decltype(next)::value;
     const int sb = after(sa, 1), na = after(sa, 2), nb = after(sa, 3), aa = after(sa, 4);
     if constexpr (MORE && !FAST) {
-      fetch_a(s + 1);
-      fetch_b(s + 1);
+      put_a(na);
+      put_b(nb);
+      if (s + 2 < s1) {
+        fetch_a(s + 2);
+        fetch_b(s + 2);
+      }
     }
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
@@ -403,14 +428,12 @@ __global__ __launch_bounds__(256, MB * NB > 8 ? 1 : 2) void product_tiles(Produc
         if (ks < 3) frag_part(sa, sb, ks + 1, i, MB - 1);
         else if (MORE && i > 0) frag_part(na, nb, 0, i - 1, MB - 1);
 #pragma unroll
-        for (int j = 0; j < NB; ++j) acc[i][j] = mfma16<ET>(fa[cur][i], fb[cur][j], acc[i][j]);
+        for (int j = 0; j < NB; ++j) acc[i][j] = mfma16<ET>(fb[cur][j], fa[cur][i], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
         if (MORE && region == kMeet) {
           if constexpr (FAST) {
             asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLA) : "memory");
           } else {
-            put_a(na);
-            put_b(nb);
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
           }
           __builtin_amdgcn_s_barrier();
@@ -433,55 +456,77 @@ __global__ __launch_bounds__(256, MB * NB > 8 ? 1 : 2) void product_tiles(Produc
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   constexpr int kBandCols = kGate ? 16 * NB : 32 * NB, kRegion = kSlots * kSlot / 4;
-  static_assert(32 * (kBandCols * (CT == AMP_F32 ? 4 : 2) + 32) <= kRegion, "a wave's band exceeds its part of the slots");
+  static_assert(32 * (kBandCols * (kGate ? 2 : 4) + 16) <= kRegion, "a wave's band exceeds its part of the slots");
   uint8_t* buf = smem + wave * kRegion;
   const int64_t row0 = m0 + wm * 32 * MB, col0 = n0 + wn * kBandCols;
   if constexpr (OUT == kOutC) {
-    void* C = g.splits > 1 ? static_cast<void*>(static_cast<float*>(g.C) + blockIdx.y * g.M * g.N) : g.C;
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-      band_out<CT, NB>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][nb][r]; }, C, g.ldc, row0 + 32 * i, col0, g.M, g.N, buf);
+    for (int i = 0; i < MB; ++i) {
+      auto value = [&](int nb, int r) __attribute__((always_inline)) { return acc[i][nb][r]; };
+      if (g.out32) band_out<AMP_F32, NB>(value, static_cast<float*>(g.C) + z * g.M * g.N, g.ldc, row0 + 32 * i, col0, g.M, g.N, buf);
+      else band_out<ET, NB>(value, g.C, g.ldc, row0 + 32 * i, col0, g.M, g.N, buf);
+    }
   } else {
+    void* const gu2 = static_cast<uint16_t*>(g.gu) + g.N;       // the up half of [g | u]
+    Band<NBH> next;
+    if constexpr (OUT == kOutGrad) next.load(g.dy, g.lddy, row0, col0, g.M, g.N);
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
       const int64_t row = row0 + 32 * i;
-      if constexpr (OUT == kOutGate) {
-        if (g.gu) {
-          band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][nb][r]; }, g.gu, g.ldgu, row, col0, g.M, g.N, buf);
-          band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][NBH + nb][r]; },
-                            static_cast<uint16_t*>(g.gu) + g.N, g.ldgu, row, col0, g.M, g.N, buf);
-        }
-      } else {
-        float dy[NBH][16];
-        band_in<ET, NBH>(dy, g.dy, g.lddy, row, col0, g.M, g.N, buf);
-        if (g.C)
-          band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) {
-            const float x = acc[i][nb][r];
-            return x * gate(x).s * acc[i][NBH + nb][r];
-          }, g.C, g.ldc, row, col0, g.M, g.N, buf);
-        // dg = dy u s (1 + g (1 - s)), du = dy s g
+      u32x2 dy[NBH][4];
+      if constexpr (OUT == kOutGrad) {
+        next.spread(dy, buf);
+        if (i + 1 < MB) next.load(g.dy, g.lddy, row + 32, col0, g.M, g.N);
+      }
+      if (OUT == kOutGate && g.gu) {
+        band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][nb][r]; }, g.gu, g.ldgu, row, col0, g.M, g.N, buf);
+        band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][NBH + nb][r]; }, gu2, g.ldgu, row, col0, g.M, g.N, buf);
+      }
+      // y = g s u; with dy, g and u make place for dg = dy s u (1 + g (1 - s)) and du = dy s g
+      float y[NBH][16];
 #pragma unroll
-        for (int nb = 0; nb < NBH; ++nb)
+      for (int nb = 0; nb < NBH; ++nb)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const float x = acc[i][nb][r], u = acc[i][NBH + nb][r];
-            const Gate q = gate(x);
-            const float ds = dy[nb][r] * q.s;
+        for (int r = 0; r < 16; ++r) {
+          const float x = acc[i][nb][r], u = acc[i][NBH + nb][r];
+          const Gate q = gate(x);
+          y[nb][r] = x * q.s * u;
+          if constexpr (OUT == kOutGrad) {
+            const float ds = from16<ET>(dy[nb][r >> 2][(r & 3) >> 1] >> (16 * (r & 1)) & 0xffffu) * q.s;
             acc[i][nb][r] = ds * u * (1.0f + x * q.om);
             acc[i][NBH + nb][r] = ds * x;
           }
+        }
+      if (g.C) band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return y[nb][r]; }, g.C, g.ldc, row, col0, g.M, g.N, buf);
+      if constexpr (OUT == kOutGrad) {
         band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][nb][r]; }, g.gu, g.ldgu, row, col0, g.M, g.N, buf);
-        band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][NBH + nb][r]; },
-                          static_cast<uint16_t*>(g.gu) + g.N, g.ldgu, row, col0, g.M, g.N, buf);
-      }
-      if constexpr (OUT == kOutGate) {
-        if (g.C)
-          band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) {
-            const float x = acc[i][nb][r];
-            return x * gate(x).s * acc[i][NBH + nb][r];
-          }, g.C, g.ldc, row, col0, g.M, g.N, buf);
+        band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][NBH + nb][r]; }, gu2, g.ldgu, row, col0, g.M, g.N, buf);
       }
     }
+  }
+}
+
+// Both projections with their gate.
+template <int ET, int OUT, int MB, int NB, bool FAST>
+__global__ __launch_bounds__(256, MB * NB > 8 ? 1 : 2) void gate_tiles(ProductArgs g) {
+  __shared__ __align__(16) uint8_t smem[lds_bytes(MB, NB)];
+  product<ET, true, true, OUT, MB, NB, FAST>(g, blockIdx.x, 0, smem);
+}
+
+// The two gradient products in one launch, that of the longer sums first: the
+// blocks of one fill what the other leaves of the machine.  nx: blocks of dx.
+template <int ET, int MB, int NB, bool FAST>
+__global__ __launch_bounds__(256, MB * NB > 8 ? 1 : 2) void gradient_tiles(ProductArgs gx, ProductArgs gw, uint32_t nx, uint32_t nw, int dx_first) {
+  __shared__ __align__(16) uint8_t smem[lds_bytes(MB, NB)];
+  const uint32_t before = dx_first ? nx : nw;
+  const bool first = blockIdx.x < before, is_dx = first == (dx_first != 0);
+  const uint32_t b = first ? blockIdx.x : blockIdx.x - before;
+  if (is_dx) {
+    const uint32_t tiles = nx / gx.splits;
+    product<ET, true, false, kOutC, MB, NB, FAST>(gx, b % tiles, b / tiles, smem);
+  } else {
+    const uint32_t tiles = nw / gw.splits;
+    product<ET, false, false, kOutC, MB, NB, FAST>(gw, b % tiles, b / tiles, smem);
   }
 }
 
@@ -494,25 +539,22 @@ inline bool direct_operand(const void* p, int64_t ld, bool kc, int64_t outs) {
 }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t tiles_of(int64_t M, int64_t cols, int64_t edge) { return ceil_div(M, edge) * ceil_div(cols, edge); }
 
-// Tiles of 256 x 128, two to a CU, or of 128 x 128, three to a CU, which need about
-// a tenth more time for the same products; the fewer turns of the machine win.
-inline bool large_tiles(int64_t M, int64_t cols) {
-  const int64_t big = ceil_div(ceil_div(M, 256) * ceil_div(cols, 256), 256) * 40;
-  const int64_t small = ceil_div(ceil_div(M, 128) * ceil_div(cols, 128), 768) * 33;
-  return big <= small;
-}
+// Microseconds of a step of 64 along the summed dimension: a tile of 256 x 256
+// has a CU for itself, tiles of 128 x 128 run two to a CU; with fewer than one a
+// CU a step of theirs is bound by latency.
+constexpr double kStepLarge = 1.5, kStepSmall = 1.05, kStepAlone = 0.55;
 
-template <int ET, bool A_KC, bool B_KC, int OUT, int CT>
-hipError_t launch_product(const ProductArgs& g, hipStream_t s) {
-  constexpr int64_t kBoth = OUT == kOutC ? 1 : 2;
-  const bool fast = direct_operand(g.A, g.lda, A_KC, g.M) && direct_operand(g.B, g.ldb, B_KC, g.N);
-  const bool large = fast && g.splits == 1 && large_tiles(g.M, g.N * kBoth);
-  const int64_t edge = large ? 256 : 128;
-  const dim3 grid(static_cast<unsigned>(ceil_div(g.M, edge) * ceil_div(g.N * kBoth, edge)), static_cast<unsigned>(g.splits));
-  if (large) product_tiles<ET, A_KC, B_KC, OUT, CT, 4, 4, true><<<grid, 256, 0, s>>>(g);
-  else if (fast) product_tiles<ET, A_KC, B_KC, OUT, CT, 2, 2, true><<<grid, 256, 0, s>>>(g);
-  else product_tiles<ET, A_KC, B_KC, OUT, CT, 2, 2, false><<<grid, 256, 0, s>>>(g);
+template <int ET, int OUT>
+hipError_t launch_gate(const ProductArgs& g, hipStream_t s) {
+  const bool fast = direct_operand(g.A, g.lda, true, g.M) && direct_operand(g.B, g.ldb, true, g.N);
+  const int64_t big = tiles_of(g.M, 2 * g.N, 256), small = tiles_of(g.M, 2 * g.N, 128);
+  const bool large = fast && kStepLarge * ceil_div(big, 256) <= (small <= 256 ? kStepAlone : kStepSmall * ceil_div(small, 512));
+  const dim3 grid(static_cast<unsigned>(large ? big : small));
+  if (large) gate_tiles<ET, OUT, 4, 4, true><<<grid, 256, 0, s>>>(g);
+  else if (fast) gate_tiles<ET, OUT, 2, 2, true><<<grid, 256, 0, s>>>(g);
+  else gate_tiles<ET, OUT, 2, 2, false><<<grid, 256, 0, s>>>(g);
   return hipGetLastError();
 }
 

@@ -5,7 +5,7 @@
 //
 // The activation's gradient comes from the kept projections (the element-wise
 // pass of amp_swiglu_backward) or out of the epilogue of the product that forms
-// them again.  Both gradient products are product_tiles (ffn.hpp) on it.
+// them again.  The two gradient products on it are one launch.
 #include "ffn.hpp"
 
 namespace amp {
@@ -25,30 +25,63 @@ __global__ __launch_bounds__(256) void join_parts(const float* __restrict__ part
   }
 }
 
-// Parts of the summed dimension where the output has too few tiles for the
-// machine: each at least eight steps long, their sums within the work area.
-inline int parts_of(int64_t M, int64_t N, int64_t K, bool work) {
-  const int64_t tiles = ceil_div(M, 128) * ceil_div(N, 128);
-  if (!work || tiles >= 256) return 1;
-  int64_t n = 512 / tiles;
-  if (n > K / 512) n = K / 512;
-  if (n > AMP_GEMM_SWIGLU_WORK / (M * N)) n = AMP_GEMM_SWIGLU_WORK / (M * N);
+// Parts of a product whose tiles are too few for the machine: about `steps`
+// steps each where that at least halves them, their sums within `room` numbers
+// of the work area.
+inline int parts_of(const ProductArgs& g, int64_t steps, int64_t room) {
+  const int64_t all = ceil_div(g.K, kStepK);
+  int64_t n = all >= 2 * steps ? all / steps : 1;
+  if (g.M * g.N > 0 && n > room / (g.M * g.N)) n = room / (g.M * g.N);
   return n > 1 ? static_cast<int>(n) : 1;
 }
 
-template <int ET, bool A_KC, int CT>
-hipError_t gradient(ProductArgs g, float* work, hipStream_t s) {
-  if (g.M == 0 || g.N == 0) return hipSuccess;
-  g.splits = parts_of(g.M, g.N, g.K, work != nullptr);
-  if (g.splits == 1) return launch_product<ET, A_KC, false, kOutC, CT>(g, s);
-  void* const C = g.C;
-  const int64_t ldc = g.ldc;
-  g.C = work;
-  g.ldc = g.N;
-  if (hipError_t e = launch_product<ET, A_KC, false, kOutC, AMP_F32>(g, s)) return e;
+template <int ET>
+hipError_t join(const ProductArgs& g, const float* part, void* C, int64_t ldc, int ct, hipStream_t s) {
   const int64_t blocks = ceil_div(g.M * g.N, 256);
-  join_parts<CT><<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(work, g.splits, g.M, g.N, C, ldc);
+  const unsigned grid = static_cast<unsigned>(blocks < 4096 ? blocks : 4096);
+  if (ct == AMP_F32) join_parts<AMP_F32><<<grid, 256, 0, s>>>(part, g.splits, g.M, g.N, C, ldc);
+  else join_parts<ET><<<grid, 256, 0, s>>>(part, g.splits, g.M, g.N, C, ldc);
   return hipGetLastError();
+}
+
+// dx = dgu w and dw = dgu^T x (either may be absent, M * N == 0).
+template <int ET>
+hipError_t gradients(ProductArgs gx, ProductArgs gw, int ct, float* work, hipStream_t s) {
+  const bool dx = gx.C && gx.M > 0 && gx.N > 0, dw = gw.C && gw.M > 0 && gw.N > 0;
+  if (!dx && !dw) return hipSuccess;
+  if (!dx) gx.M = gx.N = 0;
+  if (!dw) gw.M = gw.N = 0;
+  const bool fast = (!dx || (direct_operand(gx.A, gx.lda, true, gx.M) && direct_operand(gx.B, gx.ldb, false, gx.N))) &&
+                    (!dw || (direct_operand(gw.A, gw.lda, false, gw.M) && direct_operand(gw.B, gw.ldb, false, gw.N)));
+  const int64_t sx = ceil_div(gx.K, kStepK), sw = ceil_div(gw.K, kStepK);
+  const int64_t tx = tiles_of(gx.M, gx.N, 128), tw = tiles_of(gw.M, gw.N, 128);
+  const int64_t bx = tiles_of(gx.M, gx.N, 256), bw = tiles_of(gw.M, gw.N, 256);
+  // 128 x 128 tiles, in parts that share the work out to two blocks a CU
+  const int64_t even = (tx * sx + tw * sw) / 512;
+  const int64_t each = even < 8 ? 8 : even;
+  const int64_t room = work ? AMP_GEMM_SWIGLU_WORK : 0;
+  gx.splits = dx ? parts_of(gx, each, room) : 1;
+  gw.splits = dw ? parts_of(gw, each, room - (gx.splits > 1 ? gx.splits * gx.M * gx.N : 0)) : 1;
+  auto most = [](double a, double b) { return a > b ? a : b; };
+  const double longest = most(dx ? static_cast<double>(sx) / gx.splits : 0, dw ? static_cast<double>(sw) / gw.splits : 0);
+  const double small = most(kStepSmall * static_cast<double>(tx * sx + tw * sw) / 512, kStepAlone * longest);
+  const double large = kStepLarge * most(static_cast<double>(bx * sx + bw * sw) / 256, most(dx ? sx : 0, dw ? sw : 0));
+  const bool wide = fast && large <= small;
+  if (wide) gx.splits = gw.splits = 1;
+  const ProductArgs x0 = gx, w0 = gw;      // where the results go
+  gx.out32 = gx.splits > 1;
+  if (gx.splits > 1) { gx.C = work; gx.ldc = gx.N; }
+  gw.out32 = gw.splits > 1 || ct == AMP_F32;
+  if (gw.splits > 1) { gw.C = work + (gx.splits > 1 ? gx.splits * gx.M * gx.N : 0); gw.ldc = gw.N; }
+  const uint32_t nx = static_cast<uint32_t>((wide ? bx : tx) * gx.splits), nw = static_cast<uint32_t>((wide ? bw : tw) * gw.splits);
+  const int dx_first = sx * gw.splits >= sw * gx.splits;
+  if (wide) gradient_tiles<ET, 4, 4, true><<<nx + nw, 256, 0, s>>>(gx, gw, nx, nw, dx_first);
+  else if (fast) gradient_tiles<ET, 2, 2, true><<<nx + nw, 256, 0, s>>>(gx, gw, nx, nw, dx_first);
+  else gradient_tiles<ET, 2, 2, false><<<nx + nw, 256, 0, s>>>(gx, gw, nx, nw, dx_first);
+  if (hipError_t e = hipGetLastError()) return e;
+  if (gx.splits > 1)
+    if (hipError_t e = join<ET>(gx, static_cast<const float*>(gx.C), x0.C, x0.ldc, ET, s)) return e;
+  return gw.splits > 1 ? join<ET>(gw, static_cast<const float*>(gw.C), w0.C, w0.ldc, ct, s) : hipSuccess;
 }
 
 template <int ET>
@@ -64,21 +97,14 @@ hipError_t launch_backward(int64_t M, int64_t F, int64_t K, const void* dy, int6
       ProductArgs g{};
       g.A = x; g.lda = ldx; g.B = w; g.ldb = ldw; g.M = M; g.N = F; g.K = K;
       g.C = y; g.ldc = ldy; g.gu = dgu; g.ldgu = lddgu; g.dy = dy; g.lddy = lddy; g.splits = 1;
-      e = launch_product<ET, true, true, kOutGrad, ET>(g, s);
+      e = launch_gate<ET, kOutGrad>(g, s);
     }
     if (e) return e;
   }
-  if (dx) {
-    ProductArgs g{};
-    g.A = dgu; g.lda = lddgu; g.B = w; g.ldb = ldw; g.M = M; g.N = K; g.K = 2 * F; g.C = dx; g.ldc = lddx;
-    if (hipError_t e = gradient<ET, true, ET>(g, work, s)) return e;
-  }
-  if (dw) {
-    ProductArgs g{};
-    g.A = dgu; g.lda = lddgu; g.B = x; g.ldb = ldx; g.M = 2 * F; g.N = K; g.K = M; g.C = dw; g.ldc = lddw;
-    return dwt == AMP_F32 ? gradient<ET, false, AMP_F32>(g, work, s) : gradient<ET, false, ET>(g, work, s);
-  }
-  return hipSuccess;
+  ProductArgs gx{}, gw{};
+  gx.A = dgu; gx.lda = lddgu; gx.B = w; gx.ldb = ldw; gx.M = M; gx.N = K; gx.K = 2 * F; gx.C = dx; gx.ldc = lddx;
+  gw.A = dgu; gw.lda = lddgu; gw.B = x; gw.ldb = ldx; gw.M = 2 * F; gw.N = K; gw.K = M; gw.C = dw; gw.ldc = lddw;
+  return gradients<ET>(gx, gw, dwt, work, s);
 }
 
 }  // namespace

@@ -3,17 +3,15 @@
 //
 //   [g | u] = x [Wg; Wu]^T,  y = g sigmoid(g) u
 //
-// Many tokens: product_tiles (ffn.hpp).  Few tokens: the weights stream past
+// Many tokens: gate_tiles (ffn.hpp).  Few tokens: the weights stream past
 // them once, which is all the time there is.
 #include "ffn.hpp"
 
 namespace amp {
 namespace {
 
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
 template <int ET>
-__device__ __forceinline__ f32x4_t mfma16x16(u32x4 a, u32x4 b, f32x4_t c) {
+__device__ __forceinline__ f32x4 mfma16x16(u32x4 a, u32x4 b, f32x4 c) {
   if constexpr (ET == AMP_F16)
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
   else
@@ -21,10 +19,10 @@ __device__ __forceinline__ f32x4_t mfma16x16(u32x4 a, u32x4 b, f32x4_t c) {
 }
 
 // Up to 16 MT tokens.  A block owns 16 FT features; its NW waves share the
-// summed dimension, 128 elements a wave and turn, straight from memory into
+// summed dimension, 32 KC elements a wave and turn, straight from memory into
 // the 16x16x32 instruction's operands (weights as rows, tokens as columns: lane
 // l holds row l % 16 and elements 8 (l / 16) .. + 7), and join their sums in LDS.
-template <int ET, int MT, int FT, int NW>
+template <int ET, int MT, int FT, int NW, int KC>
 __global__ __launch_bounds__(NW * 64) void gate_few(ProductArgs g) {
   __shared__ float part[NW][2 * FT][4][64];
   const int lane = threadIdx.x & 63, wave = wave_id(), q = lane >> 4, i16 = lane & 15;
@@ -43,23 +41,23 @@ __global__ __launch_bounds__(NW * 64) void gate_few(ProductArgs g) {
     const int64_t m = 16 * i + i16;
     px[i] = x + (m < g.M ? m : g.M - 1) * g.lda + 8 * q;
   }
-  f32x4_t acc[2 * FT][MT];
+  f32x4 acc[2 * FT][MT];
 #pragma unroll
   for (int i = 0; i < 2 * FT; ++i)
 #pragma unroll
-    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  int64_t k = wave * 128;
-  for (; k + 128 <= g.K; k += NW * 128) {
-    u32x4 a[2 * FT][4], b[MT][4];
+    for (int j = 0; j < MT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  int64_t k = wave * (32 * KC);
+  for (; k + 32 * KC <= g.K; k += NW * (32 * KC)) {
+    u32x4 a[2 * FT][KC], b[MT][KC];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < KC; ++c) {
 #pragma unroll
       for (int i = 0; i < 2 * FT; ++i) a[i][c] = ld16u(pw[i] + k + 32 * c);
 #pragma unroll
       for (int j = 0; j < MT; ++j) b[j][c] = ld16u(px[j] + k + 32 * c);
     }
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < KC; ++c)
 #pragma unroll
       for (int i = 0; i < 2 * FT; ++i)
 #pragma unroll
@@ -108,18 +106,19 @@ __global__ __launch_bounds__(NW * 64) void gate_few(ProductArgs g) {
   }
 }
 
+template <int ET, int MT, int FT, int NW, int KC>
+hipError_t launch_few(const ProductArgs& g, hipStream_t s) {
+  gate_few<ET, MT, FT, NW, KC><<<static_cast<unsigned>(ceil_div(g.N, 16 * FT)), NW * 64, 0, s>>>(g);
+  return hipGetLastError();
+}
+
 template <int ET>
 hipError_t launch_forward(const ProductArgs& g, hipStream_t s) {
-  if (g.M <= 16) {
-    gate_few<ET, 1, 1, 8><<<static_cast<unsigned>(ceil_div(g.N, 16)), 512, 0, s>>>(g);
-  } else if (g.M <= 32) {
-    gate_few<ET, 2, 1, 8><<<static_cast<unsigned>(ceil_div(g.N, 16)), 512, 0, s>>>(g);
-  } else if (g.M <= 64) {
-    gate_few<ET, 4, 1, 8><<<static_cast<unsigned>(ceil_div(g.N, 16)), 512, 0, s>>>(g);
-  } else {
-    return launch_product<ET, true, true, kOutGate, ET>(g, s);
-  }
-  return hipGetLastError();
+  if (g.M <= 16) return launch_few<ET, 1, 1, 8, 4>(g, s);
+  if (g.M <= 32) return launch_few<ET, 2, 2, 4, 2>(g, s);
+  if (g.M <= 48) return launch_few<ET, 3, 2, 4, 2>(g, s);
+  if (g.M <= 64) return launch_few<ET, 4, 2, 4, 2>(g, s);
+  return launch_gate<ET, kOutGate>(g, s);
 }
 
 }  // namespace
