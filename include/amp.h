@@ -535,8 +535,8 @@ int amp_requantize_blockwise(const amp_fp8_tiles* x, int64_t rows, int64_t cols,
  * output, but for dgu and gu as said below.  K and F are at most 2^26 and a
  * product may have at most 2^22 tiles of 128 x 128 (else AMP_EUNSUPPORTED). */
 
-/* amp_gemm_swiglu -- the forward pass.  Up to 64 tokens (one token included)
- * the weights stream past them once.
+/* amp_gemm_swiglu -- the forward pass.  Of few tokens (one token included) the
+ * weights stream past them once.
  * x: [M, K], stride ldx >= K.  w: [2F, K], stride ldw >= K.
  * y: [M, F], stride ldy >= F; NULL for none.
  * gu: [g | u] rounded, [M, 2F], stride ldgu >= 2F, for the backward pass; NULL

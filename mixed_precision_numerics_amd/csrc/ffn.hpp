@@ -170,20 +170,20 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t dst
 
 constexpr int kStepK = 64, kStepBytes = 2 * kStepK;      // elements and bytes of a row of a step
 static_assert(kStepBytes == kRowBytes, "the slots' layout");
-constexpr int kSlots = 5;
 
 // The same in an output-contiguous stage, rows of `pitch` bytes along K.
 __device__ __forceinline__ int mn_at(int k, int c, int pitch) { return k * pitch + ((c ^ (4 * (k & 3))) << 4); }
 
-constexpr int lds_bytes(int MB, int NB) { return kSlots * 64 * (MB > NB ? MB : NB) * kStepBytes; }
+// LDS of a ring that reaches D steps ahead: slots of one operand's step.
+constexpr int lds_bytes(int MB, int NB, int D) { return (2 * D + 1) * 64 * (MB > NB ? MB : NB) * kStepBytes; }
 
 // Block `block` of the product's tiles, part z of the summed dimension.
-template <int ET, bool A_KC, bool B_KC, int OUT, int MB, int NB, bool FAST>
+template <int ET, bool A_KC, bool B_KC, int OUT, int MB, int NB, int D, bool FAST>
 __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, uint32_t z, uint8_t* smem) {
   constexpr bool kGate = OUT != kOutC;
   static_assert(!kGate || (A_KC && B_KC), "the projections' operands are K-contiguous");
   constexpr int BM = 64 * MB, BN = 64 * NB, BNO = kGate ? BN / 2 : BN, NBH = NB / 2;
-  constexpr int kSlot = lds_bytes(MB, NB) / kSlots;            // one operand of a step
+  constexpr int kSlots = 2 * D + 1, kSlot = lds_bytes(MB, NB, D) / kSlots;      // a slot holds one operand of a step
   constexpr int kLA = 2 * MB, kLB = 2 * NB;                    // direct loads of a wave and operand
 
   // Blocks of one XCD (every eighth) take one contiguous run of tiles, eight
@@ -355,10 +355,11 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
       }
   };
 
-  // Operand slots form a ring, A and B of a step side by side: A of step s + 2 and
-  // B of step s + 1 are on their way while step s is multiplied, one load for each
-  // row of products (the first of B as soon as the step before has met).
-  constexpr int kMeet = 3 * MB, kAhead = MB - 1;
+  // Operand slots form a ring, A and B of a step side by side: while step s is
+  // multiplied the operands up to B of step s + D - 1 and A of step s + D are on
+  // their way, one load for each row of products (the first of B as soon as the step
+  // before has met).  Loads land in order, so they are waited for by count.
+  constexpr int kMeet = 3 * MB, kAhead = MB - 1, kFlying = (D - 1) * kLA + (D - 2) * kLB;
   static_assert(4 * MB == kLA + kLB, "a load for each row of products");
   auto after = [](int slot, int n) __attribute__((always_inline)) { return slot + n >= kSlots ? slot + n - kSlots : slot + n; };
   const bool more = s0 + 1 < s1;
@@ -376,10 +377,13 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
     }
     if (FAST && more) {
 #pragma unroll
-      for (int i = 0; i < kLA; ++i) direct_a(s0 + 1, 2, i);
+      for (int d = 1; d < D; ++d) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) direct_b(s0 + 1, 3, i);
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLA + kAhead) : "memory");
+        for (int i = 0; i < kLA; ++i) direct_a(s0 + d, 2 * d, i);
+#pragma unroll
+        for (int i = 0; i < (d + 1 < D ? kLB : kAhead); ++i) direct_b(s0 + d, 2 * d + 1, i);
+      }
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kFlying + kAhead) : "memory");
     } else {
       asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     }
@@ -405,7 +409,7 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
   // keeps to this order.
   auto step = [&](int s, int sa, auto next) __attribute__((always_inline)) {
     constexpr bool MORE = decltype(next)::value;
-    const int sb = after(sa, 1), na = after(sa, 2), nb = after(sa, 3), aa = after(sa, 4);
+    const int sb = after(sa, 1), na = after(sa, 2), nb = after(sa, 3);
     if constexpr (MORE && !FAST) {
       put_a(na);
       put_b(nb);
@@ -421,9 +425,9 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
       for (int i = 0; i < MB; ++i) {
         const int region = ks * MB + i, l = region + kAhead;
         if constexpr (MORE && FAST) {
-          if (region > kMeet) direct_b(s + 2, sa, region - kMeet - 1);
-          else if (l < kLB) direct_b(s + 1, nb, l);
-          else direct_a(s + 2, aa, l - kLB);
+          if (region > kMeet) direct_b(s + D, sa, region - kMeet - 1);
+          else if (l < kLB) direct_b(s + D - 1, after(sa, 2 * D - 1), l);
+          else direct_a(s + D, after(sa, 2 * D), l - kLB);
         }
         if (ks < 3) frag_part(sa, sb, ks + 1, i, MB - 1);
         else if (MORE && i > 0) frag_part(na, nb, 0, i - 1, MB - 1);
@@ -432,7 +436,7 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
         __builtin_amdgcn_sched_barrier(0);
         if (MORE && region == kMeet) {
           if constexpr (FAST) {
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLA) : "memory");
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kFlying) : "memory");
           } else {
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
           }
@@ -507,26 +511,26 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
 }
 
 // Both projections with their gate.
-template <int ET, int OUT, int MB, int NB, bool FAST>
-__global__ __launch_bounds__(256, MB * NB > 8 ? 1 : 2) void gate_tiles(ProductArgs g) {
-  __shared__ __align__(16) uint8_t smem[lds_bytes(MB, NB)];
-  product<ET, true, true, OUT, MB, NB, FAST>(g, blockIdx.x, 0, smem);
+template <int ET, int OUT, int MB, int NB, int D, bool FAST>
+__global__ __launch_bounds__(256, MB * NB > 8 || D > 2 ? 1 : 2) void gate_tiles(ProductArgs g) {
+  __shared__ __align__(16) uint8_t smem[lds_bytes(MB, NB, D)];
+  product<ET, true, true, OUT, MB, NB, D, FAST>(g, blockIdx.x, 0, smem);
 }
 
 // The two gradient products in one launch, that of the longer sums first: the
 // blocks of one fill what the other leaves of the machine.  nx: blocks of dx.
 template <int ET, int MB, int NB, bool FAST>
 __global__ __launch_bounds__(256, MB * NB > 8 ? 1 : 2) void gradient_tiles(ProductArgs gx, ProductArgs gw, uint32_t nx, uint32_t nw, int dx_first) {
-  __shared__ __align__(16) uint8_t smem[lds_bytes(MB, NB)];
+  __shared__ __align__(16) uint8_t smem[lds_bytes(MB, NB, 2)];
   const uint32_t before = dx_first ? nx : nw;
   const bool first = blockIdx.x < before, is_dx = first == (dx_first != 0);
   const uint32_t b = first ? blockIdx.x : blockIdx.x - before;
   if (is_dx) {
     const uint32_t tiles = nx / gx.splits;
-    product<ET, true, false, kOutC, MB, NB, FAST>(gx, b % tiles, b / tiles, smem);
+    product<ET, true, false, kOutC, MB, NB, 2, FAST>(gx, b % tiles, b / tiles, smem);
   } else {
     const uint32_t tiles = nw / gw.splits;
-    product<ET, false, false, kOutC, MB, NB, FAST>(gw, b % tiles, b / tiles, smem);
+    product<ET, false, false, kOutC, MB, NB, 2, FAST>(gw, b % tiles, b / tiles, smem);
   }
 }
 
@@ -552,9 +556,12 @@ hipError_t launch_gate(const ProductArgs& g, hipStream_t s) {
   const int64_t big = tiles_of(g.M, 2 * g.N, 256), small = tiles_of(g.M, 2 * g.N, 128);
   const bool large = fast && kStepLarge * ceil_div(big, 256) <= (small <= 256 ? kStepAlone : kStepSmall * ceil_div(small, 512));
   const dim3 grid(static_cast<unsigned>(large ? big : small));
-  if (large) gate_tiles<ET, OUT, 4, 4, true><<<grid, 256, 0, s>>>(g);
-  else if (fast) gate_tiles<ET, OUT, 2, 2, true><<<grid, 256, 0, s>>>(g);
-  else gate_tiles<ET, OUT, 2, 2, false><<<grid, 256, 0, s>>>(g);
+  // up to one block a CU a ring of four steps, 144 KB, keeps more of the weights in
+  // flight (65 x 4096 x 14336 BF16 64 -> 52 us)
+  if (large) gate_tiles<ET, OUT, 4, 4, 2, true><<<grid, 256, 0, s>>>(g);
+  else if (fast && small <= 256) gate_tiles<ET, OUT, 2, 2, 4, true><<<grid, 256, 0, s>>>(g);
+  else if (fast) gate_tiles<ET, OUT, 2, 2, 2, true><<<grid, 256, 0, s>>>(g);
+  else gate_tiles<ET, OUT, 2, 2, 2, false><<<grid, 256, 0, s>>>(g);
   return hipGetLastError();
 }
 
