@@ -91,50 +91,54 @@ __device__ __forceinline__ void wave_lds() { asm volatile("s_waitcnt lgkmcnt(0)"
 // holds row l % 32 and columns 8 q + 4 (l / 32) + e in register 4 q + e.  A band of
 // 32 rows x 32 NBW columns leaves through this wave's LDS region as whole 16-byte
 // pieces of rows; the pitch, a row's bytes + 16, spreads 16 rows over all banks.
-// value(nb, r): the element of column block nb in register r.
-template <int CT, int NBW, typename V>
-__device__ __forceinline__ void band_out(V&& value, void* C, int64_t ldc, int64_t row0, int64_t col0, int64_t M,
-                                         int64_t N, uint8_t* buf) {
-  constexpr int kES = CT == AMP_F32 ? 4 : 2, kRow = NBW * 32 * kES, kPitch = kRow + 16;
-  constexpr int kLPR = kRow / 16, kRPP = 64 / kLPR, kEPL = 16 / kES;
-  const int lane = threadIdx.x & 63;
-  uint8_t* mine = buf + (lane & 31) * kPitch + (lane >> 5) * 4 * kES;
-  wave_lds();
+// value(nb, r): the element of column block nb in register r.  Several bands are put
+// before the first is stored: LDS latency is met once.
+template <int CT, int NBW>
+struct BandOut {
+  static constexpr int kES = CT == AMP_F32 ? 4 : 2, kRow = NBW * 32 * kES, kPitch = kRow + 16, kBytes = 32 * kPitch;
+  static constexpr int kLPR = kRow / 16, kRPP = 64 / kLPR, kEPL = 16 / kES;
+  template <typename V>
+  static __device__ __forceinline__ void put(V&& value, uint8_t* buf) {
+    const int lane = threadIdx.x & 63;
+    uint8_t* mine = buf + (lane & 31) * kPitch + (lane >> 5) * 4 * kES;
 #pragma unroll
-  for (int nb = 0; nb < NBW; ++nb)
+    for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float x[4] = {value(nb, 4 * q), value(nb, 4 * q + 1), value(nb, 4 * q + 2), value(nb, 4 * q + 3)};
-      uint8_t* p = mine + (nb * 32 + 8 * q) * kES;
-      if constexpr (CT == AMP_F32) *reinterpret_cast<u32x4*>(p) = u32x4{fbits(x[0]), fbits(x[1]), fbits(x[2]), fbits(x[3])};
-      else *reinterpret_cast<u32x2*>(p) = u32x2{to16x2<CT>(x[0], x[1]), to16x2<CT>(x[2], x[3])};
-    }
-  wave_lds();
-  const int64_t col = col0 + (lane % kLPR) * kEPL;
+      for (int q = 0; q < 4; ++q) {
+        const float x[4] = {value(nb, 4 * q), value(nb, 4 * q + 1), value(nb, 4 * q + 2), value(nb, 4 * q + 3)};
+        uint8_t* p = mine + (nb * 32 + 8 * q) * kES;
+        if constexpr (CT == AMP_F32) *reinterpret_cast<u32x4*>(p) = u32x4{fbits(x[0]), fbits(x[1]), fbits(x[2]), fbits(x[3])};
+        else *reinterpret_cast<u32x2*>(p) = u32x2{to16x2<CT>(x[0], x[1]), to16x2<CT>(x[2], x[3])};
+      }
+  }
+  static __device__ __forceinline__ void store(void* C, int64_t ldc, int64_t row0, int64_t col0, int64_t M, int64_t N, const uint8_t* buf) {
+    const int lane = threadIdx.x & 63;
+    const int64_t col = col0 + (lane % kLPR) * kEPL;
 #pragma unroll
-  for (int ps = 0; ps < 32 / kRPP; ++ps) {
-    const int rl = ps * kRPP + lane / kLPR;
-    const int64_t row = row0 + rl;
-    const uint8_t* q = buf + rl * kPitch + (lane % kLPR) * 16;
-    if (row >= M || col >= N) continue;
-    uint8_t* out = static_cast<uint8_t*>(C) + (row * ldc + col) * kES;
-    if (col + kEPL <= N) {
-      *reinterpret_cast<u32x4_u*>(out) = *reinterpret_cast<const u32x4*>(q);
-    } else {
-      for (int j = 0; j < N - col; ++j) {
-        if constexpr (CT == AMP_F32) reinterpret_cast<float*>(out)[j] = reinterpret_cast<const float*>(q)[j];
-        else reinterpret_cast<uint16_t*>(out)[j] = reinterpret_cast<const uint16_t*>(q)[j];
+    for (int ps = 0; ps < 32 / kRPP; ++ps) {
+      const int rl = ps * kRPP + lane / kLPR;
+      const int64_t row = row0 + rl;
+      const uint8_t* q = buf + rl * kPitch + (lane % kLPR) * 16;
+      if (row >= M || col >= N) continue;
+      uint8_t* out = static_cast<uint8_t*>(C) + (row * ldc + col) * kES;
+      if (col + kEPL <= N) {
+        *reinterpret_cast<u32x4_u*>(out) = *reinterpret_cast<const u32x4*>(q);
+      } else {
+        for (int j = 0; j < N - col; ++j) {
+          if constexpr (CT == AMP_F32) reinterpret_cast<float*>(out)[j] = reinterpret_cast<const float*>(q)[j];
+          else reinterpret_cast<uint16_t*>(out)[j] = reinterpret_cast<const uint16_t*>(q)[j];
+        }
       }
     }
   }
-}
+};
 
 // The reverse way for a band of a 16-bit matrix: its pieces on their way into
 // registers (zeros outside), then through LDS into the lanes' elements, four of
 // one row in v[nb][q].
 template <int NBW>
-struct Band {
-  static constexpr int kRow = NBW * 64, kPitch = kRow + 16, kLPR = kRow / 16, kRPP = 64 / kLPR;
+struct BandIn {
+  static constexpr int kRow = NBW * 64, kPitch = kRow + 16, kBytes = 32 * kPitch, kLPR = kRow / 16, kRPP = 64 / kLPR;
   u32x4 w[32 / kRPP];
   __device__ __forceinline__ void load(const void* X, int64_t ldx, int64_t row0, int64_t col0, int64_t M, int64_t N) {
     const int lane = threadIdx.x & 63;
@@ -146,13 +150,14 @@ struct Band {
       w[ps] = row < M ? ld16_part(static_cast<const uint16_t*>(X) + row * ldx + col, left) : u32x4{0u, 0u, 0u, 0u};
     }
   }
-  __device__ __forceinline__ void spread(u32x2 (&v)[NBW][4], uint8_t* buf) const {
+  __device__ __forceinline__ void put(uint8_t* buf) const {
     const int lane = threadIdx.x & 63;
-    wave_lds();
 #pragma unroll
     for (int ps = 0; ps < 32 / kRPP; ++ps)
       *reinterpret_cast<u32x4*>(buf + (ps * kRPP + lane / kLPR) * kPitch + (lane % kLPR) * 16) = w[ps];
-    wave_lds();
+  }
+  static __device__ __forceinline__ void spread(u32x2 (&v)[NBW][4], const uint8_t* buf) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int nb = 0; nb < NBW; ++nb)
 #pragma unroll
@@ -460,51 +465,100 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   constexpr int kBandCols = kGate ? 16 * NB : 32 * NB, kRegion = kSlots * kSlot / 4;
-  static_assert(32 * (kBandCols * (kGate ? 2 : 4) + 16) <= kRegion, "a wave's band exceeds its part of the slots");
   uint8_t* buf = smem + wave * kRegion;
   const int64_t row0 = m0 + wm * 32 * MB, col0 = n0 + wn * kBandCols;
   if constexpr (OUT == kOutC) {
+    auto leave = [&](auto band, void* C) __attribute__((always_inline)) {
+      using Out = decltype(band);
+      constexpr int kAtOnce = MB * Out::kBytes <= kRegion ? MB : MB / 2;
+      static_assert(kAtOnce * Out::kBytes <= kRegion, "the bands exceed a wave's part of the slots");
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      auto value = [&](int nb, int r) __attribute__((always_inline)) { return acc[i][nb][r]; };
-      if (g.out32) band_out<AMP_F32, NB>(value, static_cast<float*>(g.C) + z * g.M * g.N, g.ldc, row0 + 32 * i, col0, g.M, g.N, buf);
-      else band_out<ET, NB>(value, g.C, g.ldc, row0 + 32 * i, col0, g.M, g.N, buf);
-    }
+      for (int i0 = 0; i0 < MB; i0 += kAtOnce) {
+        wave_lds();
+#pragma unroll
+        for (int i = i0; i < i0 + kAtOnce; ++i)
+          Out::put([&](int nb, int r) __attribute__((always_inline)) { return acc[i][nb][r]; }, buf + (i - i0) * Out::kBytes);
+        wave_lds();
+#pragma unroll
+        for (int i = i0; i < i0 + kAtOnce; ++i) Out::store(C, g.ldc, row0 + 32 * i, col0, g.M, g.N, buf + (i - i0) * Out::kBytes);
+      }
+    };
+    if (g.out32) leave(BandOut<AMP_F32, NB>{}, static_cast<float*>(g.C) + z * g.M * g.N);
+    else leave(BandOut<ET, NB>{}, g.C);
   } else {
+    using Out = BandOut<ET, NBH>;
     void* const gu2 = static_cast<uint16_t*>(g.gu) + g.N;       // the up half of [g | u]
-    Band<NBH> next;
-    if constexpr (OUT == kOutGrad) next.load(g.dy, g.lddy, row0, col0, g.M, g.N);
+    auto store = [&](void* C, int64_t ldc, int i, int place) __attribute__((always_inline)) {
+      Out::store(C, ldc, row0 + 32 * i, col0, g.M, g.N, buf + place * Out::kBytes);
+    };
+    auto put = [&](int i, int half, int place) __attribute__((always_inline)) {
+      Out::put([&](int nb, int r) __attribute__((always_inline)) { return acc[i][half * NBH + nb][r]; }, buf + place * Out::kBytes);
+    };
+    if constexpr (OUT == kOutGate) {
+      static_assert(2 * MB * Out::kBytes <= kRegion, "the bands exceed a wave's part of the slots");
+      if (g.gu) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i) {
-      const int64_t row = row0 + 32 * i;
-      u32x2 dy[NBH][4];
-      if constexpr (OUT == kOutGrad) {
-        next.spread(dy, buf);
-        if (i + 1 < MB) next.load(g.dy, g.lddy, row + 32, col0, g.M, g.N);
+        for (int i = 0; i < MB; ++i) {
+          put(i, 0, 2 * i);
+          put(i, 1, 2 * i + 1);
+        }
+        wave_lds();
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+          store(g.gu, g.ldgu, i, 2 * i);
+          store(gu2, g.ldgu, i, 2 * i + 1);
+        }
+        wave_lds();
       }
-      if (OUT == kOutGate && g.gu) {
-        band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][nb][r]; }, g.gu, g.ldgu, row, col0, g.M, g.N, buf);
-        band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][NBH + nb][r]; }, gu2, g.ldgu, row, col0, g.M, g.N, buf);
+      if (g.C) {
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+          Out::put([&](int nb, int r) __attribute__((always_inline)) {
+            const float x = acc[i][nb][r];
+            return x * gate(x).s * acc[i][NBH + nb][r];
+          }, buf + i * Out::kBytes);
+        wave_lds();
+#pragma unroll
+        for (int i = 0; i < MB; ++i) store(g.C, g.ldc, i, i);
       }
-      // y = g s u; with dy, g and u make place for dg = dy s u (1 + g (1 - s)) and du = dy s g
-      float y[NBH][16];
+    } else {
+      // dy first, all of it; then y, dg and du of one band after the other
+      using In = BandIn<NBH>;
+      static_assert(MB * In::kBytes + 3 * Out::kBytes <= kRegion, "the bands exceed a wave's part of the slots");
+      uint8_t* const dys = buf + 3 * Out::kBytes;
+      In in[MB];
 #pragma unroll
-      for (int nb = 0; nb < NBH; ++nb)
+      for (int i = 0; i < MB; ++i) in[i].load(g.dy, g.lddy, row0 + 32 * i, col0, g.M, g.N);
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float x = acc[i][nb][r], u = acc[i][NBH + nb][r];
-          const Gate q = gate(x);
-          y[nb][r] = x * q.s * u;
-          if constexpr (OUT == kOutGrad) {
+      for (int i = 0; i < MB; ++i) in[i].put(dys + i * In::kBytes);
+      wave_lds();
+#pragma unroll
+      for (int i = 0; i < MB; ++i) {
+        u32x2 dy[NBH][4];
+        In::spread(dy, dys + i * In::kBytes);
+        if (g.C)
+          Out::put([&](int nb, int r) __attribute__((always_inline)) {
+            const float x = acc[i][nb][r];
+            return x * gate(x).s * acc[i][NBH + nb][r];
+          }, buf + 2 * Out::kBytes);
+        // dg = dy s u (1 + g (1 - s)) and du = dy s g in place of g and u
+#pragma unroll
+        for (int nb = 0; nb < NBH; ++nb)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float x = acc[i][nb][r], u = acc[i][NBH + nb][r];
+            const Gate q = gate(x);
             const float ds = from16<ET>(dy[nb][r >> 2][(r & 3) >> 1] >> (16 * (r & 1)) & 0xffffu) * q.s;
             acc[i][nb][r] = ds * u * (1.0f + x * q.om);
             acc[i][NBH + nb][r] = ds * x;
           }
-        }
-      if (g.C) band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return y[nb][r]; }, g.C, g.ldc, row, col0, g.M, g.N, buf);
-      if constexpr (OUT == kOutGrad) {
-        band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][nb][r]; }, g.gu, g.ldgu, row, col0, g.M, g.N, buf);
-        band_out<ET, NBH>([&](int nb, int r) __attribute__((always_inline)) { return acc[i][NBH + nb][r]; }, gu2, g.ldgu, row, col0, g.M, g.N, buf);
+        put(i, 0, 0);
+        put(i, 1, 1);
+        wave_lds();
+        if (g.C) store(g.C, g.ldc, i, 2);
+        store(g.gu, g.ldgu, i, 0);
+        store(gu2, g.ldgu, i, 1);
+        wave_lds();
       }
     }
   }
