@@ -5,8 +5,8 @@ A thin ctypes binding of ``libamp.so`` (built from ``csrc/`` by
 argument order of the C entry point declared in ``include/amp.h``; this module
 only marshals arguments (device pointers from torch tensors or ints, host
 structs, the stream handle) and turns a negative status into ``AmpError``; the
-norm, gated-activation and requantization calls do so in C (``_quick``) where
-every operand is a contiguous tensor on the current GPU.
+norm, gated-activation, requantization, feed-forward-block and list calls do so
+in C (``_quick``) where every operand is a contiguous tensor on the current GPU.
 All arithmetic runs in the HIP kernels.  There is no CPU fallback: when the
 library is missing or no gfx950 device is current, the calls raise.
 """
@@ -131,8 +131,6 @@ class TensorList:
                     self.where = t.get_device()
                 elif self.where != t.get_device():
                     raise ValueError(f"TensorList: tensor {i} is on {t.device}, others are not")
-        # the class's method, of which a call over hundreds of tensors takes three quarters of the time
-        self.ask = type(self.tensors[0]).data_ptr if self.tensors and all(type(t) is type(self.tensors[0]) for t in self.tensors) else _ptr
         self.places = [t.data_ptr() for t in self.tensors]
 
     def __len__(self):
@@ -235,6 +233,8 @@ def _bind() -> None:
     import torch
     q.bind(torch.Tensor, Fp8Tiles, *(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
         "amp_rmsnorm", "amp_rmsnorm_backward", "amp_swiglu", "amp_swiglu_backward", "amp_requantize_blockwise")))
+    q.bind_block(TensorList, *(ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in (
+        "amp_gemm_swiglu", "amp_gemm_swiglu_backward", "amp_grad_norm_list", "amp_grad_clip_list")))
     _plain = q
 
 
@@ -581,6 +581,10 @@ def amp_requantize_blockwise(x, rows, cols, d_row, col, ct, qt, stream=None):
 
 def amp_gemm_swiglu(M, F, K, x, t, ldx, w, ldw, y=None, ldy=0, gu=None, ldgu=0, stream=None):
     f = "amp_gemm_swiglu"
+    if stream is None and _plain is not None:
+        st = _plain.gemm_swiglu(M, F, K, x, t, ldx, w, ldw, y, ldy, gu, ldgu, *_now())
+        if st is not None:
+            return _check(f, st)
     at = _where()
     _check(f, load().amp_gemm_swiglu(
         M, F, K, _mem(f, "x", x, _mat(M, K, ldx, t), at), t, ldx, _mem(f, "w", w, _mat(2 * F, K, ldw, t), at), ldw,
@@ -591,6 +595,11 @@ def amp_gemm_swiglu(M, F, K, x, t, ldx, w, ldw, y=None, ldy=0, gu=None, ldgu=0, 
 def amp_gemm_swiglu_backward(M, F, K, dy, t, lddy, x, ldx, w, ldw, gu, ldgu, dgu, lddgu, y=None, ldy=0, dx=None, lddx=0,
                              dw=None, dwt=BF16, lddw=0, d_work=None, stream=None):
     f = "amp_gemm_swiglu_backward"
+    if stream is None and _plain is not None:
+        st = _plain.gemm_swiglu_backward(M, F, K, dy, t, lddy, x, ldx, w, ldw, gu, ldgu, dgu, lddgu, y, ldy, dx, lddx, dw, dwt, lddw,
+                                         d_work, *_now())
+        if st is not None:
+            return _check(f, st)
     at = _where()
     _check(f, load().amp_gemm_swiglu_backward(
         M, F, K, _mem(f, "dy", dy, _mat(M, F, lddy, t), at), t, lddy, _mem(f, "x", x, _mat(M, K, ldx, t), at), ldx,
@@ -604,7 +613,7 @@ def _listed(fn: str, what: str, ts: TensorList | None, at: list) -> int | None:
     """Address of a list's array; a tensor that has moved is refused."""
     if ts is None:
         return None
-    if list(map(ts.ask, ts.tensors)) != ts.places:
+    if [t.data_ptr() for t in ts.tensors] != ts.places:
         raise ValueError(f"{fn}: a tensor of {what} has moved since the TensorList was made from it")
     if ts.tensors and ts.where != at[0]:
         at.append(f"{what} is on {ts.tensors[0].device}")
@@ -613,6 +622,10 @@ def _listed(fn: str, what: str, ts: TensorList | None, at: list) -> int | None:
 
 def amp_grad_norm_list(grads: TensorList, first, d_state, d_norm, max_norm=1.0, d_out=None, stream=None):
     f = "amp_grad_norm_list"
+    if stream is None and _plain is not None:
+        st = _plain.norm_list(grads, first, d_state, d_norm, max_norm, d_out, *_now())
+        if st is not None:
+            return _check(f, st)
     at = _where()
     _check(f, load().amp_grad_norm_list(
         _listed(f, "grads", grads, at), len(grads), int(bool(first)),
@@ -622,6 +635,10 @@ def amp_grad_norm_list(grads: TensorList, first, d_state, d_norm, max_norm=1.0, 
 
 def amp_grad_clip_list(grads: TensorList, outs: TensorList | None = None, d_state=None, d_coef=None, stream=None):
     f = "amp_grad_clip_list"
+    if stream is None and _plain is not None:
+        st = _plain.clip_list(grads, outs, d_state, d_coef, *_now())
+        if st is not None:
+            return _check(f, st)
     if outs is not None and len(outs) != len(grads):
         raise ValueError(f"{f}: {len(grads)} gradients, {len(outs)} outputs")
     at = _where()

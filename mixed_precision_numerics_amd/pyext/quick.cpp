@@ -1,5 +1,5 @@
-// The common case of the norm, gated-activation and requantization calls from
-// Python, in C: operands that are contiguous torch tensors on the current GPU
+// The common case of the norm, gated-activation and requantization calls, of the
+// gated feed-forward block and of the calls over lists of tensors from Python, in C: operands that are contiguous torch tensors on the current GPU
 // with room for what the call spans.  A call of one token spends most of its
 // time in the checks and conversions, not in the kernel.
 //
@@ -18,13 +18,19 @@ namespace {
 
 PyTypeObject* g_tensor;   // torch.Tensor
 PyTypeObject* g_tiles;    // Fp8Tiles
-PyObject *g_get_device, *g_nbytes, *g_is_contiguous, *g_data_ptr, *g_tensors;
+PyTypeObject* g_list;     // TensorList
+PyObject *g_get_device, *g_nbytes, *g_is_contiguous, *g_data_ptr, *g_tensors, *g_array, *g_places, *g_where;
+PyObject* g_where_is;      // torch.Tensor.data_ptr
 
 decltype(&amp_rmsnorm) g_rmsnorm;
 decltype(&amp_rmsnorm_backward) g_rmsnorm_backward;
 decltype(&amp_swiglu) g_swiglu;
 decltype(&amp_swiglu_backward) g_swiglu_backward;
 decltype(&amp_requantize_blockwise) g_requantize;
+decltype(&amp_gemm_swiglu) g_gemm_swiglu;
+decltype(&amp_gemm_swiglu_backward) g_gemm_swiglu_backward;
+decltype(&amp_grad_norm_list) g_norm_list;
+decltype(&amp_grad_clip_list) g_clip_list;
 
 typedef __int128 wide;
 
@@ -103,6 +109,34 @@ struct Args {
     ok = mem(PyTuple_GET_ITEM(qs, 1), some ? 4 * (static_cast<wide>(nb - 1) * t.lds + rows) : 0) == t.s && ok;
     Py_DECREF(qs);
     return ok ? &t : nullptr;
+  }
+  // The array of a TensorList whose tensors are where they were.
+  const amp_tensor* list(int i, int32_t& count) {
+    PyObject* o = v[i];
+    count = 0;
+    if (!ok || o == Py_None) return nullptr;
+    PyObject *a = nullptr, *ts = nullptr, *at = nullptr;
+    Py_buffer b{};
+    if (!PyObject_TypeCheck(o, g_list) || !(a = PyObject_GetAttr(o, g_array)) || !(ts = PyObject_GetAttr(o, g_tensors)) ||
+        !(at = PyObject_GetAttr(o, g_places)) || !PyList_Check(ts) || !PyList_Check(at) || PyList_GET_SIZE(ts) != PyList_GET_SIZE(at) ||
+        PyObject_GetBuffer(a, &b, PyBUF_SIMPLE) != 0)
+      ok = false;
+    const amp_tensor* p = ok ? static_cast<const amp_tensor*>(b.buf) : nullptr;
+    if (ok) count = static_cast<int32_t>(b.len / static_cast<Py_ssize_t>(sizeof(amp_tensor)));
+    if (ok && PyList_GET_SIZE(ts) > 0) ok = ask(o, g_where, false) == dev && ok;
+    for (Py_ssize_t k = 0; ok && k < PyList_GET_SIZE(ts); ++k) {
+      // the method itself, not looked up in each of hundreds of tensors
+      PyObject* t = PyList_GET_ITEM(ts, k);
+      PyObject* r = PyObject_TypeCheck(t, g_tensor) ? PyObject_Vectorcall(g_where_is, &t, 1, nullptr) : nullptr;
+      ok = r && num(r) == num(PyList_GET_ITEM(at, k)) && ok;
+      Py_XDECREF(r);
+    }
+    PyErr_Clear();
+    if (b.obj) PyBuffer_Release(&b);
+    Py_XDECREF(a);                     // the list keeps its array
+    Py_XDECREF(ts);
+    Py_XDECREF(at);
+    return ok ? p : nullptr;
   }
 };
 
@@ -190,6 +224,74 @@ PyObject* requantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
   AMP_CALL(g_requantize(xq, rows, cols, row, col, ct, qt, stream));
 }
 
+PyObject* gemm_swiglu(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  AMP_OPEN(12);
+  const int64_t M = a.num(0), F = a.num(1), K = a.num(2), ldx = a.num(5), ldw = a.num(7), ldy = a.num(9), ldgu = a.num(11);
+  const int t = a.type(4);
+  if (F < 0 || F > INT64_MAX / 4) Py_RETURN_NONE;
+  const void *x = a.mem(3, span(M, K, ldx, t)), *w = a.mem(6, span(2 * F, K, ldw, t));
+  void *y = a.mem(8, span(M, F, ldy, t)), *gu = a.mem(10, span(M, 2 * F, ldgu, t));
+  AMP_CALL(g_gemm_swiglu(M, F, K, x, t, ldx, w, ldw, y, ldy, gu, ldgu, stream));
+}
+
+PyObject* gemm_swiglu_backward(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  AMP_OPEN(22);
+  const int64_t M = a.num(0), F = a.num(1), K = a.num(2), lddy = a.num(5), ldx = a.num(7), ldw = a.num(9), ldgu = a.num(11),
+                lddgu = a.num(13), ldy = a.num(15), lddx = a.num(17), lddw = a.num(20);
+  const int t = a.type(4), dwt = a.type(19);
+  if (F < 0 || F > INT64_MAX / 4) Py_RETURN_NONE;
+  const void *dy = a.mem(3, span(M, F, lddy, t)), *x = a.mem(6, span(M, K, ldx, t)), *w = a.mem(8, span(2 * F, K, ldw, t)),
+             *gu = a.mem(10, span(M, 2 * F, ldgu, t));
+  void *dgu = a.mem(12, span(M, 2 * F, lddgu, t)), *y = a.mem(14, span(M, F, ldy, t)), *dx = a.mem(16, span(M, K, lddx, t)),
+       *dw = a.mem(18, span(2 * F, K, lddw, dwt));
+  float* work = a.mem<float>(21, span(1, AMP_GEMM_SWIGLU_WORK, AMP_GEMM_SWIGLU_WORK, AMP_F32));
+  AMP_CALL(g_gemm_swiglu_backward(M, F, K, dy, t, lddy, x, ldx, w, ldw, gu, ldgu, dgu, lddgu, y, ldy, dx, lddx, dw, dwt, lddw, work,
+                                  stream));
+}
+
+PyObject* norm_list(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  AMP_OPEN(6);
+  int32_t count;
+  const amp_tensor* grads = a.list(0, count);
+  const int first = PyObject_IsTrue(v[1]);
+  amp_scaler_state* state = a.mem<amp_scaler_state>(2, sizeof(amp_scaler_state));
+  amp_grad_norm_state* norm = a.mem<amp_grad_norm_state>(3, sizeof(amp_grad_norm_state));
+  float* out = a.mem<float>(5, 8);
+  if (first < 0) PyErr_Clear();
+  if (first < 0 || !grads || !PyFloat_Check(v[4])) Py_RETURN_NONE;
+  const float max_norm = static_cast<float>(PyFloat_AS_DOUBLE(v[4]));
+  AMP_CALL(g_norm_list(grads, count, first, state, norm, max_norm, out, stream));
+}
+
+PyObject* clip_list(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  AMP_OPEN(4);
+  int32_t count, as_many;
+  const amp_tensor *grads = a.list(0, count), *outs = a.list(1, as_many);
+  const amp_scaler_state* state = a.mem<amp_scaler_state>(2, sizeof(amp_scaler_state));
+  const float* coef = a.mem<float>(3, 4);
+  if (!grads || (outs && as_many != count)) Py_RETURN_NONE;
+  AMP_CALL(g_clip_list(grads, outs, count, state, coef, stream));
+}
+
+// bind_block(TensorList, addresses of the four entry points above), after bind
+PyObject* bind_block(PyObject*, PyObject* const* v, Py_ssize_t n) {
+  if (n != 5 || !PyType_Check(v[0]) || !g_tensor) { PyErr_SetString(PyExc_TypeError, "bind_block"); return nullptr; }
+  void* p[4];
+  for (int i = 0; i < 4; ++i) {
+    p[i] = PyLong_AsVoidPtr(v[1 + i]);
+    if (!p[i]) { if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind_block"); return nullptr; }
+  }
+  Py_INCREF(v[0]);
+  g_where_is = PyObject_GetAttr(reinterpret_cast<PyObject*>(g_tensor), g_data_ptr);
+  if (!g_where_is) return nullptr;
+  g_list = reinterpret_cast<PyTypeObject*>(v[0]);
+  g_gemm_swiglu = reinterpret_cast<decltype(g_gemm_swiglu)>(p[0]);
+  g_gemm_swiglu_backward = reinterpret_cast<decltype(g_gemm_swiglu_backward)>(p[1]);
+  g_norm_list = reinterpret_cast<decltype(g_norm_list)>(p[2]);
+  g_clip_list = reinterpret_cast<decltype(g_clip_list)>(p[3]);
+  Py_RETURN_NONE;
+}
+
 // bind(torch.Tensor, Fp8Tiles, addresses of the five entry points)
 PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
   if (n != 7 || !PyType_Check(v[0]) || !PyType_Check(v[1])) { PyErr_SetString(PyExc_TypeError, "bind"); return nullptr; }
@@ -212,7 +314,8 @@ PyObject* bind(PyObject*, PyObject* const* v, Py_ssize_t n) {
 
 #define AMP_DEF(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {AMP_DEF(bind), AMP_DEF(rmsnorm), AMP_DEF(rmsnorm_backward), AMP_DEF(swiglu), AMP_DEF(swiglu_backward),
-                           AMP_DEF(requantize), {nullptr, nullptr, 0, nullptr}};
+                           AMP_DEF(requantize), AMP_DEF(bind_block), AMP_DEF(gemm_swiglu), AMP_DEF(gemm_swiglu_backward), AMP_DEF(norm_list),
+                           AMP_DEF(clip_list), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_quick", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
@@ -223,5 +326,8 @@ PyMODINIT_FUNC PyInit__quick(void) {
   g_is_contiguous = PyUnicode_InternFromString("is_contiguous");
   g_data_ptr = PyUnicode_InternFromString("data_ptr");
   g_tensors = PyUnicode_InternFromString("tensors");
+  g_array = PyUnicode_InternFromString("array");
+  g_places = PyUnicode_InternFromString("places");
+  g_where = PyUnicode_InternFromString("where");
   return PyModule_Create(&g_module);
 }
