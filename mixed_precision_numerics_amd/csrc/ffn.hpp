@@ -47,9 +47,8 @@ struct ProductArgs {
   int splits;              // parts of the summed dimension; > 1: C is FP32 [splits][M][N]
 };
 
-// 16 bytes at any 2-byte address: one load or store instruction either way.
+// 16 bytes at any 2-byte address in one load or store.
 typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
-__device__ __forceinline__ u32x4 ld16u(const uint16_t* p) { return *reinterpret_cast<const u32x4_u*>(p); }
 
 template <int ET>
 __device__ __forceinline__ float from16(uint32_t c) {
@@ -73,7 +72,7 @@ __device__ __forceinline__ f32x16 mfma16(u32x4 a, u32x4 b, f32x16 c) {
 
 // Eight elements from p on of which the first n exist, zeros behind them.
 __device__ __forceinline__ u32x4 ld16_part(const uint16_t* p, int n) {
-  if (n >= 8) return ld16u(p);
+  if (n >= 8) return *reinterpret_cast<const u32x4_u*>(p);
   u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int j = 0; j < 8; ++j)

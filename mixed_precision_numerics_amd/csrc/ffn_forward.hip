@@ -18,6 +18,26 @@ __device__ __forceinline__ f32x4 mfma16x16(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
+// Eight elements at any 2-byte address from the dwords that hold them, shifted into
+// place (each dword read holds one of the elements: none lies outside the
+// operand's pages).  Waves that only stream would wait for 16-byte loads at odd
+// addresses: 1 x 4097 x 14336 106 us, so 64.
+typedef uint32_t u32x4_dw __attribute__((ext_vector_type(4), aligned(4)));
+struct Piece {
+  u32x4 w;
+  uint32_t last;
+  static __device__ __forceinline__ uint32_t odd(const uint16_t* p) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 2u; }
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(2));
+    w = *reinterpret_cast<const u32x4_dw*>(q);
+    last = q[3 + (odd(p) >> 1)];
+  }
+  __device__ __forceinline__ u32x4 shifted(uint32_t by) const {
+    return u32x4{__builtin_amdgcn_alignbit(w[1], w[0], by), __builtin_amdgcn_alignbit(w[2], w[1], by),
+                 __builtin_amdgcn_alignbit(w[3], w[2], by), __builtin_amdgcn_alignbit(last, w[3], by)};
+  }
+};
+
 // Up to 16 tokens.  A block owns 16 features; its waves share the summed
 // dimension, 64 elements a wave and turn, straight from memory into the 16x16x32
 // instruction's operands (weights as rows, tokens as columns: lane l holds row l %
@@ -26,7 +46,8 @@ __device__ __forceinline__ f32x4 mfma16x16(u32x4 a, u32x4 b, f32x4 c) {
 // waves with 128 elements a turn: 46), 1 x 5120 x 20480 72 us = 5.8 TB/s (81).
 constexpr int kFewTokens = 16, kFewWaves = 16, kFewTurn = 64;
 
-template <int ET>
+// WHOLE: every row is whole 16-byte pieces.
+template <int ET, bool WHOLE>
 __global__ __launch_bounds__(kFewWaves * 64) void gate_few(ProductArgs g) {
   constexpr int kC = kFewTurn / 32;
   __shared__ float part[kFewWaves][2][4][64];
@@ -39,17 +60,27 @@ __global__ __launch_bounds__(kFewWaves * 64) void gate_few(ProductArgs g) {
   f32x4 acc[2] = {};
   int64_t k = wave * kFewTurn;
   for (; k + kFewTurn <= g.K; k += kFewWaves * kFewTurn) {
-    u32x4 a[2][kC], b[kC];
+    Piece a[2][kC], b[kC];
+    auto load = [&](Piece& v, const uint16_t* p) __attribute__((always_inline)) {
+      if constexpr (WHOLE) v.w = ld16(p);
+      else v.load(p);
+    };
+    auto value = [&](const Piece& v, const uint16_t* p) __attribute__((always_inline)) {
+      if constexpr (WHOLE) return v.w;
+      else return v.shifted(8 * Piece::odd(p));
+    };
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
-      a[0][c] = ld16u(pw[0] + k + 32 * c);
-      a[1][c] = ld16u(pw[1] + k + 32 * c);
-      b[c] = ld16u(px + k + 32 * c);
+      load(a[0][c], pw[0] + k + 32 * c);
+      load(a[1][c], pw[1] + k + 32 * c);
+      load(b[c], px + k + 32 * c);
     }
+    // (k and 32 c are even: a row's pieces are all odd or all even)
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
-      acc[0] = mfma16x16<ET>(a[0][c], b[c], acc[0]);
-      acc[1] = mfma16x16<ET>(a[1][c], b[c], acc[1]);
+      const u32x4 x = value(b[c], px);
+      acc[0] = mfma16x16<ET>(value(a[0][c], pw[0]), x, acc[0]);
+      acc[1] = mfma16x16<ET>(value(a[1][c], pw[1]), x, acc[1]);
     }
   }
   // the one wave whose turn meets the end; zeros behind it on both sides
@@ -85,7 +116,9 @@ __global__ __launch_bounds__(kFewWaves * 64) void gate_few(ProductArgs g) {
 template <int ET>
 hipError_t launch_forward(const ProductArgs& g, hipStream_t s) {
   if (g.M > kFewTokens) return launch_gate<ET, kOutGate>(g, s);
-  gate_few<ET><<<static_cast<unsigned>(ceil_div(g.N, 16)), kFewWaves * 64, 0, s>>>(g);
+  const unsigned blocks = static_cast<unsigned>(ceil_div(g.N, 16));
+  if (aligned(g.A, 16) && aligned(g.B, 16) && g.lda % 8 == 0 && g.ldb % 8 == 0) gate_few<ET, true><<<blocks, kFewWaves * 64, 0, s>>>(g);
+  else gate_few<ET, false><<<blocks, kFewWaves * 64, 0, s>>>(g);
   return hipGetLastError();
 }
 
