@@ -23,6 +23,7 @@
 // not meet a zero), as the first step of a tile.  Operands without 16-byte
 // rows go that way in every step (FAST == false).
 #pragma once
+#include <algorithm>
 #include <type_traits>
 
 #include "common.hpp"
@@ -563,6 +564,117 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
   }
 }
 
+template <int ET>
+__device__ __forceinline__ f32x4 mfma16x16(u32x4 a, u32x4 b, f32x4 c) {
+  if constexpr (ET == AMP_F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// Eight elements at any 2-byte address from the dwords that hold them, shifted into
+// place (each dword read holds one of the elements: none lies outside the
+// operand's pages).  Waves that only stream would wait for 16-byte loads at odd
+// addresses: 1 x 4097 x 14336 106 us, so 64.
+typedef uint32_t u32x4_dw __attribute__((ext_vector_type(4), aligned(4)));
+struct Piece {
+  u32x4 w;
+  uint32_t last;
+  static __device__ __forceinline__ uint32_t odd(const uint16_t* p) { return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 2u; }
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(2));
+    w = *reinterpret_cast<const u32x4_dw*>(q);
+    last = q[3 + (odd(p) >> 1)];
+  }
+  __device__ __forceinline__ u32x4 shifted(uint32_t by) const {
+    return u32x4{__builtin_amdgcn_alignbit(w[1], w[0], by), __builtin_amdgcn_alignbit(w[2], w[1], by),
+                 __builtin_amdgcn_alignbit(w[3], w[2], by), __builtin_amdgcn_alignbit(last, w[3], by)};
+  }
+};
+
+// 16 tokens and 16 features a block; its waves share the summed
+// dimension, 64 elements a wave and turn, straight from memory into the 16x16x32
+// instruction's operands (weights as rows, tokens as columns: lane l holds row l %
+// 16 and elements 8 (l / 16) .. + 7), and join their sums in LDS.  16 waves a block
+// keep 64 KB of weights a CU in flight: 1 x 4096 x 14336 BF16 43 us = 5.5 TB/s (8
+// waves with 128 elements a turn: 46), 1 x 5120 x 20480 72 us = 5.8 TB/s (81).
+constexpr int kFewWaves = 16, kFewTurn = 64;
+
+// WHOLE: every row is whole 16-byte pieces.
+template <int ET, int OUT, bool WHOLE>
+__global__ __launch_bounds__(kFewWaves * 64) void gate_few(ProductArgs g) {
+  __shared__ float part[kFewWaves][2][4][64];
+  const int lane = threadIdx.x & 63, wave = wave_id(), q = lane >> 4, i16 = lane & 15;
+  const int64_t f0 = static_cast<int64_t>(blockIdx.x) * 16, m0 = static_cast<int64_t>(blockIdx.y) * 16;
+  const int64_t f = f0 + i16 < g.N ? f0 + i16 : g.N - 1, m = m0 + i16 < g.M ? m0 + i16 : g.M - 1;
+  const uint16_t* w = static_cast<const uint16_t*>(g.B) + 8 * q;
+  const uint16_t* const px = static_cast<const uint16_t*>(g.A) + m * g.lda + 8 * q;
+  const uint16_t* const pw[2] = {w + f * g.ldb, w + (g.N + f) * g.ldb};
+  f32x4 acc[2] = {};
+  auto load = [&](Piece& v, const uint16_t* p) __attribute__((always_inline)) {
+    if constexpr (WHOLE) v.w = ld16(p);
+    else v.load(p);
+  };
+  // (a turn's start is even: a row's pieces are all odd or all even)
+  auto value = [&](const Piece& v, const uint16_t* p) __attribute__((always_inline)) {
+    if constexpr (WHOLE) return v.w;
+    else return v.shifted(8 * Piece::odd(p));
+  };
+  int64_t k = wave * kFewTurn;
+  for (; k + kFewTurn <= g.K; k += kFewWaves * kFewTurn) {
+    constexpr int kC = kFewTurn / 32;
+    Piece a[2][kC], b[kC];
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      load(a[0][c], pw[0] + k + 32 * c);
+      load(a[1][c], pw[1] + k + 32 * c);
+      load(b[c], px + k + 32 * c);
+    }
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      const u32x4 x = value(b[c], px);
+      acc[0] = mfma16x16<ET>(value(a[0][c], pw[0]), x, acc[0]);
+      acc[1] = mfma16x16<ET>(value(a[1][c], pw[1]), x, acc[1]);
+    }
+  }
+  // the one wave whose turn meets the end; zeros behind it on both sides
+  for (; k < g.K; k += 32) {
+    const int64_t left = g.K - k - 8 * q;
+    const int n = left < 0 ? 0 : left < 8 ? static_cast<int>(left) : 8;
+    const u32x4 b = ld16_part(px + k, n);
+    acc[0] = mfma16x16<ET>(ld16_part(pw[0] + k, n), b, acc[0]);
+    acc[1] = mfma16x16<ET>(ld16_part(pw[1] + k, n), b, acc[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) part[wave][i][r][lane] = acc[i][r];
+  __syncthreads();
+  // row 4 (l / 16) + r of a tile, token l % 16; neighbouring threads store neighbouring features
+  const int fl = threadIdx.x % 16, tok = threadIdx.x / 16, at = fl / 4 * 16 + tok;
+  const int64_t row = m0 + tok, col = f0 + fl;
+  if (threadIdx.x >= 256 || col >= g.N || row >= g.M) return;
+  float a = 0.0f, u = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kFewWaves; ++v) {
+    a += part[v][0][fl % 4][at];
+    u += part[v][1][fl % 4][at];
+  }
+  const Gate s = gate(a);
+  if (g.C) static_cast<uint16_t*>(g.C)[row * g.ldc + col] = static_cast<uint16_t>(to16<ET>(a * s.s * u));
+  if constexpr (OUT == kOutGrad) {
+    const float ds = from16<ET>(static_cast<const uint16_t*>(g.dy)[row * g.lddy + col]) * s.s;
+    const float dg = ds * u * (1.0f + a * s.om);
+    u = ds * a;
+    a = dg;
+  }
+  if (g.gu) {
+    uint16_t* p = static_cast<uint16_t*>(g.gu) + row * g.ldgu + col;
+    p[0] = static_cast<uint16_t>(to16<ET>(a));
+    p[g.N] = static_cast<uint16_t>(to16<ET>(u));
+  }
+}
+
 // Both projections with their gate.
 template <int ET, int OUT, int MB, int NB, int D, bool FAST>
 __global__ __launch_bounds__(256, MB * NB > 8 || D > 2 ? 1 : 2) void gate_tiles(ProductArgs g) {
@@ -600,14 +712,34 @@ inline int64_t tiles_of(int64_t M, int64_t cols, int64_t edge) { return ceil_div
 
 // Microseconds of a step of 64 along the summed dimension: a tile of 256 x 256
 // has a CU for itself, tiles of 128 x 128 run two to a CU; with fewer than one a
-// CU a step of theirs is bound by latency.
-constexpr double kStepLarge = 1.5, kStepSmall = 1.05, kStepAlone = 0.55;
+// CU a step of theirs is bound by latency, less with a longer ring.
+constexpr double kStepLarge = 1.5, kStepSmall = 1.05, kStepAlone = 0.55, kStepFar = 0.4;
+// Of a tile's beginning and end, of the gate and of its gradient.
+constexpr double kGateLarge = 11.0, kGateSmall = 6.0, kGradLarge = 25.0, kGradSmall = 8.0;
+// Of a turn of gate_few's waves, of which two blocks share a CU, and its ends; and
+// the weights' bytes a microsecond.
+constexpr double kTurnFew = 2.0, kBlockFew = 3.0, kStream = 5.0e6;
 
 template <int ET, int OUT>
 hipError_t launch_gate(const ProductArgs& g, hipStream_t s) {
   const bool fast = direct_operand(g.A, g.lda, true, g.M) && direct_operand(g.B, g.ldb, true, g.N);
-  const int64_t big = tiles_of(g.M, 2 * g.N, 256), small = tiles_of(g.M, 2 * g.N, 128);
-  const bool large = fast && kStepLarge * ceil_div(big, 256) <= (small <= 256 ? kStepAlone : kStepSmall * ceil_div(small, 512));
+  const int64_t big = tiles_of(g.M, 2 * g.N, 256), small = tiles_of(g.M, 2 * g.N, 128), steps = ceil_div(g.K, kStepK);
+  constexpr double kLarge = OUT == kOutGrad ? kGradLarge : kGateLarge, kSmall = OUT == kOutGrad ? kGradSmall : kGateSmall;
+  const double t_large = static_cast<double>(ceil_div(big, 256)) * (kStepLarge * steps + kLarge);
+  const double t_small = small <= 256 ? (fast ? kStepFar : 2 * kStepAlone) * steps + kSmall
+                                      : static_cast<double>(ceil_div(small, 512)) * (kStepSmall * steps + kSmall);
+  const int64_t groups = ceil_div(g.M, 16), few = groups * ceil_div(g.N, 16);
+  const double weights = 4.0 * static_cast<double>(g.N) * static_cast<double>(g.K) / kStream;
+  const double t_few = std::max(static_cast<double>(ceil_div(few, 512)) * (kTurnFew * ceil_div(g.K, kFewWaves * kFewTurn) + kBlockFew),
+                                static_cast<double>(groups) * weights);
+  if (groups == 1 || (groups <= 8 && small <= 256 && t_few < std::max(t_small, weights))) {
+    const dim3 grid(static_cast<unsigned>(ceil_div(g.N, 16)), static_cast<unsigned>(groups));
+    const bool whole = aligned(g.A, 16) && aligned(g.B, 16) && g.lda % 8 == 0 && g.ldb % 8 == 0;
+    if (whole) gate_few<ET, OUT, true><<<grid, kFewWaves * 64, 0, s>>>(g);
+    else gate_few<ET, OUT, false><<<grid, kFewWaves * 64, 0, s>>>(g);
+    return hipGetLastError();
+  }
+  const bool large = fast && t_large <= t_small;
   const dim3 grid(static_cast<unsigned>(large ? big : small));
   // up to one block a CU a ring of four steps, 144 KB, keeps more of the weights in
   // flight (65 x 4096 x 14336 BF16 64 -> 52 us)
