@@ -162,14 +162,30 @@ __global__ __launch_bounds__(kListThreads) void norm_list_kernel(const NormTable
 }
 
 // The partial sums in a fixed order, the sum's scaling by 1/S^2 and the clip
-// coefficient.
-__global__ __launch_bounds__(kWave) void norm_list_finish(const double* __restrict__ partial, int nb, int first, double* __restrict__ sumsq,
-                                                          const amp_scaler_state* st, float max_norm, float* out) {
-  double v = 0.0;
-  for (int b = threadIdx.x; b < nb; b += kWave) v += partial[b];
+// coefficient.  All latency: every load is on its way before the first is used
+// (1024 sums by one wave, one after the other: 7.7 us instead of 4.0).
+constexpr int kFinishThreads = 256;
+__global__ __launch_bounds__(kFinishThreads) void norm_list_finish(const double* __restrict__ partial, int nb, int first,
+                                                                   double* __restrict__ sumsq, const amp_scaler_state* st, float max_norm,
+                                                                   float* out) {
+  __shared__ double red[kFinishThreads / kWave];
+  constexpr int kEach = AMP_NORM_PARTIALS / kFinishThreads;
+  static_assert(kEach * kFinishThreads == AMP_NORM_PARTIALS, "every partial sum has a thread");
+  double each[kEach], v = 0.0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int b = i * kFinishThreads + threadIdx.x;
+    each[i] = b < nb ? partial[b] : 0.0;
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) v += each[i];
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, kWave);
+  if (threadIdx.x % kWave == 0) red[threadIdx.x / kWave] = v;
+  __syncthreads();
   if (threadIdx.x != 0) return;
+  v = 0.0;
+  for (int w = 0; w < kFinishThreads / kWave; ++w) v += red[w];
   const double inv = static_cast<double>(1.0f / st->scale);
   v = (first ? 0.0 : *sumsq) + v * inv * inv;
   *sumsq = v;
@@ -316,7 +332,7 @@ hipError_t launch_grad_norm_list(const amp_tensor* grads, int32_t count, int fir
     if (hipError_t e = hipGetLastError()) return e;
     nb += static_cast<int>(blocks);
   }
-  norm_list_finish<<<1, kWave, 0, s>>>(ns->partial, nb, first, &ns->sumsq, st, max_norm, out);
+  norm_list_finish<<<1, kFinishThreads, 0, s>>>(ns->partial, nb, first, &ns->sumsq, st, max_norm, out);
   return hipGetLastError();
 }
 
