@@ -113,7 +113,8 @@ class TensorList:
     Made once, e.g. beside a model's parameters, and passed to every step.
     Tensors are kept alive; each has to hold its elements one after another on
     one GPU, checked here, and has to stay where it was: a call with a list of
-    which one was resized or given other storage is refused."""
+    which one was resized or given other storage is refused.  A list that is
+    written to names no memory twice."""
 
     def __init__(self, entries):
         entries = list(entries)
@@ -123,6 +124,9 @@ class TensorList:
             if dtype not in (F32, F16, BF16):
                 raise ValueError(f"TensorList: tensor {i} is of type {dtype}")
             _room("TensorList", f"tensor {i}", t, _vec(n, dtype))
+            if n > 0 and hasattr(t, "stride") and not t.is_contiguous():
+                if 1 + sum((size - 1) * step for size, step in zip(t.shape, t.stride())) != t.numel():
+                    raise ValueError(f"TensorList: tensor {i}'s elements are not one after another")
             a = self.array[i]
             a.p, a.n, a.type = _ptr(t), n, dtype
             if n > 0 and hasattr(t, "get_device"):
@@ -132,6 +136,8 @@ class TensorList:
                 elif self.where != t.get_device():
                     raise ValueError(f"TensorList: tensor {i} is on {t.device}, others are not")
         self.places = [t.data_ptr() for t in self.tensors]
+        spans = sorted((a.p, a.p + _vec(a.n, a.type)) for a in self.array if a.n > 0 and a.p)
+        self.apart = all(one[1] <= two[0] for one, two in zip(spans, spans[1:]))     # may be written to
 
     def __len__(self):
         return len(self.array)
@@ -641,6 +647,8 @@ def amp_grad_clip_list(grads: TensorList, outs: TensorList | None = None, d_stat
             return _check(f, st)
     if outs is not None and len(outs) != len(grads):
         raise ValueError(f"{f}: {len(grads)} gradients, {len(outs)} outputs")
+    if not (grads if outs is None else outs).apart:
+        raise ValueError(f"{f}: tensors of {'grads' if outs is None else 'outs'} overlap")
     at = _where()
     _check(f, load().amp_grad_clip_list(
         _listed(f, "grads", grads, at), _listed(f, "outs", outs, at), len(grads),

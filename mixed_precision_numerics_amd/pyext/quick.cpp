@@ -1,7 +1,8 @@
 // The common case of the norm, gated-activation and requantization calls, of the
-// gated feed-forward block and of the calls over lists of tensors from Python, in C: operands that are contiguous torch tensors on the current GPU
-// with room for what the call spans.  A call of one token spends most of its
-// time in the checks and conversions, not in the kernel.
+// gated feed-forward block and of the calls over lists of tensors from Python, in
+// C: operands that are contiguous torch tensors on the current GPU with room for
+// what the call spans.  A call of one token spends most of its time in the checks
+// and conversions, not in the kernel.
 //
 // Each function takes its Python counterpart's arguments in order, then the
 // stream's handle and the current device's index, and returns the entry
@@ -19,7 +20,7 @@ namespace {
 PyTypeObject* g_tensor;   // torch.Tensor
 PyTypeObject* g_tiles;    // Fp8Tiles
 PyTypeObject* g_list;     // TensorList
-PyObject *g_get_device, *g_nbytes, *g_is_contiguous, *g_data_ptr, *g_tensors, *g_array, *g_places, *g_where;
+PyObject *g_get_device, *g_nbytes, *g_is_contiguous, *g_data_ptr, *g_tensors, *g_array, *g_places, *g_where, *g_apart;
 PyObject* g_where_is;      // torch.Tensor.data_ptr
 
 decltype(&amp_rmsnorm) g_rmsnorm;
@@ -269,7 +270,7 @@ PyObject* clip_list(PyObject*, PyObject* const* v, Py_ssize_t n) {
   const amp_tensor *grads = a.list(0, count), *outs = a.list(1, as_many);
   const amp_scaler_state* state = a.mem<amp_scaler_state>(2, sizeof(amp_scaler_state));
   const float* coef = a.mem<float>(3, 4);
-  if (!grads || (outs && as_many != count)) Py_RETURN_NONE;
+  if (!grads || (outs && as_many != count) || a.ask(v[outs ? 1 : 0], g_apart, false) != 1) Py_RETURN_NONE;
   AMP_CALL(g_clip_list(grads, outs, count, state, coef, stream));
 }
 
@@ -329,5 +330,6 @@ PyMODINIT_FUNC PyInit__quick(void) {
   g_array = PyUnicode_InternFromString("array");
   g_places = PyUnicode_InternFromString("places");
   g_where = PyUnicode_InternFromString("where");
+  g_apart = PyUnicode_InternFromString("apart");
   return PyModule_Create(&g_module);
 }

@@ -148,3 +148,23 @@ def test_lists_that_do_not_fit_are_refused():
     with pytest.raises(ValueError, match="tensor 0 is of type 3"):
         amp.TensorList([(a, 100, amp.E4M3)])
     assert len(amp.TensorList([])) == 0
+
+
+def test_lists_that_are_written_to_hold_no_memory_twice():
+    a, b = torch.zeros(100), torch.zeros(100)
+    twice, over = [(a, 100, amp.F32), (a, 100, amp.F32)], [(a, 100, amp.F32), (a[99:], 1, amp.F32)]
+    for entries in (twice, over):
+        some = amp.TensorList(entries)
+        with pytest.raises(ValueError, match="tensors of grads overlap"):
+            amp.amp_grad_clip_list(some)
+        with pytest.raises(ValueError, match="tensors of outs overlap"):
+            amp.amp_grad_clip_list(amp.TensorList([(b, e[1], amp.F32) for e in entries]), some)
+    assert amp.TensorList([(a[50:], 50, amp.F32), (a, 50, amp.F32), (a, 0, amp.F32)]).apart
+
+
+def test_lists_of_elements_with_gaps_are_refused():
+    a = torch.zeros(8, 8)
+    for t in (a[:, :4], a[::2]):
+        with pytest.raises(ValueError, match="tensor 1's elements are not one after another"):
+            amp.TensorList([(a, 64, amp.F32), (t, 32, amp.F32)])
+    assert len(amp.TensorList([(a.t(), 64, amp.F32), (a[:4], 32, amp.F32), (a[:, :1], 0, amp.F32)])) == 3
