@@ -6,15 +6,23 @@
 //   backward     dg, du of dy from g, u formed again           (kOutGrad)
 //   gradients    dx = [dg | du] W,  dW = [dg | du]^T x         (kOutC)
 //
-// A block of four waves (2 x 2) owns an output tile of 64 MB x 64 NB (columns
-// of both projections together: a wave's first NB/2 blocks of 32 columns are
-// gate columns, the others the up columns of the same features, so that a
-// lane's accumulators pair up with no exchange).  The summed dimension advances
-// 32 elements at a time through three LDS stages, filled by direct loads two
-// steps ahead, while this step's fragments feed the 32x32x16 instruction.  Two
-// blocks share a CU: one's prologue and epilogue run under the other's products.
-// Operands are contiguous along the summed dimension (KC) or along their rows
-// of outputs (then read with transposing LDS reads).
+// A block of four waves (2 x 2) owns an output tile of 64 MB x 64 NB (columns of
+// both projections together: a wave's first NB/2 blocks of 32 columns are gate
+// columns, the others the up columns of the same features, so that a lane's
+// accumulators pair up with no exchange).  The summed dimension advances 64
+// elements at a time through a ring of LDS slots that direct loads fill up to D
+// steps ahead, one load for each row of 32x32x16 products, with one meeting of the
+// block a step.  Operands are contiguous along the summed dimension (KC) or along
+// their rows of outputs (then read with transposing LDS reads).
+//
+// Bound by the matrix cores from a few hundred tokens on.  A 256 x 256 tile needs
+// half the LDS reads and a quarter of the loads of a 128 x 128 tile a product, which
+// is worth more than a second block on the CU (8192 x 4096 x 14336 BF16 with [g | u]
+// kept: 1445 us, so 2021 us); 128 x 128 tiles, two to a CU, are for outputs of fewer
+// large tiles than CUs and short sums.  At that size the K loop runs at 89 % of the
+// matrix cores' rate, the tiles' ends cost 11 us of a CU each (of 106), and the last
+// round leaves 6 % of the machine idle; 1.33 PFLOP/s where a library product of the
+// same operands, without gate or second output, reaches 1.5.
 //
 // Edges.  Output rows and columns past the end are read from the last valid
 // one (their results are not stored), so no load leaves the operand.  What
@@ -732,7 +740,8 @@ hipError_t launch_gate(const ProductArgs& g, hipStream_t s) {
   const double weights = 4.0 * static_cast<double>(g.N) * static_cast<double>(g.K) / kStream;
   const double t_few = std::max(static_cast<double>(ceil_div(few, 512)) * (kTurnFew * ceil_div(g.K, kFewWaves * kFewTurn) + kBlockFew),
                                 static_cast<double>(groups) * weights);
-  if (groups == 1 || (groups <= 8 && small <= 256 && t_few < std::max(t_small, weights))) {
+  // (a launch counts fewer than 2^32 threads)
+  if (few < (int64_t(1) << 22) && (groups == 1 || (groups <= 8 && small <= 256 && t_few < std::max(t_small, weights)))) {
     const dim3 grid(static_cast<unsigned>(ceil_div(g.N, 16)), static_cast<unsigned>(groups));
     const bool whole = aligned(g.A, 16) && aligned(g.B, 16) && g.lda % 8 == 0 && g.ldb % 8 == 0;
     if (whole) gate_few<ET, OUT, true><<<grid, kFewWaves * 64, 0, s>>>(g);

@@ -163,6 +163,39 @@ def test_backward_of_no_tokens_or_features(t):
     assert not dx.codes().any()
 
 
+# more tokens than the kernel for few of them takes, in tiles that hold little
+TILE_SHAPES = [(129, 1, 1), (130, 17, 1000), (144, 130, 72), (257, 40, 7), (161, 64, 192), (400, 9, 65)]
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("pad", [0, 8, 3])
+@pytest.mark.parametrize("M,Fn,K", TILE_SHAPES)
+def test_small_tiles(M, Fn, K, pad, t):
+    run_forward(M, Fn, K, t, pad, Hollow)
+    run_backward(M, Fn, K, t, pad, False, t, Hollow)
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("M,Fn,K", [(1, 300, 2050), (18, 130, 4161), (128, 33, 1025), (100, 100, 63)])
+def test_few_tokens_recomputed(M, Fn, K, t):
+    """The last waves' turns past the end of the summed dimension, groups of 16 tokens that are not full."""
+    for pad in (0, 3):
+        run_forward(M, Fn, K, t, pad, Hollow)
+        run_backward(M, Fn, K, t, pad, False, amp.F32, Hollow)
+
+
+def test_one_token_of_the_most_features():
+    """F = 2^26 with K = 1: y of every feature is that of its own two weights."""
+    Fn = 1 << 26
+    w = torch.randint(-300, 300, (2 * Fn, 1), device="cuda").float().div_(64).to(torch.bfloat16)
+    x, y = torch.ones(1, 1, dtype=torch.bfloat16, device="cuda"), torch.full((1, Fn), float("nan"), dtype=torch.bfloat16, device="cuda")
+    amp.amp_gemm_swiglu(1, Fn, 1, x, amp.BF16, 1, w, 1, y, Fn)
+    at = torch.cat([torch.randint(0, Fn, (4000,), device="cuda"), torch.tensor([0, Fn // 2, Fn - 1], device="cuda")])
+    g, u = (w[i, 0].double().cpu().numpy() for i in (at, Fn + at))
+    check_values(y[0, at].double().cpu().numpy(), FMT[amp.BF16], g / (1 + np.exp(-g)) * u, swiglu_err(g, u), "y")
+    assert not torch.isnan(y).any()
+
+
 def rows_and_columns(rng, n):
     return np.unique(np.concatenate([rng.integers(0, n, 24), [0, n - 1, n // 2]]))
 
