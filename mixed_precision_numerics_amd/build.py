@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -81,6 +82,8 @@ def _build_quick() -> None:
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-o", tmp,
            os.path.join(PKG, "pyext", "quick.cpp"), "-I" + os.path.join(ROOT, "include"),
            "-I" + sysconfig.get_paths()["include"]]
+    torch = importlib.util.find_spec("torch")                 # its copy of the DLPack header, if it has one
+    cmd += ["-I" + os.path.join(where, "include") for where in (torch.submodule_search_locations if torch else [])]
     try:
         r = subprocess.run(cmd, capture_output=True, text=True)
         failed = r.stderr if r.returncode else None
