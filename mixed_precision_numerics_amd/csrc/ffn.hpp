@@ -79,15 +79,35 @@ __device__ __forceinline__ f32x16 mfma16(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
 
-// Eight elements from p on of which the first n exist, zeros behind them.
+// Eight elements from p on of which the first n exist, zeros behind them.  The
+// loads of an incomplete piece are under way together, past its end from its
+// first element.
 __device__ __forceinline__ u32x4 ld16_part(const uint16_t* p, int n) {
   if (n >= 8) return *reinterpret_cast<const u32x4_u*>(p);
   u32x4 v = {0u, 0u, 0u, 0u};
+  if (n > 0) {
+    uint32_t e[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (j < n) v[j >> 1] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
+    for (int j = 0; j < 8; ++j) e[j] = p[j < n ? j : 0];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j >> 1] |= (j < n ? e[j] : 0u) << (16 * (j & 1));
+  }
   return v;
 }
+
+// v without its first `by` elements (0 .. 8), zeros behind what is left.
+__device__ __forceinline__ u32x4 without(u32x4 v, int by) {
+  const bool half = by & 1;
+  if (by & 2) v = u32x4{v[1], v[2], v[3], 0u};
+  if (by & 4) v = u32x4{v[2], v[3], 0u, 0u};
+  if (by & 8) v = u32x4{0u, 0u, 0u, 0u};
+  return u32x4{half ? __builtin_amdgcn_alignbit(v[1], v[0], 16) : v[0], half ? __builtin_amdgcn_alignbit(v[2], v[1], 16) : v[1],
+               half ? __builtin_amdgcn_alignbit(v[3], v[2], 16) : v[2], half ? v[3] >> 16 : v[3]};
+}
+
+// How far a piece of which n elements exist is loaded before its place, so as to
+// end with them; `without` of as many puts them there.
+__device__ __forceinline__ int back_of(int n) { return n >= 8 ? 0 : n <= 0 ? 8 : 8 - n; }
 
 // LDS writes of one wave before its own reads of them (and reads before the
 // next writes): a wave's LDS operations complete in order, the compiler has to
@@ -292,43 +312,75 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
     }
   };
 
-  // ---- the same through registers, masked
+  // ---- the same through registers, masked.  Where every step has incomplete pieces
+  // (outputs contiguous), one is loaded as the last whole piece of its row and put
+  // right on its way into LDS: branches would have the loads wait for one another
+  // (gradients of 300 x 1001 x 2047 BF16 38 us, so 35).  Rows of fewer than eight
+  // elements have no whole piece.
   u32x4 ha[kLA], hb[kLB];
+  const bool short_a = !A_KC && g.M < 8, short_b = !B_KC && g.N < 8;
+  auto left_of = [&](int s) __attribute__((always_inline)) {
+    const int64_t left = g.K - first_k(s);
+    return static_cast<int>(left < kStepK ? left : kStepK);
+  };
   auto fetch_a = [&](int s) __attribute__((always_inline)) {
-    const int k0 = first_k(s), n = static_cast<int>(g.K - k0 < kStepK ? g.K - k0 : kStepK);
+    const int k0 = first_k(s), n = left_of(s);
 #pragma unroll
     for (int i = 0; i < kLA; ++i) {
       const int e = t + 256 * i;
       if constexpr (A_KC) {
-        const int r = e >> 3, c = e & 7;
-        ha[i] = ld16_part(A + (r < rows_a ? r : rows_a - 1) * g.lda + k0 + 8 * c, n - 8 * c);
+        const int r = e >> 3, c = 8 * (e & 7);
+        ha[i] = ld16_part(A + (r < rows_a ? r : rows_a - 1) * g.lda + k0 + c, n - c);
       } else {
-        const int k = e / kChA, c = e % kChA;
-        ha[i] = ld16_part(A + static_cast<int64_t>(k0 + k) * g.lda + 8 * c, k < n ? rows_a - 8 * c : 0);
+        const int k = e / kChA, c = 8 * (e % kChA);
+        const uint16_t* p = A + static_cast<int64_t>(k0 + (k < n ? k : n - 1)) * g.lda;
+        ha[i] = short_a ? ld16_part(p + c, k < n ? rows_a - c : 0) : *reinterpret_cast<const u32x4_u*>(p + (c + 8 <= rows_a ? c : rows_a - 8));
       }
     }
   };
   auto fetch_b = [&](int s) __attribute__((always_inline)) {
-    const int k0 = first_k(s), n = static_cast<int>(g.K - k0 < kStepK ? g.K - k0 : kStepK);
+    const int k0 = first_k(s), n = left_of(s);
 #pragma unroll
     for (int i = 0; i < kLB; ++i) {
       const int e = t + 256 * i;
       if constexpr (B_KC) {
-        hb[i] = ld16_part(B + row_b(e >> 3) * g.ldb + k0 + 8 * (e & 7), n - 8 * (e & 7));
+        const int c = 8 * (e & 7);
+        hb[i] = ld16_part(B + row_b(e >> 3) * g.ldb + k0 + c, n - c);
       } else {
-        const int k = e / kChB, c = e % kChB;
-        hb[i] = ld16_part(B + static_cast<int64_t>(k0 + k) * g.ldb + 8 * c, k < n ? rows_b - 8 * c : 0);
+        const int k = e / kChB, c = 8 * (e % kChB);
+        const uint16_t* p = B + static_cast<int64_t>(k0 + (k < n ? k : n - 1)) * g.ldb;
+        hb[i] = short_b ? ld16_part(p + c, k < n ? rows_b - c : 0) : *reinterpret_cast<const u32x4_u*>(p + (c + 8 <= rows_b ? c : rows_b - 8));
       }
     }
   };
-  auto put_a = [&](int slot) __attribute__((always_inline)) {
+  auto put_a = [&](int s, int slot) __attribute__((always_inline)) {
+    if constexpr (!A_KC) {
+      const int n = left_of(s);
+      if (!short_a && (n < kStepK || rows_a < BM)) {
+#pragma unroll
+        for (int i = 0; i < kLA; ++i) {
+          const int e = t + 256 * i;
+          ha[i] = without(ha[i], e / kChA < n ? back_of(rows_a - 8 * (e % kChA)) : 8);
+        }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kLA; ++i) {
       const int e = t + 256 * i;
       *reinterpret_cast<u32x4*>(smem + slot * kSlot + (A_KC ? swz(e >> 3, e & 7) : mn_at(e / kChA, e % kChA, BM * 2))) = ha[i];
     }
   };
-  auto put_b = [&](int slot) __attribute__((always_inline)) {
+  auto put_b = [&](int s, int slot) __attribute__((always_inline)) {
+    if constexpr (!B_KC) {
+      const int n = left_of(s);
+      if (!short_b && (n < kStepK || rows_b < BN)) {
+#pragma unroll
+        for (int i = 0; i < kLB; ++i) {
+          const int e = t + 256 * i;
+          hb[i] = without(hb[i], e / kChB < n ? back_of(rows_b - 8 * (e % kChB)) : 8);
+        }
+      }
+    }
 #pragma unroll
     for (int i = 0; i < kLB; ++i) {
       const int e = t + 256 * i;
@@ -379,9 +431,9 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
   if (s0 < s1) {
     if (!FAST || (tail && s0 == 0)) {
       fetch_a(s0);
-      put_a(0);
+      put_a(s0, 0);
       fetch_b(s0);
-      put_b(1);
+      put_b(s0, 1);
     } else {
 #pragma unroll
       for (int i = 0; i < kLA; ++i) direct_a(s0, 0, i);
@@ -424,8 +476,8 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
     constexpr bool MORE = decltype(next)::value;
     const int sb = after(sa, 1), na = after(sa, 2), nb = after(sa, 3);
     if constexpr (MORE && !FAST) {
-      put_a(na);
-      put_b(nb);
+      put_a(s + 1, na);
+      put_b(s + 1, nb);
       if (s + 2 < s1) {
         fetch_a(s + 2);
         fetch_b(s + 2);
@@ -583,7 +635,7 @@ __device__ __forceinline__ f32x4 mfma16x16(u32x4 a, u32x4 b, f32x4 c) {
 // Eight elements at any 2-byte address from the dwords that hold them, shifted into
 // place (each dword read holds one of the elements: none lies outside the
 // operand's pages).  Waves that only stream would wait for 16-byte loads at odd
-// addresses: 1 x 4097 x 14336 106 us, so 64.
+// addresses: 1 x 4097 x 14336 106 us, so 64 (57 since ld16_part's loads overlap).
 typedef uint32_t u32x4_dw __attribute__((ext_vector_type(4), aligned(4)));
 struct Piece {
   u32x4 w;
