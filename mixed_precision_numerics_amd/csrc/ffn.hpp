@@ -29,7 +29,8 @@
 // does not fill a step of the summed dimension is put into LDS through
 // registers, masked with zeros on both sides (a NaN behind a row's end must
 // not meet a zero), as the first step of a tile.  Operands without 16-byte
-// rows go that way in every step (FAST == false).
+// rows go that way in every step (FAST == false), where loads that are not
+// 16-byte aligned bound them: 1000 x 4097 x 14336 385 us against 190 for 4096.
 #pragma once
 #include <algorithm>
 #include <type_traits>
@@ -315,7 +316,7 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
   // ---- the same through registers, masked.  Where every step has incomplete pieces
   // (outputs contiguous), one is loaded as the last whole piece of its row and put
   // right on its way into LDS: branches would have the loads wait for one another
-  // (gradients of 300 x 1001 x 2047 BF16 38 us, so 35).  Rows of fewer than eight
+  // (gradients of 300 x 2047 x 1001 BF16 38 us, so 35).  Rows of fewer than eight
   // elements have no whole piece.
   u32x4 ha[kLA], hb[kLB];
   const bool short_a = !A_KC && g.M < 8, short_b = !B_KC && g.N < 8;
@@ -469,9 +470,9 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
 
   // One step, slots sa and sa + 1: four slices of 16, a slice's products row by
-  // row, between them the next slice's fragments and the loads.  The block meets once, after the last slice's first row: the next step
-  // has landed, and every wave has its last fragments of this one.  The compiler
-  // keeps to this order.
+  // row, between them the next slice's fragments and the loads.  The block meets
+  // once, after the last slice's first row: the next step has landed, and every wave
+  // has its last fragments of this one.  The compiler keeps to this order.
   auto step = [&](int s, int sa, auto next) __attribute__((always_inline)) {
     constexpr bool MORE = decltype(next)::value;
     const int sb = after(sa, 1), na = after(sa, 2), nb = after(sa, 3);
@@ -735,7 +736,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void gate_few(ProductArgs g) {
   }
 }
 
-// Both projections with their gate.
+// Both projections with their gate.  1000 x 4096 x 14336 BF16 188 us (1.25 PFLOP/s),
+// 33 x 5120 x 20480 92 us (4.6 TB/s of weights; 320 tiles of 128 x 128).
 template <int ET, int OUT, int MB, int NB, int D, bool FAST>
 __global__ __launch_bounds__(256, MB * NB > 8 || D > 2 ? 1 : 2) void gate_tiles(ProductArgs g) {
   __shared__ __align__(16) uint8_t smem[lds_bytes(MB, NB, D)];
@@ -743,7 +745,8 @@ __global__ __launch_bounds__(256, MB * NB > 8 || D > 2 ? 1 : 2) void gate_tiles(
 }
 
 // The two gradient products in one launch, that of the longer sums first: the
-// blocks of one fill what the other leaves of the machine.  nx: blocks of dx.
+// blocks of one fill what the other leaves of the machine (8192 x 4096 x 14336 BF16,
+// both 256 x 256: 2850 us for 3.85 TFLOP).  nx: blocks of dx.
 template <int ET, int MB, int NB, bool FAST>
 __global__ __launch_bounds__(256, MB * NB > 8 ? 1 : 2) void gradient_tiles(ProductArgs gx, ProductArgs gw, uint32_t nx, uint32_t nw, int dx_first) {
   __shared__ __align__(16) uint8_t smem[lds_bytes(MB, NB, 2)];
