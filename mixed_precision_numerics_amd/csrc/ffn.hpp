@@ -16,7 +16,7 @@
 // their rows of outputs (then read with transposing LDS reads).
 //
 // Bound by the matrix cores from a few hundred tokens on.  A 256 x 256 tile needs
-// half the LDS reads and a quarter of the loads of a 128 x 128 tile a product, which
+// half the LDS reads and half the loads of a 128 x 128 tile a product, which
 // is worth more than a second block on the CU (8192 x 4096 x 14336 BF16 with [g | u]
 // kept: 1445 us against 2021); 128 x 128 tiles, two to a CU, are for outputs of fewer
 // large tiles than CUs and short sums.  At that size the K loop runs at 89 % of the
