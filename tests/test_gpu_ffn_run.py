@@ -251,3 +251,34 @@ def test_results_do_not_change_from_call_to_call():
         s.run()
         for a, b in zip(s.results(), first):
             assert torch.equal(a, b)
+
+
+def test_operands_that_are_views_or_parameters():
+    """Rows of larger tensors, a strided view, a parameter, a row whose one-element dimension has any stride."""
+    M, Fn, K, b, tt = 7, 40, 64, amp.BF16, torch.bfloat16
+    g = torch.Generator(device="cuda").manual_seed(9)
+
+    def normal(*s):
+        return torch.randn(*s, generator=g, device="cuda").to(tt)
+    big, w, wide = normal(M + 5, K), normal(2 * Fn, K), normal(M, 2 * K)
+    want, got = torch.empty(M, Fn, dtype=tt, device="cuda"), torch.full((M + 2, Fn), float("nan"), dtype=tt, device="cuda")
+    amp.amp_gemm_swiglu(M, Fn, K, big[3:3 + M].clone(), b, K, w, K, want, Fn)
+    amp.amp_gemm_swiglu(M, Fn, K, big[3:3 + M], b, K, torch.nn.Parameter(w), K, got[1:1 + M], Fn)
+    assert torch.equal(got[1:1 + M], want) and torch.isnan(got[[0, M + 1]]).all()
+    amp.amp_gemm_swiglu(M, Fn, K, wide[:, K:].contiguous(), b, K, w, K, want, Fn)
+    amp.amp_gemm_swiglu(M, Fn, K, wide[:, K:], b, 2 * K, w, K, got[1:1 + M], Fn)
+    assert torch.equal(got[1:1 + M], want)
+    amp.amp_gemm_swiglu(1, Fn, K, big[:1].clone(), b, K, w, K, want, Fn)
+    amp.amp_gemm_swiglu(1, Fn, K, big.as_strided((1, K, 1), (12345, 1, 777)), b, K, w, K, got[1:2], Fn)
+    assert torch.equal(got[1:2], want[:1])
+    with pytest.raises(ValueError, match="x holds"):
+        amp.amp_gemm_swiglu(M, Fn, K, big[6:], b, K, w, K, want, Fn)
+    n = torch.nn.Parameter(torch.full((33,), 2.0, device="cuda"))
+    st, ns, out = empty(40), empty(amp.NORM_STATE_BYTES), torch.zeros(2, device="cuda")
+    amp.amp_scaler_init(st, 1.0)
+    some = amp.TensorList([(n, 33, amp.F32), (torch.ones(4, device="cuda")[1:], 3, amp.F32)])
+    amp.amp_grad_norm_list(some, True, st, ns, 1.0, out)
+    assert host(ns, np.float64)[0] == 33 * 4 + 3
+    n.data = torch.zeros(33, device="cuda")
+    with pytest.raises(ValueError, match="has moved"):
+        amp.amp_grad_norm_list(some, True, st, ns, 1.0, out)
