@@ -113,8 +113,8 @@ class TensorList:
     Made once, e.g. beside a model's parameters, and passed to every step.
     Tensors are kept alive; each has to hold its elements one after another on
     one GPU, checked here, and has to stay where it was: a call with a list of
-    which one was resized or given other storage is refused.  A list that is
-    written to names no memory twice."""
+    which one lies elsewhere, or in less memory than its elements take, is
+    refused.  A list that is written to names no memory twice."""
 
     def __init__(self, entries):
         entries = list(entries)
@@ -136,6 +136,7 @@ class TensorList:
                 elif self.where != t.get_device():
                     raise ValueError(f"TensorList: tensor {i} is on {t.device}, others are not")
         self.places = [t.data_ptr() for t in self.tensors]
+        self.bytes = [_vec(n, dtype) for t, n, dtype in entries if n > 0 and hasattr(t, "get_device")]
         spans = sorted((a.p, a.p + _vec(a.n, a.type)) for a in self.array if a.n > 0 and a.p)
         self.apart = all(one[1] <= two[0] for one, two in zip(spans, spans[1:]))     # may be written to
 
@@ -616,11 +617,14 @@ def amp_gemm_swiglu_backward(M, F, K, dy, t, lddy, x, ldx, w, ldw, gu, ldgu, dgu
 
 
 def _listed(fn: str, what: str, ts: TensorList | None, at: list) -> int | None:
-    """Address of a list's array; a tensor that has moved is refused."""
+    """Address of a list's array; a tensor that has moved, or whose memory is less
+    than it was, is refused."""
     if ts is None:
         return None
     if [t.data_ptr() for t in ts.tensors] != ts.places:
         raise ValueError(f"{fn}: a tensor of {what} has moved since the TensorList was made from it")
+    for t, need in zip(ts.tensors, ts.bytes):
+        _room(fn, f"a tensor of {what}", t, need)
     if ts.tensors and ts.where != at[0]:
         at.append(f"{what} is on {ts.tensors[0].device}")
     return ctypes.addressof(ts.array)

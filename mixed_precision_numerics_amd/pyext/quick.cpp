@@ -23,7 +23,7 @@ namespace {
 PyTypeObject* g_tensor;   // torch.Tensor
 PyTypeObject* g_tiles;    // Fp8Tiles
 PyTypeObject* g_list;     // TensorList
-PyObject *g_get_device, *g_nbytes, *g_is_contiguous, *g_data_ptr, *g_tensors, *g_array, *g_places, *g_where, *g_apart;
+PyObject *g_get_device, *g_nbytes, *g_is_contiguous, *g_data_ptr, *g_tensors, *g_array, *g_places, *g_bytes, *g_where, *g_apart;
 PyObject* g_where_is;      // torch.Tensor.data_ptr
 
 typedef __int128 wide;
@@ -46,10 +46,14 @@ bool view(PyObject* t, DLTensor& v) {
   PyErr_Clear();
   return false;
 }
-bool place(PyObject* t, uint64_t& p) {
+wide bytes_per(const DLTensor& v) { return (static_cast<wide>(v.dtype.bits) * v.dtype.lanes + 7) / 8; }
+// A tensor's address and the bytes of its elements.
+bool place(PyObject* t, uint64_t& p, wide& bytes) {
   DLTensor v;
   if (!view(t, v)) return false;
   p = reinterpret_cast<uint64_t>(v.data) + v.byte_offset;
+  bytes = bytes_per(v);
+  for (int32_t i = 0; i < v.ndim; ++i) bytes *= v.shape[i];
   return true;
 }
 // Whether t is contiguous, on GPU dev and holds `need` bytes; its address.
@@ -62,13 +66,13 @@ Look look(PyObject* t, int64_t dev, wide need, void*& p) {
     if (v.strides && v.shape[i] != 1 && v.strides[i] != n) return kOther;      // (an empty tensor may count as one with gaps)
     n *= v.shape[i];
   }
-  if (n * ((static_cast<wide>(v.dtype.bits) * v.dtype.lanes + 7) / 8) < need) return kOther;
+  if (n * bytes_per(v) < need) return kOther;
   p = static_cast<char*>(v.data) + v.byte_offset;
   return kPlain;
 }
 #else
 void bind_view() {}
-bool place(PyObject*, uint64_t&) { return false; }
+bool place(PyObject*, uint64_t&, wide&) { return false; }
 Look look(PyObject*, int64_t, wide, void*&) { return kUnseen; }
 #endif
 
@@ -161,15 +165,17 @@ struct Args {
     Py_DECREF(qs);
     return ok ? &t : nullptr;
   }
-  // The array of a TensorList whose tensors are where they were.
+  // The array of a TensorList whose tensors are where they were and still hold the
+  // elements.
   const amp_tensor* list(int i, int32_t& count) {
     PyObject* o = v[i];
     count = 0;
     if (!ok || o == Py_None) return nullptr;
-    PyObject *a = nullptr, *ts = nullptr, *at = nullptr;
+    PyObject *a = nullptr, *ts = nullptr, *at = nullptr, *bs = nullptr;
     Py_buffer b{};
     if (!PyObject_TypeCheck(o, g_list) || !(a = PyObject_GetAttr(o, g_array)) || !(ts = PyObject_GetAttr(o, g_tensors)) ||
-        !(at = PyObject_GetAttr(o, g_places)) || !PyList_Check(ts) || !PyList_Check(at) || PyList_GET_SIZE(ts) != PyList_GET_SIZE(at) ||
+        !(at = PyObject_GetAttr(o, g_places)) || !(bs = PyObject_GetAttr(o, g_bytes)) || !PyList_Check(ts) || !PyList_Check(at) ||
+        !PyList_Check(bs) || PyList_GET_SIZE(ts) != PyList_GET_SIZE(at) || PyList_GET_SIZE(ts) != PyList_GET_SIZE(bs) ||
         PyObject_GetBuffer(a, &b, PyBUF_SIMPLE) != 0)
       ok = false;
     const amp_tensor* p = ok ? static_cast<const amp_tensor*>(b.buf) : nullptr;
@@ -178,10 +184,13 @@ struct Args {
     for (Py_ssize_t k = 0; ok && k < PyList_GET_SIZE(ts); ++k) {
       PyObject* t = PyList_GET_ITEM(ts, k);
       uint64_t p;
+      wide bytes;
       if (!PyObject_TypeCheck(t, g_tensor)) {
         ok = false;
-      } else if (place(t, p)) {
-        ok = static_cast<int64_t>(p) == num(PyList_GET_ITEM(at, k)) && ok;
+      } else if (place(t, p, bytes)) {
+        ok = static_cast<int64_t>(p) == num(PyList_GET_ITEM(at, k)) && bytes >= num(PyList_GET_ITEM(bs, k)) && ok;
+      } else if (ask(t, g_nbytes, false) < num(PyList_GET_ITEM(bs, k))) {
+        ok = false;
       } else {
         PyObject* r = PyObject_Vectorcall(g_where_is, &t, 1, nullptr);
         ok = r && num(r) == num(PyList_GET_ITEM(at, k)) && ok;
@@ -193,6 +202,7 @@ struct Args {
     Py_XDECREF(a);                     // the list keeps its array
     Py_XDECREF(ts);
     Py_XDECREF(at);
+    Py_XDECREF(bs);
     return ok ? p : nullptr;
   }
 };
@@ -386,6 +396,7 @@ PyMODINIT_FUNC PyInit__quick(void) {
   g_tensors = PyUnicode_InternFromString("tensors");
   g_array = PyUnicode_InternFromString("array");
   g_places = PyUnicode_InternFromString("places");
+  g_bytes = PyUnicode_InternFromString("bytes");
   g_where = PyUnicode_InternFromString("where");
   g_apart = PyUnicode_InternFromString("apart");
   return PyModule_Create(&g_module);
