@@ -716,7 +716,8 @@ int amp_grad_norm_list(const amp_tensor* grads, int32_t count, int first,
  * outs: count tensors of the same lengths, each of any of the three types; NULL
  * or tensors that are the gradients themselves (same p and type): in place,
  * where a factor of exactly 1 leaves the tensor as it is.  No other overlap of
- * an output with any tensor of the call is allowed. */
+ * an output with any tensor of the call is allowed (AMP_EINVAL for one with the
+ * gradient of its own place; the Python binding refuses all). */
 int amp_grad_clip_list(const amp_tensor* grads, const amp_tensor* outs, int32_t count,
                        const amp_scaler_state* d_state, const float* d_coef, void* stream);
 

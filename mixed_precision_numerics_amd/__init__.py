@@ -12,8 +12,10 @@ library is missing or no gfx950 device is current, the calls raise.
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import importlib.util
+import itertools
 import os
 import warnings
 
@@ -114,7 +116,10 @@ class TensorList:
     Tensors are kept alive; each has to hold its elements one after another on
     one GPU, checked here, and has to stay where it was: a call with a list of
     which one lies elsewhere, or in less memory than its elements take, is
-    refused.  A list that is written to names no memory twice."""
+    refused.  A list that is written to names no memory twice, and none of
+    another tensor that the call reads."""
+
+    _serials = itertools.count()
 
     def __init__(self, entries):
         entries = list(entries)
@@ -139,9 +144,28 @@ class TensorList:
         self.bytes = [_vec(n, dtype) for t, n, dtype in entries if n > 0 and hasattr(t, "get_device")]
         spans = sorted((a.p, a.p + _vec(a.n, a.type)) for a in self.array if a.n > 0 and a.p)
         self.apart = all(one[1] <= two[0] for one, two in zip(spans, spans[1:]))     # may be written to
+        self.serial, self.beside = next(TensorList._serials), set()    # beside: serials of lists known to be clear of this one
 
     def __len__(self):
         return len(self.array)
+
+    def clear_of(self, grads) -> bool:
+        """Whether these tensors, none over another, can be written while ``grads``
+        are read: each lies over none of them, or is the one of its own place (same
+        address and type).  Found out once for a pair of lists."""
+        if grads.serial in self.beside:
+            return True
+        outs = sorted((a.p, a.p + _vec(a.n, a.type), i) for i, a in enumerate(self.array) if a.n > 0 and a.p)
+        starts = [o[0] for o in outs]
+        for i, g in enumerate(grads.array):
+            if g.n > 0 and g.p:
+                k = bisect.bisect_left(starts, g.p + _vec(g.n, g.type)) - 1      # the last that begins before its end
+                if k >= 0 and outs[k][1] > g.p and not (outs[k][2] == i and outs[k][0] == g.p and self.array[i].type == g.type):
+                    return False
+        if len(self.beside) >= 64:
+            self.beside.clear()
+        self.beside.add(grads.serial)
+        return True
 
 
 _P, _I, _I64, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64
@@ -654,8 +678,11 @@ def amp_grad_clip_list(grads: TensorList, outs: TensorList | None = None, d_stat
     if not (grads if outs is None else outs).apart:
         raise ValueError(f"{f}: tensors of {'grads' if outs is None else 'outs'} overlap")
     at = _where()
+    where = _listed(f, "grads", grads, at), _listed(f, "outs", outs, at)
+    if outs is not None and not outs.clear_of(grads):
+        raise ValueError(f"{f}: a tensor of outs lies over one of grads that is not its own")
     _check(f, load().amp_grad_clip_list(
-        _listed(f, "grads", grads, at), _listed(f, "outs", outs, at), len(grads),
+        *where, len(grads),
         _mem(f, "d_state", d_state, SCALER_STATE_DTYPE.itemsize, at), _mem(f, "d_coef", d_coef, 4, at),
         _ready(f, stream, at)))
 

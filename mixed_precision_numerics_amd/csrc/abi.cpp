@@ -90,7 +90,11 @@ int list_status(const amp_tensor* a, const amp_tensor* outs, int32_t count) {
     if (a[i].n == 0) continue;
     for (const amp_tensor* t : {a + i, outs ? outs + i : a + i})
       if (!t->p || !al(t->p, t->type == AMP_F32 ? 4 : 2)) return AMP_EINVAL;
-    if (outs && outs[i].p == a[i].p && outs[i].type != a[i].type) return AMP_EINVAL;
+    if (!outs) continue;
+    // an output is its own gradient's place or lies clear of it
+    const uintptr_t g = reinterpret_cast<uintptr_t>(a[i].p), o = reinterpret_cast<uintptr_t>(outs[i].p);
+    const uintptr_t n = static_cast<uintptr_t>(a[i].n), ge = n * (a[i].type == AMP_F32 ? 4 : 2), oe = n * (outs[i].type == AMP_F32 ? 4 : 2);
+    if (g == o ? outs[i].type != a[i].type : (g < o ? o - g < ge : g - o < oe)) return AMP_EINVAL;
   }
   return AMP_OK;
 }

@@ -23,7 +23,7 @@ namespace {
 PyTypeObject* g_tensor;   // torch.Tensor
 PyTypeObject* g_tiles;    // Fp8Tiles
 PyTypeObject* g_list;     // TensorList
-PyObject *g_get_device, *g_nbytes, *g_is_contiguous, *g_data_ptr, *g_tensors, *g_array, *g_places, *g_bytes, *g_where, *g_apart;
+PyObject *g_get_device, *g_nbytes, *g_is_contiguous, *g_data_ptr, *g_tensors, *g_array, *g_places, *g_bytes, *g_where, *g_apart, *g_serial, *g_beside;
 PyObject* g_where_is;      // torch.Tensor.data_ptr
 
 typedef __int128 wide;
@@ -205,6 +205,15 @@ struct Args {
     Py_XDECREF(bs);
     return ok ? p : nullptr;
   }
+  // Whether the lists are known to lie clear of each other (TensorList.clear_of).
+  static bool beside(PyObject* outs, PyObject* grads) {
+    PyObject *known = PyObject_GetAttr(outs, g_beside), *serial = PyObject_GetAttr(grads, g_serial);
+    const bool yes = known && serial && PySet_Check(known) && PySet_Contains(known, serial) == 1;
+    Py_XDECREF(known);
+    Py_XDECREF(serial);
+    PyErr_Clear();
+    return yes;
+  }
 };
 
 #define AMP_OPEN(count)                                                            \
@@ -337,6 +346,7 @@ PyObject* clip_list(PyObject*, PyObject* const* v, Py_ssize_t n) {
   const amp_scaler_state* state = a.mem<amp_scaler_state>(2, sizeof(amp_scaler_state));
   const float* coef = a.mem<float>(3, 4);
   if (!grads || (outs && as_many != count) || a.ask(v[outs ? 1 : 0], g_apart, false) != 1) Py_RETURN_NONE;
+  if (outs && !a.beside(v[1], v[0])) Py_RETURN_NONE;
   AMP_CALL(g_clip_list(grads, outs, count, state, coef, stream));
 }
 
@@ -399,5 +409,7 @@ PyMODINIT_FUNC PyInit__quick(void) {
   g_bytes = PyUnicode_InternFromString("bytes");
   g_where = PyUnicode_InternFromString("where");
   g_apart = PyUnicode_InternFromString("apart");
+  g_serial = PyUnicode_InternFromString("serial");
+  g_beside = PyUnicode_InternFromString("beside");
   return PyModule_Create(&g_module);
 }

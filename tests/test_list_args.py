@@ -58,3 +58,80 @@ def test_a_tensor_that_shrank_within_its_memory_is_taken():
     assert amp._listed("f", "grads", some, [-1])
     t.resize_(100)
     assert amp._listed("f", "grads", some, [-1])
+
+
+def both(entries, outs):
+    return amp.TensorList(entries), amp.TensorList(outs)
+
+
+def overlaps():
+    """Outputs over gradients that other blocks still read: swapped, shifted, of another type, of another length, of a gradient named twice."""
+    a, b = torch.zeros(100), torch.zeros(1000)
+    h = a.view(torch.bfloat16)
+    yield both([(a[:50], 50, amp.F32), (a[50:], 50, amp.F32)], [(a[50:], 50, amp.F32), (a[:50], 50, amp.F32)])
+    yield both([(a[1:], 99, amp.F32)], [(a, 99, amp.F32)])
+    yield both([(a, 99, amp.F32)], [(a[1:], 99, amp.F32)])
+    yield both([(h[:100], 100, amp.BF16)], [(a, 100, amp.F32)])
+    yield both([(a[:50], 50, amp.F32), (b, 10, amp.F32)], [(b[500:], 50, amp.F32), (a[49:], 10, amp.F32)])
+    yield both([(a, 100, amp.F32), (a[7:], 1, amp.F32)], [(a, 100, amp.F32), (b, 1, amp.F32)])
+    yield both([(b[k:], 9, amp.F32) for k in range(0, 900, 10)] + [(a, 7, amp.F32)],
+               [(a[8:], 9, amp.F32)] + [(torch.zeros(9), 9, amp.F32) for _ in range(89)] + [(b[898:], 7, amp.F32)])
+
+
+@pytest.mark.parametrize("which", range(7))
+def test_outputs_over_gradients_that_are_not_their_own_are_refused(quick, which):
+    grads, outs = list(overlaps())[which]
+    for _ in range(2):
+        with pytest.raises(ValueError, match="lies over one of grads"):
+            amp.amp_grad_clip_list(grads, outs)
+        assert quick.clip_list(grads, outs, None, None, 0, -1) is None
+
+
+def test_outputs_beside_or_in_place_of_their_gradients_are_taken(quick):
+    a, b = torch.zeros(100), torch.zeros(90)
+    flat = [(a[k:], 10, amp.F32) for k in range(0, 100, 10)]
+    grads = amp.TensorList(flat)
+    mixed = amp.TensorList([e if i % 2 else (b[10 * (i // 2):], 10, amp.F32) for i, e in enumerate(flat)])
+    twice = amp.TensorList([(a, 100, amp.F32), (a, 100, amp.F32)])          # (read only)
+    apart = amp.TensorList([(torch.zeros(100), 100, amp.F32) for _ in range(2)])
+    empty = amp.TensorList([(a, 0, amp.F32)])
+    for g, o in ((grads, grads), (grads, mixed), (grads, amp.TensorList(flat)), (twice, apart)):
+        with pytest.raises(ValueError, match="on cpu"):
+            amp.amp_grad_clip_list(g, o)
+        assert o.clear_of(g) and g.serial in o.beside
+    assert empty.clear_of(grads) and grads.clear_of(empty)
+    # known to be clear, the pair is the compiled module's: a NULL gradient of one element is what the library refuses
+    null = [(0, 1, amp.F32)]
+    g, o = both(null, null)
+    assert quick.clip_list(g, o, None, None, 0, -1) is None and o.clear_of(g)
+    assert quick.clip_list(g, o, None, None, 0, -1) == EINVAL
+
+
+def test_pairs_of_many_lists_are_not_kept_for_good():
+    a, o = torch.zeros(4), amp.TensorList([(torch.zeros(4), 4, amp.F32)])
+    for _ in range(200):
+        g = amp.TensorList([(a, 4, amp.F32)])
+        assert o.clear_of(g) and o.clear_of(g)
+    assert len(o.beside) <= 64
+
+
+@pytest.mark.parametrize("gt,g,n,ot,o", [(amp.F32, 4096, 10, amp.F32, 4100), (amp.F32, 4100, 10, amp.F32, 4096), (amp.BF16, 4096, 10, amp.F32, 4112),
+                                         (amp.BF16, 4132, 10, amp.F32, 4096), (amp.F32, 4096, 10, amp.BF16, 4134)])
+def test_the_library_refuses_an_output_that_its_own_gradient_runs_into(gt, g, n, ot, o):
+    arr, out = (amp._Tensor * 1)(), (amp._Tensor * 1)()
+    for a, p, t in ((arr[0], g, gt), (out[0], o, ot)):
+        a.p, a.n, a.type = p, n, t
+    f = amp.load().amp_grad_clip_list
+    assert f(amp.ctypes.addressof(arr), amp.ctypes.addressof(out), 1, None, None, None) == EINVAL
+
+
+@pytest.mark.parametrize("gt,g,n,ot,o", [(amp.F32, 4096, 10, amp.F32, 4136), (amp.F32, 4136, 10, amp.F32, 4096), (amp.BF16, 4096, 10, amp.F32, 4116),
+                                         (amp.BF16, 4136, 10, amp.F32, 4096), (amp.F32, 4096, 10, amp.BF16, 4136), (amp.F16, 4096, 10, amp.F16, 4096)])
+def test_the_library_takes_neighbours(gt, g, n, ot, o):
+    """Seen from the order of its checks: a tensor behind them is of no supported type."""
+    arr, out = (amp._Tensor * 2)(), (amp._Tensor * 2)()
+    for a, p, t in ((arr[0], g, gt), (out[0], o, ot)):
+        a.p, a.n, a.type = p, n, t
+    arr[1].type = out[1].type = amp.E4M3
+    f = amp.load().amp_grad_clip_list
+    assert f(amp.ctypes.addressof(arr), amp.ctypes.addressof(out), 2, None, None, None) == -2
