@@ -531,8 +531,10 @@ int amp_requantize_blockwise(const amp_fp8_tiles* x, int64_t rows, int64_t cols,
  * exact and summed in FP32, y is formed from the FP32 sums, each result is
  * rounded once.  Any size, row stride and 2-byte alignment; rows that are 16-byte
  * aligned (pointers, strides % 8 == 0 and, in the backward pass, F % 4 == 0 and
- * K % 8 == 0) are the fast ones.  No output may overlap an input or another
- * output, but for dgu and gu as said below.  K and F are at most 2^26 and a
+ * K % 8 == 0) are the fast ones.  No output may overlap an input, another
+ * output or the work area, but for dgu and gu as said below (AMP_EINVAL, unless
+ * both matrices have gaps between their rows and different strides: those are not
+ * compared).  K and F are at most 2^26 and a
  * product may have at most 2^22 tiles of 128 x 128 (else AMP_EUNSUPPORTED). */
 
 /* amp_gemm_swiglu -- the forward pass.  Of few tokens (one token included) the

@@ -79,6 +79,50 @@ bool block_sizes(int64_t M, int64_t F, int64_t K) {
   return m * (f > k ? f : k) <= most && f * k <= most;
 }
 
+// Where a matrix operand lies: `rows` rows of `width` bytes, `pitch` bytes apart.
+struct Place {
+  const void* p;
+  int64_t rows;
+  __int128 width, pitch;
+};
+Place place_of(const void* p, int64_t rows, int64_t cols, int64_t ld, int t) {
+  const int bytes = t == AMP_F32 ? 4 : 2;
+  return {p, rows, static_cast<__int128>(cols) * bytes, static_cast<__int128>(ld) * bytes};
+}
+
+// Whether some row of a meets some row of b: exact where one of them has no gaps
+// or both have one pitch.  How the rows of two matrices with gaps of different
+// pitches lie is the caller's to know; they pass.
+bool meet(Place a, Place b) {
+  using wide = __int128;
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+  const wide d = static_cast<wide>(reinterpret_cast<uintptr_t>(b.p)) - static_cast<wide>(reinterpret_cast<uintptr_t>(a.p));
+  const wide ea = (a.rows - 1) * a.pitch + a.width, eb = (b.rows - 1) * b.pitch + b.width;
+  if (d >= ea || -d >= eb) return false;
+  if (a.pitch == a.width) a = {a.p, 1, ea, ea};
+  if (b.pitch == b.width) b = {b.p, 1, eb, eb};
+  if (a.rows == 1 && b.rows == 1) return true;
+  const wide pitch = a.rows > 1 ? a.pitch : b.pitch;
+  if (a.rows > 1 && b.rows > 1 && b.pitch != pitch) return false;
+  // row i of a and row i + k of b meet if  -b.width < d + k pitch < a.width
+  const wide n = -b.width - d;
+  wide k = n / pitch - (n % pitch < 0 ? 1 : 0) + 1;
+  if (k < 1 - a.rows) k = 1 - a.rows;
+  return k < b.rows && d + k * pitch < a.width;
+}
+
+// Whether an output meets an input or another output.
+template <size_t N, size_t I>
+bool any_meet(const Place (&outs)[N], const Place (&ins)[I]) {
+  for (size_t i = 0; i < N; ++i) {
+    for (size_t j = i + 1; j < N; ++j)
+      if (meet(outs[i], outs[j])) return true;
+    for (const Place& in : ins)
+      if (meet(outs[i], in)) return true;
+  }
+  return false;
+}
+
 // Tensors of a list (outs: of the same lengths).
 int list_status(const amp_tensor* a, const amp_tensor* outs, int32_t count) {
   if (count < 0) return AMP_EINVAL;
@@ -532,6 +576,9 @@ int amp_gemm_swiglu(int64_t M, int64_t F, int64_t K, const void* x, int t, int64
   if (M == 0 || F == 0) return AMP_OK;
   if ((K > 0 && (!x || !w)) || (!y && !gu) || !al(x, 2) || !al(w, 2) || !al(y, 2) || !al(gu, 2)) return AMP_EINVAL;
   if (ldx < K || ldw < K || (y && ldy < F) || (gu && ldgu < 2 * F)) return AMP_EINVAL;
+  const Place ins[] = {place_of(x, M, K, ldx, t), place_of(w, 2 * F, K, ldw, t)};
+  const Place outs[] = {place_of(y, M, F, ldy, t), place_of(gu, M, 2 * F, ldgu, t)};
+  if (any_meet(outs, ins)) return AMP_EINVAL;
   if (int e = check_device()) return e;
   return hip_status(amp::launch_gemm_swiglu(M, F, K, x, t, ldx, w, ldw, y, ldy, gu, ldgu, static_cast<hipStream_t>(stream)));
 }
@@ -553,6 +600,11 @@ int amp_gemm_swiglu_backward(int64_t M, int64_t F, int64_t K, const void* dy, in
   }
   if ((dx && lddx < K) || (dw && lddw < K)) return AMP_EINVAL;
   if ((M == 0 || F == 0) && (!dx || M == 0) && (!dw || F == 0)) return AMP_OK;
+  const Place ins[] = {place_of(dy, M, F, lddy, t), place_of(!gu || dw ? x : nullptr, M, K, ldx, t),
+                       place_of(!gu || dx ? w : nullptr, 2 * F, K, ldw, t), place_of(gu == dgu ? nullptr : gu, M, 2 * F, ldgu, t)};
+  const Place outs[] = {place_of(dgu, M, 2 * F, lddgu, t), place_of(y, M, F, ldy, t), place_of(dx, M, K, lddx, t),
+                        place_of(dw, 2 * F, K, lddw, dwt), place_of(d_work, 1, AMP_GEMM_SWIGLU_WORK, AMP_GEMM_SWIGLU_WORK, AMP_F32)};
+  if (any_meet(outs, ins)) return AMP_EINVAL;
   if (int e = check_device()) return e;
   return hip_status(amp::launch_gemm_swiglu_backward(M, F, K, dy, t, lddy, x, ldx, w, ldw, gu, ldgu, dgu, lddgu, y, ldy, dx, lddx,
                                                      dw, dwt, lddw, d_work, static_cast<hipStream_t>(stream)));
