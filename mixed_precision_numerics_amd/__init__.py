@@ -130,8 +130,11 @@ class TensorList:
                 raise ValueError(f"TensorList: tensor {i} is of type {dtype}")
             _room("TensorList", f"tensor {i}", t, _vec(n, dtype))
             if n > 0 and hasattr(t, "stride") and not t.is_contiguous():
-                if 1 + sum((size - 1) * step for size, step in zip(t.shape, t.stride())) != t.numel():
-                    raise ValueError(f"TensorList: tensor {i}'s elements are not one after another")
+                step = 1                                      # each dimension steps over those below it, in some order
+                for s, size in sorted((s, size) for size, s in zip(t.shape, t.stride()) if size > 1):
+                    if s != step:
+                        raise ValueError(f"TensorList: tensor {i}'s elements are not one after another")
+                    step *= size
             a = self.array[i]
             a.p, a.n, a.type = _ptr(t), n, dtype
             if n > 0 and hasattr(t, "get_device"):

@@ -135,3 +135,18 @@ def test_the_library_takes_neighbours(gt, g, n, ot, o):
     arr[1].type = out[1].type = amp.E4M3
     f = amp.load().amp_grad_clip_list
     assert f(amp.ctypes.addressof(arr), amp.ctypes.addressof(out), 2, None, None, None) == -2
+
+
+@pytest.mark.parametrize("shape,stride", [((3, 3), (2, 2)), ((2, 2, 2), (1, 3, 3)), ((4, 2), (0, 7)), ((4, 4), (3, 2)), ((5,), (2,)),
+                                          ((2, 3), (4, 1)), ((6, 2), (1, 1)), ((3, 2), (1, 4))])
+def test_elements_that_leave_gaps_or_lie_twice_are_refused(shape, stride):
+    a = torch.zeros(64)
+    with pytest.raises(ValueError, match="tensor 0's elements are not one after another"):
+        amp.TensorList([(a.as_strided(shape, stride), 2, amp.F32)])
+
+
+@pytest.mark.parametrize("shape,stride", [((3, 3), (1, 3)), ((2, 3, 4), (12, 1, 3)), ((2, 3, 4), (1, 8, 2)), ((1, 4), (77, 1)), ((4, 1, 2), (1, 99, 4)),
+                                          ((1, 1), (5, 5)), ((2, 3, 4), (12, 4, 1)), ((1, 3, 1, 2), (0, 1, 0, 3))])
+def test_elements_one_after_another_in_any_order_are_taken(shape, stride):
+    t = torch.zeros(64).as_strided(shape, stride)
+    assert len(amp.TensorList([(t, t.numel(), amp.F32)])) == 1
