@@ -534,8 +534,9 @@ int amp_requantize_blockwise(const amp_fp8_tiles* x, int64_t rows, int64_t cols,
  * K % 8 == 0) are the fast ones.  No output may overlap an input, another
  * output or the work area, but for dgu and gu as said below (AMP_EINVAL, unless
  * both matrices have gaps between their rows and different strides: those are not
- * compared).  K and F are at most 2^26 and a
- * product may have at most 2^22 tiles of 128 x 128 (else AMP_EUNSUPPORTED). */
+ * compared).  K and F are at most 2^26 and a product that the call forms (of
+ * [M, 2F]; in the backward pass also of [M, K] and [2F, K]) may have at most 2^22
+ * tiles of 128 x 128 (else AMP_EUNSUPPORTED). */
 
 /* amp_gemm_swiglu -- the forward pass.  Of few tokens (one token included) the
  * weights stream past them once.

@@ -72,11 +72,12 @@ int tiles_status(const amp_fp8_tiles* t, int64_t rows, int64_t cols) {
 }
 
 // Sizes of a gated feed-forward block: columns as above, and tiles whose
-// threads one launch can count (both gradients' together).
-bool block_sizes(int64_t M, int64_t F, int64_t K) {
+// threads one launch can count (both gradients' together; the forward call forms
+// the projections alone).
+bool block_sizes(int64_t M, int64_t F, int64_t K, bool gradients) {
   if (K > kMostCols || F > kMostCols || M > (int64_t(1) << 31)) return false;
   const int64_t m = (M + 127) / 128, f = (2 * F + 127) / 128, k = (K + 127) / 128, most = int64_t(1) << 22;
-  return m * (f > k ? f : k) <= most && f * k <= most;
+  return m * f <= most && (!gradients || (m * k <= most && f * k <= most));
 }
 
 // Where a matrix operand lies: `rows` rows of `width` bytes, `pitch` bytes apart.
@@ -572,7 +573,7 @@ int amp_requantize_blockwise(const amp_fp8_tiles* x, int64_t rows, int64_t cols,
 int amp_gemm_swiglu(int64_t M, int64_t F, int64_t K, const void* x, int t, int64_t ldx, const void* w, int64_t ldw, void* y,
                     int64_t ldy, void* gu, int64_t ldgu, void* stream) {
   if (M < 0 || F < 0 || K < 0) return AMP_EINVAL;
-  if ((t != AMP_BF16 && t != AMP_F16) || !block_sizes(M, F, K)) return AMP_EUNSUPPORTED;
+  if ((t != AMP_BF16 && t != AMP_F16) || !block_sizes(M, F, K, false)) return AMP_EUNSUPPORTED;
   if (M == 0 || F == 0) return AMP_OK;
   if ((K > 0 && (!x || !w)) || (!y && !gu) || !al(x, 2) || !al(w, 2) || !al(y, 2) || !al(gu, 2)) return AMP_EINVAL;
   if (ldx < K || ldw < K || (y && ldy < F) || (gu && ldgu < 2 * F)) return AMP_EINVAL;
@@ -587,7 +588,7 @@ int amp_gemm_swiglu_backward(int64_t M, int64_t F, int64_t K, const void* dy, in
                              const void* w, int64_t ldw, const void* gu, int64_t ldgu, void* dgu, int64_t lddgu, void* y,
                              int64_t ldy, void* dx, int64_t lddx, void* dw, int dwt, int64_t lddw, float* d_work, void* stream) {
   if (M < 0 || F < 0 || K < 0) return AMP_EINVAL;
-  if ((t != AMP_BF16 && t != AMP_F16) || (dw && dwt != t && dwt != AMP_F32) || !block_sizes(M, F, K)) return AMP_EUNSUPPORTED;
+  if ((t != AMP_BF16 && t != AMP_F16) || (dw && dwt != t && dwt != AMP_F32) || !block_sizes(M, F, K, true)) return AMP_EUNSUPPORTED;
   if (gu && y) return AMP_EINVAL;
   if (!al(dy, 2) || !al(x, 2) || !al(w, 2) || !al(gu, 2) || !al(dgu, 2) || !al(y, 2) || !al(dx, 2) ||
       !al(dw, dwt == AMP_F32 ? 4 : 2) || !al(d_work, 4))
