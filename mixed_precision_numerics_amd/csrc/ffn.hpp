@@ -32,10 +32,10 @@
 // rows go that way in every step (FAST == false), where loads that are not
 // 16-byte aligned bound them: 1000 x 4097 x 14336 385 us against 190 for 4096.
 #pragma once
-#include <algorithm>
 #include <type_traits>
 
 #include "common.hpp"
+#include "ffn_choice.hpp"
 #include "formats.hpp"
 #include "gate.hpp"
 #include "mfma.hpp"
@@ -202,7 +202,7 @@ __device__ __forceinline__ void to_lds(__amdgpu_buffer_rsrc_t rsrc, uint32_t dst
                "{m0}"(__builtin_amdgcn_readfirstlane(dst)));
 }
 
-constexpr int kStepK = 64, kStepBytes = 2 * kStepK;      // elements and bytes of a row of a step
+constexpr int kStepBytes = 2 * kStepK;                   // bytes of a row of a step
 static_assert(kStepBytes == kRowBytes, "the slots' layout");
 
 // The same in an output-contiguous stage, rows of `pitch` bytes along K.
@@ -659,8 +659,7 @@ struct Piece {
 // 16 and elements 8 (l / 16) .. + 7), and join their sums in LDS.  16 waves a block
 // keep 64 KB of weights a CU in flight: 1 x 4096 x 14336 BF16 43 us = 5.5 TB/s (8
 // waves with 128 elements a turn: 46), 1 x 5120 x 20480 72 us = 5.8 TB/s (81).
-constexpr int kFewWaves = 16, kFewTurn = 64;
-
+//
 // WHOLE: every row is whole 16-byte pieces.
 template <int ET, int OUT, bool WHOLE>
 __global__ __launch_bounds__(kFewWaves * 64) void gate_few(ProductArgs g) {
@@ -770,47 +769,24 @@ inline bool direct_operand(const void* p, int64_t ld, bool kc, int64_t outs) {
   return aligned(p, 16) && ld % 8 == 0 && ld < (int64_t(1) << 30) / (kc ? 256 : 64) && (kc || outs % 8 == 0);
 }
 
-inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline int64_t tiles_of(int64_t M, int64_t cols, int64_t edge) { return ceil_div(M, edge) * ceil_div(cols, edge); }
-
-// Microseconds of a step of 64 along the summed dimension: a tile of 256 x 256
-// has a CU for itself, tiles of 128 x 128 run two to a CU; with fewer than one a
-// CU a step of theirs is bound by latency, less with a longer ring.
-constexpr double kStepLarge = 1.5, kStepSmall = 1.05, kStepAlone = 0.55, kStepFar = 0.4;
-// Of a tile's beginning and end, of the gate and of its gradient.
-constexpr double kGateLarge = 11.0, kGateSmall = 6.0, kGradLarge = 25.0, kGradSmall = 8.0;
-// Of a turn of gate_few's waves, of which two blocks share a CU, and its ends; and
-// the weights' bytes a microsecond.
-constexpr double kTurnFew = 2.0, kBlockFew = 3.0, kStream = 5.0e6;
-
 template <int ET, int OUT>
 hipError_t launch_gate(const ProductArgs& g, hipStream_t s) {
   const bool fast = direct_operand(g.A, g.lda, true, g.M) && direct_operand(g.B, g.ldb, true, g.N);
-  const int64_t big = tiles_of(g.M, 2 * g.N, 256), small = tiles_of(g.M, 2 * g.N, 128), steps = ceil_div(g.K, kStepK);
-  constexpr double kLarge = OUT == kOutGrad ? kGradLarge : kGateLarge, kSmall = OUT == kOutGrad ? kGradSmall : kGateSmall;
-  const double t_large = static_cast<double>(ceil_div(big, 256)) * (kStepLarge * steps + kLarge);
-  const double t_small = small <= 256 ? (fast ? kStepFar : 2 * kStepAlone) * steps + kSmall
-                                      : static_cast<double>(ceil_div(small, 512)) * (kStepSmall * steps + kSmall);
-  const int64_t groups = ceil_div(g.M, 16), few = groups * ceil_div(g.N, 16);
-  const double weights = 4.0 * static_cast<double>(g.N) * static_cast<double>(g.K) / kStream;
-  const double t_few = std::max(static_cast<double>(ceil_div(few, 512)) * (kTurnFew * ceil_div(g.K, kFewWaves * kFewTurn) + kBlockFew),
-                                static_cast<double>(groups) * weights);
-  // (a launch counts fewer than 2^32 threads)
-  if (few < (int64_t(1) << 22) && (groups == 1 || (groups <= 8 && small <= 256 && t_few < std::max(t_small, weights)))) {
-    const dim3 grid(static_cast<unsigned>(ceil_div(g.N, 16)), static_cast<unsigned>(groups));
-    const bool whole = aligned(g.A, 16) && aligned(g.B, 16) && g.lda % 8 == 0 && g.ldb % 8 == 0;
-    if (whole) gate_few<ET, OUT, true><<<grid, kFewWaves * 64, 0, s>>>(g);
-    else gate_few<ET, OUT, false><<<grid, kFewWaves * 64, 0, s>>>(g);
-    return hipGetLastError();
+  const GateForm form = gate_form(g.M, g.N, g.K, fast, OUT == kOutGrad);
+  const dim3 grid(static_cast<unsigned>(tiles_of(g.M, 2 * g.N, form == kLarge ? 256 : 128)));
+  switch (form) {
+    case kFew: {
+      const dim3 groups(static_cast<unsigned>(ceil_div(g.N, 16)), static_cast<unsigned>(ceil_div(g.M, 16)));
+      const bool whole = aligned(g.A, 16) && aligned(g.B, 16) && g.lda % 8 == 0 && g.ldb % 8 == 0;
+      if (whole) gate_few<ET, OUT, true><<<groups, kFewWaves * 64, 0, s>>>(g);
+      else gate_few<ET, OUT, false><<<groups, kFewWaves * 64, 0, s>>>(g);
+      break;
+    }
+    case kLarge: gate_tiles<ET, OUT, 4, 4, 2, true><<<grid, 256, 0, s>>>(g); break;
+    case kRing: gate_tiles<ET, OUT, 2, 2, 4, true><<<grid, 256, 0, s>>>(g); break;
+    case kSmall: gate_tiles<ET, OUT, 2, 2, 2, true><<<grid, 256, 0, s>>>(g); break;
+    case kStaged: gate_tiles<ET, OUT, 2, 2, 2, false><<<grid, 256, 0, s>>>(g); break;
   }
-  const bool large = fast && t_large <= t_small;
-  const dim3 grid(static_cast<unsigned>(large ? big : small));
-  // up to one block a CU a ring of four steps, 144 KB, keeps more of the weights in
-  // flight (65 x 4096 x 14336 BF16 64 -> 52 us)
-  if (large) gate_tiles<ET, OUT, 4, 4, 2, true><<<grid, 256, 0, s>>>(g);
-  else if (fast && small <= 256) gate_tiles<ET, OUT, 2, 2, 4, true><<<grid, 256, 0, s>>>(g);
-  else if (fast) gate_tiles<ET, OUT, 2, 2, 2, true><<<grid, 256, 0, s>>>(g);
-  else gate_tiles<ET, OUT, 2, 2, 2, false><<<grid, 256, 0, s>>>(g);
   return hipGetLastError();
 }
 

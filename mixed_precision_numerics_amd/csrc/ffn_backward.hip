@@ -40,16 +40,6 @@ __global__ __launch_bounds__(256) void join_parts(const float* __restrict__ part
   }
 }
 
-// Parts of a product whose tiles are too few for the machine: about `steps`
-// steps each where that at least halves them, their sums within `room` numbers
-// of the work area.
-inline int parts_of(const ProductArgs& g, int64_t steps, int64_t room) {
-  const int64_t all = ceil_div(g.K, kStepK);
-  int64_t n = all >= 2 * steps ? all / steps : 1;
-  if (g.M * g.N > 0 && n > room / (g.M * g.N)) n = room / (g.M * g.N);
-  return n > 1 ? static_cast<int>(n) : 1;
-}
-
 template <int ET>
 hipError_t join(const ProductArgs& g, const float* part, void* C, int64_t ldc, int ct, hipStream_t s) {
   const int64_t blocks = ceil_div(g.M * g.N, 256);
@@ -68,31 +58,19 @@ hipError_t gradients(ProductArgs gx, ProductArgs gw, int ct, float* work, hipStr
   if (!dw) gw.M = gw.N = 0;
   const bool fast = (!dx || (direct_operand(gx.A, gx.lda, true, gx.M) && direct_operand(gx.B, gx.ldb, false, gx.N))) &&
                     (!dw || (direct_operand(gw.A, gw.lda, false, gw.M) && direct_operand(gw.B, gw.ldb, false, gw.N)));
-  const int64_t sx = ceil_div(gx.K, kStepK), sw = ceil_div(gw.K, kStepK);
-  const int64_t tx = tiles_of(gx.M, gx.N, 128), tw = tiles_of(gw.M, gw.N, 128);
-  const int64_t bx = tiles_of(gx.M, gx.N, 256), bw = tiles_of(gw.M, gw.N, 256);
-  // 128 x 128 tiles, in parts that share the work out to two blocks a CU
-  const int64_t even = (tx * sx + tw * sw) / 512;
-  const int64_t each = even < 8 ? 8 : even;
-  const int64_t room = work ? AMP_GEMM_SWIGLU_WORK : 0;
-  gx.splits = dx ? parts_of(gx, each, room) : 1;
-  gw.splits = dw ? parts_of(gw, each, room - (gx.splits > 1 ? gx.splits * gx.M * gx.N : 0)) : 1;
-  auto most = [](double a, double b) { return a > b ? a : b; };
-  const double longest = most(dx ? static_cast<double>(sx) / gx.splits : 0, dw ? static_cast<double>(sw) / gw.splits : 0);
-  const double small = most(kStepSmall * static_cast<double>(tx * sx + tw * sw) / 512, kStepAlone * longest);
-  const double large = kStepLarge * most(static_cast<double>(bx * sx + bw * sw) / 256, most(dx ? sx : 0, dw ? sw : 0));
-  const bool wide = fast && large <= small;
-  if (wide) gx.splits = gw.splits = 1;
+  const GradientForm f = gradient_form(gx.M, gx.N, gx.K, gw.M, gw.N, gw.K, fast, work ? AMP_GEMM_SWIGLU_WORK : 0);
+  gx.splits = f.split_x;
+  gw.splits = f.split_w;
   const ProductArgs x0 = gx, w0 = gw;      // where the results go
   gx.out32 = gx.splits > 1;
   if (gx.splits > 1) { gx.C = work; gx.ldc = gx.N; }
   gw.out32 = gw.splits > 1 || ct == AMP_F32;
   if (gw.splits > 1) { gw.C = work + (gx.splits > 1 ? gx.splits * gx.M * gx.N : 0); gw.ldc = gw.N; }
-  const uint32_t nx = static_cast<uint32_t>((wide ? bx : tx) * gx.splits), nw = static_cast<uint32_t>((wide ? bw : tw) * gw.splits);
-  const int dx_first = sx * gw.splits >= sw * gx.splits;
-  if (wide) gradient_tiles<ET, 4, 4, true><<<nx + nw, 256, 0, s>>>(gx, gw, nx, nw, dx_first);
-  else if (fast) gradient_tiles<ET, 2, 2, true><<<nx + nw, 256, 0, s>>>(gx, gw, nx, nw, dx_first);
-  else gradient_tiles<ET, 2, 2, false><<<nx + nw, 256, 0, s>>>(gx, gw, nx, nw, dx_first);
+  const int64_t edge = f.wide ? 256 : 128;
+  const uint32_t nx = static_cast<uint32_t>(tiles_of(gx.M, gx.N, edge) * gx.splits), nw = static_cast<uint32_t>(tiles_of(gw.M, gw.N, edge) * gw.splits);
+  if (f.wide) gradient_tiles<ET, 4, 4, true><<<nx + nw, 256, 0, s>>>(gx, gw, nx, nw, f.dx_first);
+  else if (fast) gradient_tiles<ET, 2, 2, true><<<nx + nw, 256, 0, s>>>(gx, gw, nx, nw, f.dx_first);
+  else gradient_tiles<ET, 2, 2, false><<<nx + nw, 256, 0, s>>>(gx, gw, nx, nw, f.dx_first);
   if (hipError_t e = hipGetLastError()) return e;
   if (gx.splits > 1)
     if (hipError_t e = join<ET>(gx, static_cast<const float*>(gx.C), x0.C, x0.ldc, ET, s)) return e;
