@@ -12,6 +12,7 @@ library is missing or no gfx950 device is current, the calls raise.
 """
 from __future__ import annotations
 
+import array
 import bisect
 import ctypes
 import importlib.util
@@ -145,6 +146,7 @@ class TensorList:
                     raise ValueError(f"TensorList: tensor {i} is on {t.device}, others are not")
         self.places = [t.data_ptr() for t in self.tensors]
         self.bytes = [_vec(n, dtype) for t, n, dtype in entries if n > 0 and hasattr(t, "get_device")]
+        self.held = array.array("q", [v for pair in zip(self.places, self.bytes) for v in pair])      # both, for _quick
         spans = sorted((a.p, a.p + _vec(a.n, a.type)) for a in self.array if a.n > 0 and a.p)
         self.apart = all(one[1] <= two[0] for one, two in zip(spans, spans[1:]))     # may be written to
         self.serial, self.beside = next(TensorList._serials), set()    # beside: serials of lists known to be clear of this one

@@ -23,7 +23,7 @@ namespace {
 PyTypeObject* g_tensor;   // torch.Tensor
 PyTypeObject* g_tiles;    // Fp8Tiles
 PyTypeObject* g_list;     // TensorList
-PyObject *g_get_device, *g_nbytes, *g_is_contiguous, *g_data_ptr, *g_tensors, *g_array, *g_places, *g_bytes, *g_where, *g_apart, *g_serial, *g_beside;
+PyObject *g_get_device, *g_nbytes, *g_is_contiguous, *g_data_ptr, *g_tensors, *g_array, *g_held, *g_where, *g_apart, *g_serial, *g_beside;
 PyObject* g_where_is;      // torch.Tensor.data_ptr
 
 typedef __int128 wide;
@@ -171,38 +171,38 @@ struct Args {
     PyObject* o = v[i];
     count = 0;
     if (!ok || o == Py_None) return nullptr;
-    PyObject *a = nullptr, *ts = nullptr, *at = nullptr, *bs = nullptr;
-    Py_buffer b{};
+    PyObject *a = nullptr, *ts = nullptr, *held = nullptr;
+    Py_buffer b{}, h{};
     if (!PyObject_TypeCheck(o, g_list) || !(a = PyObject_GetAttr(o, g_array)) || !(ts = PyObject_GetAttr(o, g_tensors)) ||
-        !(at = PyObject_GetAttr(o, g_places)) || !(bs = PyObject_GetAttr(o, g_bytes)) || !PyList_Check(ts) || !PyList_Check(at) ||
-        !PyList_Check(bs) || PyList_GET_SIZE(ts) != PyList_GET_SIZE(at) || PyList_GET_SIZE(ts) != PyList_GET_SIZE(bs) ||
-        PyObject_GetBuffer(a, &b, PyBUF_SIMPLE) != 0)
+        !(held = PyObject_GetAttr(o, g_held)) || !PyList_Check(ts) || PyObject_GetBuffer(a, &b, PyBUF_SIMPLE) != 0 ||
+        PyObject_GetBuffer(held, &h, PyBUF_SIMPLE) != 0 || h.len != 16 * PyList_GET_SIZE(ts))
       ok = false;
+    const int64_t* was = static_cast<const int64_t*>(h.buf);      // address and bytes of each tensor
     const amp_tensor* p = ok ? static_cast<const amp_tensor*>(b.buf) : nullptr;
     if (ok) count = static_cast<int32_t>(b.len / static_cast<Py_ssize_t>(sizeof(amp_tensor)));
     if (ok && PyList_GET_SIZE(ts) > 0) ok = ask(o, g_where, false) == dev && ok;
-    for (Py_ssize_t k = 0; ok && k < PyList_GET_SIZE(ts); ++k) {
+    for (Py_ssize_t k = 0; ok && k < PyList_GET_SIZE(ts); ++k, was += 2) {
       PyObject* t = PyList_GET_ITEM(ts, k);
       uint64_t p;
       wide bytes;
       if (!PyObject_TypeCheck(t, g_tensor)) {
         ok = false;
       } else if (place(t, p, bytes)) {
-        ok = static_cast<int64_t>(p) == num(PyList_GET_ITEM(at, k)) && bytes >= num(PyList_GET_ITEM(bs, k)) && ok;
-      } else if (ask(t, g_nbytes, false) < num(PyList_GET_ITEM(bs, k))) {
+        ok = static_cast<int64_t>(p) == was[0] && bytes >= was[1];
+      } else if (ask(t, g_nbytes, false) < was[1]) {
         ok = false;
       } else {
         PyObject* r = PyObject_Vectorcall(g_where_is, &t, 1, nullptr);
-        ok = r && num(r) == num(PyList_GET_ITEM(at, k)) && ok;
+        ok = r && num(r) == was[0] && ok;
         Py_XDECREF(r);
       }
     }
     PyErr_Clear();
     if (b.obj) PyBuffer_Release(&b);
+    if (h.obj) PyBuffer_Release(&h);
     Py_XDECREF(a);                     // the list keeps its array
     Py_XDECREF(ts);
-    Py_XDECREF(at);
-    Py_XDECREF(bs);
+    Py_XDECREF(held);
     return ok ? p : nullptr;
   }
   // Whether the lists are known to lie clear of each other (TensorList.clear_of).
@@ -405,8 +405,7 @@ PyMODINIT_FUNC PyInit__quick(void) {
   g_data_ptr = PyUnicode_InternFromString("data_ptr");
   g_tensors = PyUnicode_InternFromString("tensors");
   g_array = PyUnicode_InternFromString("array");
-  g_places = PyUnicode_InternFromString("places");
-  g_bytes = PyUnicode_InternFromString("bytes");
+  g_held = PyUnicode_InternFromString("held");
   g_where = PyUnicode_InternFromString("where");
   g_apart = PyUnicode_InternFromString("apart");
   g_serial = PyUnicode_InternFromString("serial");
