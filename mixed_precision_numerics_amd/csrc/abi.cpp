@@ -601,8 +601,9 @@ int amp_gemm_swiglu_backward(int64_t M, int64_t F, int64_t K, const void* dy, in
   }
   if ((dx && lddx < K) || (dw && lddw < K)) return AMP_EINVAL;
   if ((M == 0 || F == 0) && (!dx || M == 0) && (!dw || F == 0)) return AMP_OK;
-  const Place ins[] = {place_of(dy, M, F, lddy, t), place_of(!gu || dw ? x : nullptr, M, K, ldx, t),
-                       place_of(!gu || dx ? w : nullptr, 2 * F, K, ldw, t), place_of(gu == dgu ? nullptr : gu, M, 2 * F, ldgu, t)};
+  const bool reads = M > 0 && F > 0;      // (else nothing is known of the inputs' strides)
+  const Place ins[] = {place_of(reads ? dy : nullptr, M, F, lddy, t), place_of(reads && (!gu || dw) ? x : nullptr, M, K, ldx, t),
+                       place_of(reads && (!gu || dx) ? w : nullptr, 2 * F, K, ldw, t), place_of(reads && gu != dgu ? gu : nullptr, M, 2 * F, ldgu, t)};
   const Place outs[] = {place_of(dgu, M, 2 * F, lddgu, t), place_of(y, M, F, ldy, t), place_of(dx, M, K, lddx, t),
                         place_of(dw, 2 * F, K, lddw, dwt), place_of(d_work, 1, AMP_GEMM_SWIGLU_WORK, AMP_GEMM_SWIGLU_WORK, AMP_F32)};
   if (any_meet(outs, ins)) return AMP_EINVAL;

@@ -132,3 +132,16 @@ def test_different_pitches_with_gaps_are_not_compared():
     assert taken(call(FORWARD, at, x=K + 100, y=F + 60))
     # ... but a single row has none
     assert amp.load().amp_gemm_swiglu(1, F, K, at["x"], amp.BF16, K + 100, at["w"], K, at["x"] + 2 * K - 2, F + 60, None, 0, None) == EINVAL
+
+
+@pytest.mark.parametrize("tokens,features", [(0, F), (M, 0)])
+@pytest.mark.parametrize("pad", [0, 8])
+def test_inputs_of_a_call_that_reads_none_may_be_anything(tokens, features, pad):
+    """Without tokens dw is zeros, without features dx is: inputs with no stride, over the outputs, are not looked at."""
+    for ld in (0, 1, K):
+        for off in (0, 2, 100):
+            at = 1 << 28
+            st = amp.load().amp_gemm_swiglu_backward(tokens, features, K, at + off, amp.BF16, ld, at + off, ld, at + off, ld, None, 0, at + off, ld,
+                                                     None, 0, at if features == 0 else None, K + pad, at if tokens == 0 else None, amp.F32, K + pad,
+                                                     None, None)
+            assert taken(st)
