@@ -125,11 +125,13 @@ class TensorList:
     def __init__(self, entries):
         entries = list(entries)
         self.array = (_Tensor * len(entries))()
-        self.tensors, self.where = [], None
+        self.tensors, self.places, self.bytes, self.where = [], [], [], None
+        spans = []
         for i, (t, n, dtype) in enumerate(entries):
             if dtype not in (F32, F16, BF16):
                 raise ValueError(f"TensorList: tensor {i} is of type {dtype}")
-            _room("TensorList", f"tensor {i}", t, _vec(n, dtype))
+            need = _vec(n, dtype)
+            _room("TensorList", f"tensor {i}", t, need)
             if n > 0 and hasattr(t, "stride") and not t.is_contiguous():
                 step = 1                                      # each dimension steps over those below it, in some order
                 for s, size in sorted((s, size) for size, s in zip(t.shape, t.stride()) if size > 1):
@@ -137,17 +139,23 @@ class TensorList:
                         raise ValueError(f"TensorList: tensor {i}'s elements are not one after another")
                     step *= size
             a = self.array[i]
-            a.p, a.n, a.type = _ptr(t), n, dtype
-            if n > 0 and hasattr(t, "get_device"):
+            p = _ptr(t)
+            a.p, a.n, a.type = p, n, dtype
+            if n <= 0:
+                continue
+            if p:
+                spans.append((p, p + need))
+            if hasattr(t, "get_device"):
                 self.tensors.append(t)
+                self.places.append(p)
+                self.bytes.append(need)
+                where = t.get_device()
                 if self.where is None:
-                    self.where = t.get_device()
-                elif self.where != t.get_device():
+                    self.where = where
+                elif self.where != where:
                     raise ValueError(f"TensorList: tensor {i} is on {t.device}, others are not")
-        self.places = [t.data_ptr() for t in self.tensors]
-        self.bytes = [_vec(n, dtype) for t, n, dtype in entries if n > 0 and hasattr(t, "get_device")]
         self.held = array.array("q", [v for pair in zip(self.places, self.bytes) for v in pair])      # both, for _quick
-        spans = sorted((a.p, a.p + _vec(a.n, a.type)) for a in self.array if a.n > 0 and a.p)
+        spans.sort()
         self.apart = all(one[1] <= two[0] for one, two in zip(spans, spans[1:]))     # may be written to
         self.serial, self.beside = next(TensorList._serials), set()    # beside: serials of lists known to be clear of this one
 
