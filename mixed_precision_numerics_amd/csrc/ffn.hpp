@@ -30,7 +30,7 @@
 // registers, masked with zeros on both sides (a NaN behind a row's end must
 // not meet a zero), as the first step of a tile.  Operands without 16-byte
 // rows go that way in every step (FAST == false), where loads that are not
-// 16-byte aligned bound them: 1000 x 4097 x 14336 385 us against 190 for 4096.
+// 16-byte aligned bound them: 1000 x 4097 x 14336 390 us against 190 to 200 for 4096.
 #pragma once
 #include <type_traits>
 
@@ -316,7 +316,7 @@ __device__ __forceinline__ void product(const ProductArgs& g, uint32_t block, ui
   // ---- the same through registers, masked.  Where every step has incomplete pieces
   // (outputs contiguous), one is loaded as the last whole piece of its row and put
   // right on its way into LDS: branches would have the loads wait for one another
-  // (gradients of 300 x 2047 x 1001 BF16 38 us, so 35).  Rows of fewer than eight
+  // (the backward call of 300 x 1001 x 2047 BF16 38 us, so 35).  Rows of fewer than eight
   // elements have no whole piece.
   u32x4 ha[kLA], hb[kLB];
   const bool short_a = !A_KC && g.M < 8, short_b = !B_KC && g.N < 8;
@@ -636,7 +636,8 @@ __device__ __forceinline__ f32x4 mfma16x16(u32x4 a, u32x4 b, f32x4 c) {
 // Eight elements at any 2-byte address from the dwords that hold them, shifted into
 // place (each dword read holds one of the elements: none lies outside the
 // operand's pages).  Waves that only stream would wait for 16-byte loads at odd
-// addresses: 1 x 4097 x 14336 106 us, so 64 (57 since ld16_part's loads overlap).
+// addresses: 1 x 4097 x 14336 106 us, so 64 (56 since ld16_part's loads overlap; 73
+// with weights that no cache holds).
 typedef uint32_t u32x4_dw __attribute__((ext_vector_type(4), aligned(4)));
 struct Piece {
   u32x4 w;
@@ -735,7 +736,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void gate_few(ProductArgs g) {
   }
 }
 
-// Both projections with their gate.  1000 x 4096 x 14336 BF16 188 us (1.25 PFLOP/s),
+// Both projections with their gate.  1000 x 4096 x 14336 BF16 188 to 200 us (1.18 to 1.25 PFLOP/s),
 // 33 x 5120 x 20480 92 us (4.6 TB/s of weights; 320 tiles of 128 x 128).
 template <int ET, int OUT, int MB, int NB, int D, bool FAST>
 __global__ __launch_bounds__(256, MB * NB > 8 || D > 2 ? 1 : 2) void gate_tiles(ProductArgs g) {

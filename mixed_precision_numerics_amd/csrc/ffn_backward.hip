@@ -7,6 +7,12 @@
 // pass of amp_swiglu_backward) or out of the epilogue of the product that forms
 // them again.  The two gradient products on it are one launch.
 //
+// dg and du are rounded to the operands' 16 bits before the two products: they
+// are what the matrix cores multiply, and a second part for what the rounding
+// leaves would double the products.  That rounding is all that sets dx and dw apart
+// from products of FP32 gradients: relative to those 2.6e-3 in BF16 and 3.2e-4 in
+// F16 over whole outputs, and 1e-4 and 2e-5 relative to products of the rounded ones.
+//
 // Bound by the matrix cores: 8192 x 4096 x 14336 BF16 from kept projections 3.05 ms,
 // of which the element-wise pass is 0.18 and the products run at 1.35 PFLOP/s;
 // 4000 x 5120 x 10240 with them formed again 2.0 ms, 0.68 of it for forming them.

@@ -6,7 +6,7 @@
 // HBM-bound: the norm of 0.87 G BF16 elements 293 us (5.95 TB/s), their clipping into
 // FP32 1.01 ms (5.2 TB/s); lists of small tensors are bound by launches and by the
 // host: the norm of a small net's four tensors 10.6 us, clipping 700 of 2000 elements
-// on average 67 us (27 from C).  The list's tensors are cut into chunks, none across
+// on average 60 us (27 from C).  The list's tensors are cut into chunks, none across
 // two tensors, and the chunks dealt out evenly to the blocks in one contiguous run
 // each, whatever the tensors' lengths.  The tables travel as kernel arguments:
 // nothing is allocated or copied, and a captured graph holds them.
